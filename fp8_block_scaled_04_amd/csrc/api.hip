@@ -7,22 +7,19 @@
 
 #include <hip/hip_runtime.h>
 
+#include "abi_common.h"
 #include "fp8bs.h"
 #include "launch.h"
 #include "splitk.h"
 
 namespace {
 
-using fp8bs::GemmProblem;
-
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_device_state[kMaxDevices];  // 0 unknown, 1 gfx950, 2 other
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace
 
-// The current device must be a gfx950 (MI355X / MI350X).  The answer is
-// cached per device ordinal; hipGetDevice itself fails when no GPU exists.
-fp8bs_status check_device() {
+fp8bs_status fp8bs::check_device() {
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0) return FP8BS_ERR_DEVICE;
   if (dev >= kMaxDevices) return FP8BS_ERR_DEVICE;
@@ -36,7 +33,12 @@ fp8bs_status check_device() {
   return st == 1 ? FP8BS_OK : FP8BS_ERR_DEVICE;
 }
 
-fp8bs_status launched(hipError_t e) { return e == hipSuccess ? FP8BS_OK : FP8BS_ERR_LAUNCH; }
+namespace {
+
+using fp8bs::aligned16;
+using fp8bs::check_device;
+using fp8bs::GemmProblem;
+using fp8bs::launched;
 
 constexpr int64_t kMaxGridY = 65535;
 constexpr int64_t kMaxGridX = 0x7FFFFFFF;

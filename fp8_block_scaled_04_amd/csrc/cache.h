@@ -1,0 +1,89 @@
+// Internal interface of the paged FP8 key/value cache kernels: launch
+// arguments (host and device) and the launchers.  Arguments are checked by the
+// C ABI layer; formats and rules are in include/fp8bs_cache.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fp8bs {
+
+// The cache and the sequences of one call, as the kernels take it.
+struct CacheArgs {
+  uint8_t* k;
+  float* ks;
+  uint8_t* v;
+  float* vs;
+  const int32_t* table;
+  const int32_t* kv_lens;
+  const int32_t* q_offsets;  // nullptr for the eviction
+  int64_t pages;
+  int64_t rows;              // packed rows of the call
+  int32_t batch, width, heads;
+  int32_t lg_page;           // P = 1 << lg_page
+  int32_t dim;               // D
+  int32_t max_new, max_kv;
+};
+
+struct AppendArgs {
+  CacheArgs c;
+  const void* k_new;
+  const void* v_new;
+  int64_t ld_new;
+};
+
+struct AttendArgs {
+  CacheArgs c;
+  const void* q;
+  int64_t ld_q;
+  int32_t q_heads, group;    // group = q_heads / heads
+  float scale, softcap;
+  void* out;
+  float* lse;                // may be nullptr
+  bool out_f32, full;
+  int32_t chunk, splits;     // cached tokens per split, splits
+  float* part;               // [splits][rows][q_heads][D] when splits > 1
+  float2* stat;              // [splits][rows][q_heads] (running max, log2 units; sum)
+};
+
+struct WeightArgs {
+  CacheArgs c;
+  const void* q;
+  int64_t ld_q;
+  int32_t q_heads, group;
+  float scale, softcap;
+  const float* lse;
+  const float* acc_in;       // may be nullptr
+  float* acc_out;
+  int64_t acc_slots;
+  bool full;
+};
+
+struct EvictArgs {
+  CacheArgs c;
+  const float* acc;
+  int64_t acc_slots;
+  const int32_t* dst_table;
+  int32_t dst_width, budget, recent;
+  int32_t* kept;
+  int32_t* new_lens;
+  float* acc_out;
+};
+
+// Workgroups of the launches (the ABI layer bounds them below 2^30).
+int64_t append_grid(const CacheArgs& c);
+int64_t evict_move_grid(const EvictArgs& a);
+
+// Sets chunk and splits from the sizes; the workspace is
+// splits * rows * q_heads * (D + 2) floats when splits > 1, else none.
+void attend_plan(AttendArgs& a);
+int64_t attend_workspace_bytes(const AttendArgs& a);
+int64_t attend_grid(const AttendArgs& a);
+int64_t weights_grid(const WeightArgs& a);
+
+hipError_t launch_cache_append(const AppendArgs& a, bool pow2, hipStream_t stream);
+hipError_t launch_cache_attention(const AttendArgs& a, hipStream_t stream);
+hipError_t launch_cache_weights(const WeightArgs& a, hipStream_t stream);
+hipError_t launch_cache_evict(const EvictArgs& a, hipStream_t stream);
+
+}  // namespace fp8bs

@@ -1,0 +1,101 @@
+// Quantized append to the paged FP8 cache (include/fp8bs_cache.h,
+// fp8bs_cache_append).
+//
+// One workgroup per (sequence, touched page, head, K or V): it owns the page's
+// scale and codes of that head, so the largest value, the new scale, the older
+// codes' re-encoding and the new codes need no other workgroup.
+#include "cache_device.h"
+
+namespace fp8bs {
+namespace {
+
+constexpr int kThreads = 256;
+
+__host__ __device__ int pages_touched(int max_new, int lg_page) {
+  return (int)(((int64_t)max_new + (1 << lg_page) - 2) >> lg_page) + 1;  // any alignment of the first slot
+}
+
+template <int D, bool POW2>
+__global__ __launch_bounds__(kThreads) void k_cache_append(AppendArgs a, int blocks) {
+  const CacheArgs& c = a.c;
+  constexpr int kPieces = D / 8;                     // 8-value pieces of a token
+  int id = blockIdx.x;
+  const int h = id % c.heads;
+  id /= c.heads;
+  const bool is_v = id & 1;
+  id >>= 1;
+  const int j = id % blocks, b = id / blocks;
+
+  const Seq s = sequence(c, b);
+  if (s.n == 0) return;
+  const int first = max(s.base, 0);
+  const int end = min(s.base + s.n, s.len);          // new slots [first, end)
+  const int blk = (first >> c.lg_page) + j;
+  const int P = 1 << c.lg_page, start = blk << c.lg_page;
+  const int lo = max(first, start), hi = min(end, start + P);
+  if (lo >= hi) return;
+  const int page = page_of(c, b, lo);
+  if (page < 0) return;
+  const int64_t at = (int64_t)page * c.heads + h;
+  uint8_t* codes = (is_v ? c.v : c.k) + at * ((int64_t)P * D);
+  float* scale = (is_v ? c.vs : c.ks) + at;
+  const uint16_t* src = static_cast<const uint16_t*>(is_v ? a.v_new : a.k_new) +
+                        (int64_t)(s.row0 + (lo - s.base)) * a.ld_new + (int64_t)h * D;
+
+  const int items = (hi - lo) * kPieces;
+  float amax = 0.0f;
+  for (int i = threadIdx.x; i < items; i += kThreads) {
+    const uint4 x = *reinterpret_cast<const uint4*>(src + (int64_t)(i / kPieces) * a.ld_new + (i % kPieces) * 8);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      amax = fmaxf(amax, fmaxf(__builtin_fabsf(bf16_lo(w[e])), __builtin_fabsf(bf16_hi(w[e]))));
+  }
+  __shared__ float red[kThreads / 16];
+  amax = row16_max(amax);
+  if (threadIdx.x % 16 == 0) red[threadIdx.x / 16] = amax;
+  __syncthreads();
+  amax = row16_max(red[threadIdx.x % 16]);
+
+  const float old = lo > start ? *scale : 0.0f;
+  const float now = fmaxf(old, amax > 0.0f ? tile_scale<POW2>(amax).s : 0.0f);
+  const TileScale t = divide_by(now);
+  __syncthreads();                                   // every thread has read the old scale
+  if (threadIdx.x == 0) *scale = now;
+  if (now != old) {                                  // older rows of the page, if any
+    uint32_t* row = reinterpret_cast<uint32_t*>(codes);
+    for (int i = threadIdx.x; i < (lo - start) * (D / 4); i += kThreads) row[i] = reencode4(row[i], old, t);
+  }
+  for (int i = threadIdx.x; i < items; i += kThreads) {
+    const uint4 x = *reinterpret_cast<const uint4*>(src + (int64_t)(i / kPieces) * a.ld_new + (i % kPieces) * 8);
+    uint2 q = {0u, 0u};
+    if (now > 0.0f) {
+      q.x = pack4_e4m3_sat(div_rn(bf16_lo(x.x) * t.sx, t.ss, t.r), div_rn(bf16_hi(x.x) * t.sx, t.ss, t.r),
+                           div_rn(bf16_lo(x.y) * t.sx, t.ss, t.r), div_rn(bf16_hi(x.y) * t.sx, t.ss, t.r));
+      q.y = pack4_e4m3_sat(div_rn(bf16_lo(x.z) * t.sx, t.ss, t.r), div_rn(bf16_hi(x.z) * t.sx, t.ss, t.r),
+                           div_rn(bf16_lo(x.w) * t.sx, t.ss, t.r), div_rn(bf16_hi(x.w) * t.sx, t.ss, t.r));
+    }
+    *reinterpret_cast<uint2*>(codes + (int64_t)(lo - start + i / kPieces) * D + (i % kPieces) * 8) = q;
+  }
+}
+
+}  // namespace
+
+int64_t append_grid(const CacheArgs& c) {
+  return 2 * (int64_t)c.batch * c.heads * pages_touched(c.max_new, c.lg_page);
+}
+
+hipError_t launch_cache_append(const AppendArgs& a, bool pow2, hipStream_t stream) {
+  const dim3 grid((unsigned)append_grid(a.c));
+  const int blocks = pages_touched(a.c.max_new, a.c.lg_page);
+  if (a.c.dim == 128) {
+    if (pow2) k_cache_append<128, true><<<grid, kThreads, 0, stream>>>(a, blocks);
+    else k_cache_append<128, false><<<grid, kThreads, 0, stream>>>(a, blocks);
+  } else {
+    if (pow2) k_cache_append<64, true><<<grid, kThreads, 0, stream>>>(a, blocks);
+    else k_cache_append<64, false><<<grid, kThreads, 0, stream>>>(a, blocks);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace fp8bs

@@ -1,0 +1,302 @@
+// Attention over the paged FP8 cache (include/fp8bs_cache.h,
+// fp8bs_cache_attention).
+//
+// k_attend_rows: one workgroup per (sequence, head, 16 rows, split of the
+// cached tokens).  A row is one (new token, query head of the group) pair, so
+// the group's heads share every key and value read.  Each wave walks its own
+// 32-token steps with a running maximum and sum per row; the four waves meet
+// in LDS at the end, the splits in k_attend_join.
+//
+// Products are formed transposed, S^T = K Q^T and O^T = V^T P^T: the matrix
+// core's result layout of S^T (lane = row, four consecutive tokens per lane)
+// is then its operand layout of P^T, if the 32 tokens of a step are numbered
+// 16 x tile + 4 x lane group + i, and no value moves between lanes.
+#include "cache_device.h"
+
+namespace fp8bs {
+namespace {
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves, kStep = 32;
+constexpr int kMaxSplits = 64;
+
+// cap * tanh(x / cap), as cap * (1 - 2 / (e^(2x/cap) + 1)).
+__device__ __forceinline__ float capped(float x, float cap) {
+  const float e = __builtin_amdgcn_exp2f(x * (2.0f * kLog2e / cap));
+  return cap * (1.0f - 2.0f / (e + 1.0f));
+}
+
+// Bytes of four tokens (a0..a3: the same four dims each) -> per dim the four
+// tokens' bytes.
+__device__ __forceinline__ void transpose4(const uint32_t a[4], uint32_t o[4]) {
+  const uint32_t l0 = __builtin_amdgcn_perm(a[1], a[0], 0x05010400u), h0 = __builtin_amdgcn_perm(a[1], a[0], 0x07030602u);
+  const uint32_t l1 = __builtin_amdgcn_perm(a[3], a[2], 0x05010400u), h1 = __builtin_amdgcn_perm(a[3], a[2], 0x07030602u);
+  o[0] = __builtin_amdgcn_perm(l1, l0, 0x05040100u);
+  o[1] = __builtin_amdgcn_perm(l1, l0, 0x07060302u);
+  o[2] = __builtin_amdgcn_perm(h1, h0, 0x05040100u);
+  o[3] = __builtin_amdgcn_perm(h1, h0, 0x07060302u);
+}
+
+template <int D, bool CAP>
+__global__ __launch_bounds__(kThreads) void k_attend_rows(AttendArgs a, int row_tiles) {
+  const CacheArgs& c = a.c;
+  constexpr int DT = D / 16;                         // dims per lane of V, output tiles
+  constexpr int KS = D / 32;                         // matrix steps of a score
+  int id = blockIdx.x;
+  const int rt = id % row_tiles;
+  id /= row_tiles;
+  const int split = id % a.splits;
+  id /= a.splits;
+  const int h = id % c.heads, b = id / c.heads;
+
+  const Seq s = sequence(c, b);
+  const int rows = s.n * a.group, row0 = rt * 16;
+  if (row0 >= rows) return;
+  const int begin = split * a.chunk;
+  if (split > 0 && begin >= s.len) return;           // the join knows this from the length
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, r = lane & 15;
+  const int last_row = min(row0 + 15, rows - 1);
+  const int seen_all = a.full ? s.len : min(s.len, s.base + last_row / a.group + 1);
+  const int end = min(begin + a.chunk, seen_all);
+
+  // this lane's row (clamped: rows past the end repeat the last one and are
+  // not written)
+  const int row = min(row0 + r, rows - 1);
+  const int tok = row / a.group, hq = h * a.group + row % a.group;
+  const int seen = a.full ? s.len : min(s.len, s.base + tok + 1);
+
+  v8bf qf[KS];
+  {
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)(s.row0 + tok) * a.ld_q + (int64_t)hq * D + g * (D / 4);
+#pragma unroll
+    for (int k = 0; k < KS; ++k) qf[k] = *reinterpret_cast<const v8bf*>(q + 8 * k);
+  }
+
+  v4f o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) o[d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  float m = -INFINITY, l = 0.0f;
+  const int64_t page_bytes = ((int64_t)D) << c.lg_page;
+  const int mask = (1 << c.lg_page) - 1;
+
+  for (int t = begin + wave * kStep; t < end; t += kWaves * kStep) {
+    v4f x[2];
+    float vscale[2];
+    uint32_t vraw[2][4][DT / 4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int tt = t + 16 * i;
+      // a tile past the end reads the last cached token's page, and is masked
+      int page = page_of(c, b, min(tt, s.len - 1));
+      const bool there = page >= 0;
+      page = max(page, 0);
+      const int64_t at = (int64_t)page * c.heads + h;
+      const float f = c.ks[at] * a.scale;
+      vscale[i] = c.vs[at];
+      const uint8_t* kp = c.k + at * page_bytes + (int64_t)((tt & mask) + r) * D + g * (D / 4);
+      v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const uint2 w = *reinterpret_cast<const uint2*>(kp + 8 * k);
+        v8bf kf;
+        unpack4(kf, 0, w.x);
+        unpack4(kf, 4, w.y);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[k], acc, 0, 0, 0);
+      }
+      const uint8_t* vp = c.v + at * page_bytes + (int64_t)((tt & mask) + 4 * g) * D + r * DT;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(vp + j * D);
+        const bool in = there && tt + 4 * g + j < s.len;   // rows past the cached tokens hold anything
+#pragma unroll
+        for (int e = 0; e < DT / 4; ++e) vraw[i][j][e] = in ? p[e] : 0u;
+        float y = acc[j] * f;
+        if (CAP) y = capped(y, a.softcap);
+        x[i][j] = (there && tt + 4 * g + j < min(seen, end)) ? y * kLog2e : -INFINITY;
+      }
+    }
+    float top = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
+                      fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float m2 = fmaxf(m, top);
+    const float ref = m2 == -INFINITY ? 0.0f : m2;   // nothing seen yet: every weight is 0
+    const float alpha = __builtin_amdgcn_exp2f(m - ref);
+    m = m2;
+    l *= alpha;
+    v8bf pf;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = __builtin_amdgcn_exp2f(x[i][j] - ref);
+        l += p;
+        // the weight meets the codes in BF16: its rounding (2^-9) is that of
+        // the output
+        pf[4 * i + j] = (__bf16)(p == 0.0f ? 0.0f : p * vscale[i]);
+      }
+#pragma unroll
+    for (int e = 0; e < DT / 4; ++e) {
+      uint32_t w[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t in[4] = {vraw[i][0][e], vraw[i][1][e], vraw[i][2][e], vraw[i][3][e]};
+        transpose4(in, w[i]);
+      }
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        v8bf vf;
+        unpack4(vf, 0, w[0][d]);
+        unpack4(vf, 4, w[1][d]);
+        v4f& acc = o[4 * e + d];
+        acc *= alpha;
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf, acc, 0, 0, 0);
+      }
+    }
+  }
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+
+  // the waves' maxima, sums and outputs meet in LDS; o[d][j] is dim
+  // DT (4 g + j) + d of row r
+  constexpr int kPitch = D + 4;
+  __shared__ float s_o[kWaves][16][kPitch];
+  __shared__ float2 s_ml[kWaves][16];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int d = 0; d < DT; d += 4)
+      *reinterpret_cast<v4f*>(&s_o[wave][r][DT * (4 * g + j) + d]) = v4f{o[d][j], o[d + 1][j], o[d + 2][j], o[d + 3][j]};
+  if (g == 0) s_ml[wave][r] = make_float2(m, l);
+  __syncthreads();
+
+  const int orow = tid / 16, d0 = (tid % 16) * DT;   // 16 threads per row, DT dims each
+  if (row0 + orow >= rows) return;
+  float top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_ml[w][orow].x);
+  const float ref = top == -INFINITY ? 0.0f : top;
+  float total = 0.0f, y[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) y[d] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    const float f = __builtin_amdgcn_exp2f(s_ml[w][orow].x - ref);
+    total += f * s_ml[w][orow].y;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) y[d] += f * s_o[w][orow][d0 + d];
+  }
+  const int otok = (row0 + orow) / a.group, ohq = h * a.group + (row0 + orow) % a.group;
+  const int64_t at = (int64_t)(s.row0 + otok) * a.q_heads + ohq;
+  if (a.splits > 1) {
+    float* part = a.part + ((int64_t)split * c.rows * a.q_heads + at) * D + d0;
+#pragma unroll
+    for (int d = 0; d < DT; d += 4) *reinterpret_cast<v4f*>(part + d) = v4f{y[d], y[d + 1], y[d + 2], y[d + 3]};
+    if (d0 == 0) a.stat[(int64_t)split * c.rows * a.q_heads + at] = make_float2(top, total);
+    return;
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  if (a.out_f32) {
+    float* out = static_cast<float*>(a.out) + at * D + d0;
+#pragma unroll
+    for (int d = 0; d < DT; d += 4)
+      *reinterpret_cast<v4f*>(out + d) = v4f{y[d] * inv, y[d + 1] * inv, y[d + 2] * inv, y[d + 3] * inv};
+  } else {
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at * D + d0);
+#pragma unroll
+    for (int d = 0; d < DT; d += 2) out[d / 2] = pack2_bf16(y[d] * inv, y[d + 1] * inv);
+  }
+  if (a.lse && d0 == 0) a.lse[at] = total == 0.0f ? -INFINITY : (top + __builtin_log2f(total)) * kLn2;
+}
+
+// Joins the splits of one (row, query head) per wave.
+template <int D>
+__global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a) {
+  const CacheArgs& c = a.c;
+  const int64_t id = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  const int hq = (int)(id % a.q_heads);
+  const int64_t rest = id / a.q_heads;
+  const int tok = (int)(rest % c.max_new), b = (int)(rest / c.max_new);
+  if (b >= c.batch) return;
+  const Seq s = sequence(c, b);
+  if (tok >= s.n) return;
+  const int parts = max(1, min(a.splits, (s.len + a.chunk - 1) / a.chunk));
+  const int64_t at = (int64_t)(s.row0 + tok) * a.q_heads + hq, stride = c.rows * a.q_heads;
+
+  float m = -INFINITY, l = 0.0f;                     // lane: one split (at most 64)
+  if (lane < parts) {
+    const float2 st = a.stat[lane * stride + at];
+    m = st.x;
+    l = st.y;
+  }
+  float top = m;
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
+  const float f = __builtin_amdgcn_exp2f(m - (top == -INFINITY ? 0.0f : top));
+  float total = l * f;
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) total += __shfl_xor(total, x);
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+
+  constexpr int E = D / 64;
+  float y[E] = {};
+  for (int p = 0; p < parts; ++p) {
+    const float w = __shfl(f, p);
+    const float* part = a.part + (p * stride + at) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] += w * part[e];
+  }
+  if (a.out_f32) {
+    float* out = static_cast<float*>(a.out) + at * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] = y[e] * inv;
+  } else {
+    __bf16* out = static_cast<__bf16*>(a.out) + at * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] = (__bf16)(y[e] * inv);
+  }
+  if (a.lse && lane == 0) a.lse[at] = total == 0.0f ? -INFINITY : (top + __builtin_log2f(total)) * kLn2;
+}
+
+int row_tiles(const AttendArgs& a) { return (int)(((int64_t)a.c.max_new * a.group + 15) / 16); }
+
+template <int D>
+hipError_t launch(const AttendArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)attend_grid(a));
+  if (a.softcap > 0.0f) k_attend_rows<D, true><<<grid, kThreads, 0, stream>>>(a, row_tiles(a));
+  else k_attend_rows<D, false><<<grid, kThreads, 0, stream>>>(a, row_tiles(a));
+  if (hipError_t e = hipGetLastError()) return e;
+  if (a.splits == 1) return hipSuccess;
+  const int64_t rows = (int64_t)a.c.batch * a.c.max_new * a.q_heads;
+  k_attend_join<D><<<dim3((unsigned)((rows + kWaves - 1) / kWaves)), kThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+void attend_plan(AttendArgs& a) {
+  constexpr int kUnit = kWaves * kStep;              // one step of the four waves
+  constexpr int64_t kTarget = 1024;                  // workgroups: four per CU
+  const int64_t base = (int64_t)a.c.batch * a.c.heads * row_tiles(a);
+  const int64_t units = ((int64_t)a.c.max_kv + kUnit - 1) / kUnit;
+  int64_t want = base > 0 ? (kTarget + base - 1) / base : 1;
+  if (want > kMaxSplits) want = kMaxSplits;
+  if (want > units) want = units;
+  if (want < 1) want = 1;
+  const int64_t per = units > 0 ? (units + want - 1) / want : 1;
+  a.chunk = (int32_t)(per * kUnit);
+  a.splits = units > 0 ? (int32_t)((units + per - 1) / per) : 1;
+}
+
+int64_t attend_workspace_bytes(const AttendArgs& a) {
+  return a.splits > 1 ? (int64_t)a.splits * a.c.rows * a.q_heads * (a.c.dim + 2) * 4 : 0;
+}
+
+int64_t attend_grid(const AttendArgs& a) { return (int64_t)a.c.batch * a.c.heads * row_tiles(a) * a.splits; }
+
+hipError_t launch_cache_attention(const AttendArgs& a, hipStream_t stream) {
+  return a.c.dim == 128 ? launch<128>(a, stream) : launch<64>(a, stream);
+}
+
+}  // namespace fp8bs

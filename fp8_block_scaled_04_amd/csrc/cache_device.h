@@ -1,0 +1,87 @@
+// Device helpers of the cache kernels: one sequence's geometry, page lookup,
+// code conversion, and re-encoding under another scale.
+#pragma once
+
+#include "cache.h"
+#include "quant_common.h"
+
+namespace fp8bs {
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// One sequence of a call.  Lengths come from device memory: they are clamped
+// to what the launch and the table cover, so no value of them reads or writes
+// out of range.
+struct Seq {
+  int row0;   // first packed row
+  int n;      // rows processed (at most max_new, all inside [0, rows))
+  int len;    // cached tokens
+  int base;   // slot of the first row (negative: more rows than cached tokens)
+};
+
+__device__ __forceinline__ int cached_tokens(const CacheArgs& c, int b) {
+  const int64_t room = (int64_t)c.width << c.lg_page;
+  return (int)max((int64_t)0, min((int64_t)min(c.kv_lens[b], c.max_kv), room));
+}
+
+__device__ __forceinline__ Seq sequence(const CacheArgs& c, int b) {
+  Seq s;
+  const int lo = c.q_offsets[b], hi = c.q_offsets[b + 1];
+  s.row0 = lo;
+  const bool fits = lo >= 0 && hi >= lo && hi <= c.rows;
+  s.n = fits ? min(hi - lo, c.max_new) : 0;
+  s.len = cached_tokens(c, b);
+  s.base = s.len - (fits ? hi - lo : 0);
+  return s;
+}
+
+// Page index of `slot` (below the cached tokens), or -1 for an entry outside
+// the pool.
+__device__ __forceinline__ int page_of(const CacheArgs& c, int b, int slot) {
+  const int p = c.table[(int64_t)b * c.width + (slot >> c.lg_page)];
+  return ((uint32_t)p < (uint64_t)c.pages) ? p : -1;
+}
+
+// Two E4M3 codes (the low or high half of w) as a BF16 pair: exact, every
+// code is a BF16 value.
+template <bool HI>
+__device__ __forceinline__ v2bf codes_to_bf16(uint32_t w) {
+  return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI);
+}
+
+// Four codes -> four BF16 values at f[at .. at + 3].
+__device__ __forceinline__ void unpack4(v8bf& f, int at, uint32_t w) {
+  const v2bf a = codes_to_bf16<false>(w), b = codes_to_bf16<true>(w);
+  f[at] = a[0];
+  f[at + 1] = a[1];
+  f[at + 2] = b[0];
+  f[at + 3] = b[1];
+}
+
+// A scale prepared for fl32(x / s), |x| <= 448 s up to rounding (see
+// TileScale: below s = 2^-69 both are taken times 2^64, which is exact).
+// s = 0 gives quotients that are never used.
+__device__ __forceinline__ TileScale divide_by(float s) {
+#pragma clang fp contract(off)
+  TileScale t;
+  t.s = s;
+  t.sx = (s < 0x1p-69f) ? 0x1p64f : 1.0f;
+  t.ss = s * t.sx;
+  t.r = 1.0f / t.ss;
+  return t;
+}
+
+// Four codes of scale `old` encoded again under t.s: E4M3(fl32(fl32(c old) / s)).
+__device__ __forceinline__ uint32_t reencode4(uint32_t w, float old, const TileScale& t) {
+#pragma clang fp contract(off)
+  const float a = __builtin_amdgcn_cvt_f32_fp8((int)w, 0) * old, b = __builtin_amdgcn_cvt_f32_fp8((int)w, 1) * old;
+  const float c = __builtin_amdgcn_cvt_f32_fp8((int)w, 2) * old, d = __builtin_amdgcn_cvt_f32_fp8((int)w, 3) * old;
+  return pack4_e4m3_sat(div_rn(a * t.sx, t.ss, t.r), div_rn(b * t.sx, t.ss, t.r), div_rn(c * t.sx, t.ss, t.r),
+                        div_rn(d * t.sx, t.ss, t.r));
+}
+
+}  // namespace fp8bs

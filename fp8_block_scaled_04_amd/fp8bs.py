@@ -57,12 +57,29 @@ _gsplit = _sig("fp8bs_gemm_fp8_blockscaled_splitk",
                [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _U32, _P, _I64, _P])
 _gsplit_ws = _sig("fp8bs_gemm_splitk_workspace", [_I64, _I64, _I64, _P])
 _gsplit_na = _sig("fp8bs_gemm_fp8_blockscaled_splitk_noalloc", [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _U32, _P])
+_F32 = ctypes.c_float
+
+
+class _Cache(ctypes.Structure):            # fp8bs_cache of include/fp8bs_cache.h
+    _fields_ = [("k", _P), ("ks", _P), ("v", _P), ("vs", _P), ("table", _P), ("kv_lens", _P), ("pages", _I64),
+                ("batch", _I32), ("table_width", _I32), ("heads", _I32), ("page", _I32), ("dim", _I32)]
+
+
+_CP = ctypes.POINTER(_Cache)
+_cappend = _sig("fp8bs_cache_append", [_CP, _P, _P, _I64, _P, _I64, _I32, _U32, _P])
+_cattn = _sig("fp8bs_cache_attention",
+              [_CP, _P, _I64, _I32, _P, _I64, _I32, _I32, _F32, _F32, _P, _I32, _P, _U32, _P, _I64, _P])
+_cattn_ws = _sig("fp8bs_cache_attention_workspace", [_CP, _I32, _I64, _I32, _I32, _P])
+_cweights = _sig("fp8bs_cache_attention_weights",
+                 [_CP, _P, _I64, _I32, _P, _I64, _I32, _I32, _F32, _F32, _P, _P, _P, _I64, _U32, _P])
+_cevict = _sig("fp8bs_cache_evict", [_CP, _P, _I64, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P])
 _lib.fp8bs_status_str.argtypes = [ctypes.c_int]
 _lib.fp8bs_status_str.restype = ctypes.c_char_p
 _lib.fp8bs_abi_version.argtypes = []
 _lib.fp8bs_abi_version.restype = ctypes.c_int32
 
 SCALE_POW2 = 1
+MASK_FULL = 2
 OUT_BF16, OUT_FP32 = 0, 1
 
 
@@ -419,6 +436,171 @@ def cast_to_e4m3(x: torch.Tensor) -> torch.Tensor:
     q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
     _check(_cast(_ptr(x), x.numel(), _ptr(q), _stream(x)), "cast_f32_to_e4m3")
     return q
+
+
+# ---- the paged FP8 key/value cache (include/fp8bs_cache.h) ----
+#
+# cache = (k, ks, v, vs): E4M3 codes [pages][heads][P][D] and FP32 scales
+# [pages][heads]; table [batch][width], q_offsets [batch + 1] and kv_lens
+# [batch] are int32 GPU tensors.  kv_lens counts a call's own rows.
+
+
+def _cache_args(cache, table, kv_lens):
+    k, ks, v, vs = cache
+    _codes(k, "k"); _codes(v, "v")
+    _need(k, "k", None, 4)
+    _need(v, "v", None, 4)
+    _need(ks, "ks", torch.float32, 2)
+    _need(vs, "vs", torch.float32, 2)
+    _need(table, "table", torch.int32, 2)
+    _need(kv_lens, "kv_lens", torch.int32, 1)
+    pages, heads, page, dim = k.shape
+    if v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != k.shape[:2]:
+        raise ValueError("cache shapes do not match: codes [pages][heads][P][D], scales [pages][heads]")
+    batch, width = table.shape
+    if kv_lens.shape[0] != batch:
+        raise ValueError(f"kv_lens must have {batch} entries, got {kv_lens.shape[0]}")
+    dev = k.device
+    for t, n in ((ks, "ks"), (v, "v"), (vs, "vs"), (table, "table"), (kv_lens, "kv_lens")):
+        if t.device != dev:
+            raise ValueError(f"{n} must be on {dev}")
+    c = _Cache(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), table.data_ptr(), kv_lens.data_ptr(),
+               pages, batch, width, heads, page, dim)
+    return c, dev
+
+
+def _packed(t, name, heads, dim, dev):
+    """BF16 rows [T][heads][dim], heads and dim dense, rows a stride apart."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [rows][{heads if heads is not None else 'heads'}][{dim}], "
+                         f"got {tuple(t.shape)}")
+    if t.shape[0] and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name}: the heads of a row must be dense")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim
+
+
+def _row_offsets(q_offsets, batch, dev):
+    _need(q_offsets, "q_offsets", torch.int32, 1)
+    if q_offsets.shape[0] != batch + 1 or q_offsets.device != dev:
+        raise ValueError(f"q_offsets must have {batch + 1} entries on {dev}")
+
+
+def _float_out(t, name, shape, dev, dtype=torch.float32):
+    _need(t, name, dtype)
+    if tuple(t.shape) != shape or t.device != dev:
+        raise ValueError(f"{name} must have shape {shape} on {dev}, got {tuple(t.shape)}")
+    return t
+
+
+def cache_append(k_new, v_new, cache, table, q_offsets, kv_lens, max_new: int, pow2: bool = False):
+    """Quantize new tokens' keys and values (BF16 [T][heads][D], rows may be
+    strided) into the last slots of their sequences; in place.  A page's
+    scale grows to cover its new tokens, and its older codes are then encoded
+    again."""
+    c, dev = _cache_args(cache, table, kv_lens)
+    ld = _packed(k_new, "k_new", c.heads, c.dim, dev)
+    ldv = _packed(v_new, "v_new", c.heads, c.dim, dev)
+    T = k_new.shape[0]
+    if v_new.shape[0] != T or ldv != ld:
+        raise ValueError("k_new and v_new must have the same rows and row stride")
+    _row_offsets(q_offsets, c.batch, dev)
+    _check(_cappend(c, _ptr(k_new), _ptr(v_new), ld, _ptr(q_offsets), T, max_new, SCALE_POW2 if pow2 else 0,
+                    _stream(k_new)), "cache_append")
+
+
+def cache_attention_workspace_bytes(cache, table, q_heads: int, rows: int, max_new: int, max_kv: int) -> int:
+    """Workspace bytes of cache_attention for these sizes (0: it would not
+    split the cached tokens)."""
+    pages, heads, page, dim = cache[0].shape
+    c = _Cache(None, None, None, None, None, None, pages, table.shape[0], table.shape[1], heads, page, dim)
+    out = ctypes.c_int64(0)
+    _check(_cattn_ws(c, q_heads, rows, max_new, max_kv, ctypes.byref(out)), "cache_attention_workspace")
+    return int(out.value)
+
+
+def cache_attention(q, cache, table, q_offsets, kv_lens, max_new: int, max_kv: int, scale: float, softcap: float = 0.0,
+                    full: bool = False, out_dtype=torch.bfloat16, out=None, return_lse: bool = False, workspace=None):
+    """Attention of packed rows q (BF16 [T][q_heads][D], rows may be strided)
+    over the cache: prompts, chunks and single tokens.  Row i of a sequence's
+    n sees slots 0 .. kv_len - n + i (full=True: all of them); softcap > 0
+    caps the scores by softcap * tanh(x / softcap).  Rows that see nothing
+    are 0 (lse -inf).  max_new and max_kv bound the rows and cached tokens of
+    a sequence.  -> out [T][q_heads][D], or (out, lse [T][q_heads]).
+    workspace: a uint8 tensor of cache_attention_workspace_bytes, allocated
+    here when not given."""
+    c, dev = _cache_args(cache, table, kv_lens)
+    ld = _packed(q, "q", None, c.dim, dev)
+    T, Hq, D = q.shape
+    _row_offsets(q_offsets, c.batch, dev)
+    code = _out_code(out_dtype)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=out_dtype, device=dev)
+    else:
+        _float_out(out, "out", (T, Hq, D), dev, out_dtype)
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    need = ctypes.c_int64(0)
+    _check(_cattn_ws(c, Hq, T, max_new, max_kv, ctypes.byref(need)), "cache_attention_workspace")
+    if workspace is None:
+        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
+    _check(_cattn(c, _ptr(q), ld, Hq, _ptr(q_offsets), T, max_new, max_kv, scale, softcap, _ptr(out), code, _ptr(lse),
+                  MASK_FULL if full else 0, _ptr(workspace), workspace.numel() if workspace is not None else 0,
+                  _stream(q)), "cache_attention")
+    return (out, lse) if return_lse else out
+
+
+def cache_attention_weights(q, lse, cache, table, q_offsets, kv_lens, max_new: int, max_kv: int, scale: float, acc=None,
+                            softcap: float = 0.0, full: bool = False, out=None, slots: int = None):
+    """The attention weight each cached token received from these rows (q and
+    lse of cache_attention), per key head, added to the running sums acc [batch][heads][slots]:
+    -> [batch][heads][slots] FP32, a new tensor or `out` (which may be acc).
+    Sums of the call's own slots start at 0; slots past kv_len are 0.  acc
+    None starts every sum at 0 (slots then defaults to max_kv)."""
+    c, dev = _cache_args(cache, table, kv_lens)
+    ld = _packed(q, "q", None, c.dim, dev)
+    T, Hq, _ = q.shape
+    _row_offsets(q_offsets, c.batch, dev)
+    _float_out(lse, "lse", (T, Hq), dev)
+    if acc is not None:
+        _need(acc, "acc", torch.float32, 3)
+        slots = acc.shape[2]
+        _float_out(acc, "acc", (c.batch, c.heads, slots), dev)
+    elif slots is None:
+        slots = max_kv if out is None else out.shape[-1]
+    if out is None:
+        out = torch.empty((c.batch, c.heads, slots), dtype=torch.float32, device=dev)
+    else:
+        _float_out(out, "out", (c.batch, c.heads, slots), dev)
+    _check(_cweights(c, _ptr(q), ld, Hq, _ptr(q_offsets), T, max_new, max_kv, scale, softcap, _ptr(lse), _ptr(acc),
+                     _ptr(out), slots, MASK_FULL if full else 0, _stream(q)), "cache_attention_weights")
+    return out
+
+
+def cache_evict(acc, cache, table, dst_table, kv_lens, max_kv: int, budget: int, recent: int):
+    """Keep min(kv_len, budget) tokens per sequence and head -- the last
+    `recent` ones and the largest running sums acc [batch][heads][slots] of
+    the others -- and move them, in order, to the pages dst_table
+    [batch][width] of the same pools (no page of a source sequence).
+    -> (kept int32 [batch][heads][budget]: source slots, then -1; new lengths
+    int32 [batch]; the kept tokens' sums, same shape as acc, then 0)."""
+    c, dev = _cache_args(cache, table, kv_lens)
+    _need(acc, "acc", torch.float32, 3)
+    slots = acc.shape[2]
+    _float_out(acc, "acc", (c.batch, c.heads, slots), dev)
+    _need(dst_table, "dst_table", torch.int32, 2)
+    if dst_table.shape[0] != c.batch or dst_table.device != dev:
+        raise ValueError(f"dst_table must have {c.batch} rows on {dev}")
+    kept = torch.empty((c.batch, c.heads, budget), dtype=torch.int32, device=dev)
+    lens = torch.empty((c.batch,), dtype=torch.int32, device=dev)
+    acc_out = torch.empty_like(acc)
+    _check(_cevict(c, _ptr(acc), slots, _ptr(dst_table), dst_table.shape[1], max_kv, budget, recent, _ptr(kept),
+                   _ptr(lens), _ptr(acc_out), _stream(acc)), "cache_evict")
+    return kept, lens, acc_out
 
 
 GEMM_LAYOUTS = {"dense": 0, "contiguous": 1, "masked": 2, "wgrad": 3, "fused_quantize": 4}

@@ -35,6 +35,8 @@ Modules
                 grouped, masked grouped) and an exact int64 chunk-sum path.
   accum_emu  -- emulator of a limited-precision fixed-point accumulator, with
                 and without per-128 FP32 promotion.
+  cache      -- the paged key/value cache: quantized append, attention, the
+                weight each token received, eviction (float64).
 
 Parity status: every public function here is pinned by ``-m "not gpu"``
 tests in ``tests/test_oracle_*.py`` against values fixed by something other
@@ -42,4 +44,4 @@ than this package (torch's float8/bfloat16 casts, exact integer or Fraction
 arithmetic, closed forms, brute-force searches).
 """
 
-from . import e4m3, bf16, quantize, gemm, accum_emu  # noqa: F401
+from . import e4m3, bf16, quantize, gemm, accum_emu, cache  # noqa: F401
