@@ -41,6 +41,7 @@ struct AttendArgs {
   void* out;
   float* lse;                // may be nullptr
   bool out_f32, full;
+  int32_t tile_rows;         // rows per workgroup: 16 (k_attend_rows), 128 or 256 (k_attend_tiles)
   int32_t chunk, splits;     // cached tokens per split, splits
   float* part;               // [splits][rows][q_heads][D] when splits > 1
   float2* stat;              // [splits][rows][q_heads] (running max, log2 units; sum)
@@ -74,7 +75,7 @@ struct EvictArgs {
 int64_t append_grid(const CacheArgs& c);
 int64_t evict_move_grid(const EvictArgs& a);
 
-// Sets chunk and splits from the sizes; the workspace is
+// Sets tile_rows, chunk and splits from the sizes; the workspace is
 // splits * rows * q_heads * (D + 2) floats when splits > 1, else none.
 void attend_plan(AttendArgs& a);
 int64_t attend_workspace_bytes(const AttendArgs& a);
@@ -82,6 +83,7 @@ int64_t attend_grid(const AttendArgs& a);
 int64_t weights_grid(const WeightArgs& a);
 
 hipError_t launch_cache_append(const AppendArgs& a, bool pow2, hipStream_t stream);
+hipError_t launch_attend_tiles(const AttendArgs& a, int row_tiles, hipStream_t stream);
 hipError_t launch_cache_attention(const AttendArgs& a, hipStream_t stream);
 hipError_t launch_cache_weights(const WeightArgs& a, hipStream_t stream);
 hipError_t launch_cache_evict(const EvictArgs& a, hipStream_t stream);

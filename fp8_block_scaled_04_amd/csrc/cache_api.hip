@@ -78,7 +78,8 @@ fp8bs_status fp8bs_cache_attention(const fp8bs_cache* cache, const void* q, int6
   const fp8bs_cache& c = *cache;
   if (!sizes_fit(c, rows, max_new, max_kv) || !query_sizes_fit(c, ld_q, q_heads, max_new)) return FP8BS_ERR_SHAPE;
   fp8bs::AttendArgs a{args(c, q_offsets, rows, max_new, max_kv), q, ld_q, q_heads, q_heads / c.heads, scale, softcap,
-                      out, lse, out_dtype == FP8BS_OUT_FP32, (flags & FP8BS_MASK_FULL) != 0, 0, 1, nullptr, nullptr};
+                      out, lse, out_dtype == FP8BS_OUT_FP32, (flags & FP8BS_MASK_FULL) != 0, 16, 0, 1, nullptr,
+                      nullptr};
   attend_plan(a);
   const int64_t need = attend_workspace_bytes(a);
   if (attend_grid(a) > kMaxCount || workspace_bytes < need) return FP8BS_ERR_SHAPE;

@@ -19,23 +19,6 @@ namespace {
 constexpr int kWaves = 4, kThreads = 64 * kWaves, kStep = 32;
 constexpr int kMaxSplits = 64;
 
-// cap * tanh(x / cap), as cap * (1 - 2 / (e^(2x/cap) + 1)).
-__device__ __forceinline__ float capped(float x, float cap) {
-  const float e = __builtin_amdgcn_exp2f(x * (2.0f * kLog2e / cap));
-  return cap * (1.0f - 2.0f / (e + 1.0f));
-}
-
-// Bytes of four tokens (a0..a3: the same four dims each) -> per dim the four
-// tokens' bytes.
-__device__ __forceinline__ void transpose4(const uint32_t a[4], uint32_t o[4]) {
-  const uint32_t l0 = __builtin_amdgcn_perm(a[1], a[0], 0x05010400u), h0 = __builtin_amdgcn_perm(a[1], a[0], 0x07030602u);
-  const uint32_t l1 = __builtin_amdgcn_perm(a[3], a[2], 0x05010400u), h1 = __builtin_amdgcn_perm(a[3], a[2], 0x07030602u);
-  o[0] = __builtin_amdgcn_perm(l1, l0, 0x05040100u);
-  o[1] = __builtin_amdgcn_perm(l1, l0, 0x07060302u);
-  o[2] = __builtin_amdgcn_perm(h1, h0, 0x05040100u);
-  o[3] = __builtin_amdgcn_perm(h1, h0, 0x07060302u);
-}
-
 template <int D, bool CAP>
 __global__ __launch_bounds__(kThreads) void k_attend_rows(AttendArgs a, int row_tiles) {
   const CacheArgs& c = a.c;
@@ -72,6 +55,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(AttendArgs a, int row_
     for (int k = 0; k < KS; ++k) qf[k] = *reinterpret_cast<const v8bf*>(q + 8 * k);
   }
 
+  const float inv_cap = 1.0f / a.softcap;
   v4f o[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) o[d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -111,7 +95,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(AttendArgs a, int row_
 #pragma unroll
         for (int e = 0; e < DT / 4; ++e) vraw[i][j][e] = in ? p[e] : 0u;
         float y = acc[j] * f;
-        if (CAP) y = capped(y, a.softcap);
+        if (CAP) y = capped(y, a.softcap, inv_cap);
         x[i][j] = (there && tt + 4 * g + j < min(seen, end)) ? y * kLog2e : -INFINITY;
       }
     }
@@ -259,12 +243,16 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a) {
   if (a.lse && lane == 0) a.lse[at] = total == 0.0f ? -INFINITY : (top + __builtin_log2f(total)) * kLn2;
 }
 
-int row_tiles(const AttendArgs& a) { return (int)(((int64_t)a.c.max_new * a.group + 15) / 16); }
+int row_tiles(const AttendArgs& a) {
+  return (int)(((int64_t)a.c.max_new * a.group + a.tile_rows - 1) / a.tile_rows);
+}
 
 template <int D>
 hipError_t launch(const AttendArgs& a, hipStream_t stream) {
   const dim3 grid((unsigned)attend_grid(a));
-  if (a.softcap > 0.0f) k_attend_rows<D, true><<<grid, kThreads, 0, stream>>>(a, row_tiles(a));
+  if (a.tile_rows > 16) {
+    if (hipError_t e = launch_attend_tiles(a, row_tiles(a), stream)) return e;
+  } else if (a.softcap > 0.0f) k_attend_rows<D, true><<<grid, kThreads, 0, stream>>>(a, row_tiles(a));
   else k_attend_rows<D, false><<<grid, kThreads, 0, stream>>>(a, row_tiles(a));
   if (hipError_t e = hipGetLastError()) return e;
   if (a.splits == 1) return hipSuccess;
@@ -276,16 +264,20 @@ hipError_t launch(const AttendArgs& a, hipStream_t stream) {
 }  // namespace
 
 void attend_plan(AttendArgs& a) {
-  constexpr int kUnit = kWaves * kStep;              // one step of the four waves
-  constexpr int64_t kTarget = 1024;                  // workgroups: four per CU
-  const int64_t base = (int64_t)a.c.batch * a.c.heads * row_tiles(a);
-  const int64_t units = ((int64_t)a.c.max_kv + kUnit - 1) / kUnit;
-  int64_t want = base > 0 ? (kTarget + base - 1) / base : 1;
+  const int64_t rows = (int64_t)a.c.max_new * a.group, pairs = (int64_t)a.c.batch * a.c.heads;
+  a.tile_rows = rows <= 64 ? 16 : rows <= 1024 ? 128 : 256;
+  const int unit = a.tile_rows == 16 ? kWaves * kStep : 256;
+  // workgroups that fill the GPU: four of the small ones per CU, two of 128
+  // rows, one of 256 (twice that, for an even end)
+  const int64_t target = a.tile_rows == 16 ? 1024 : a.tile_rows == 128 ? 1024 : 512;
+  const int64_t base = pairs * row_tiles(a);
+  const int64_t units = ((int64_t)a.c.max_kv + unit - 1) / unit;
+  int64_t want = base > 0 ? (target + base - 1) / base : 1;
   if (want > kMaxSplits) want = kMaxSplits;
   if (want > units) want = units;
   if (want < 1) want = 1;
   const int64_t per = units > 0 ? (units + want - 1) / want : 1;
-  a.chunk = (int32_t)(per * kUnit);
+  a.chunk = (int32_t)(per * unit);
   a.splits = units > 0 ? (int32_t)((units + per - 1) / per) : 1;
 }
 

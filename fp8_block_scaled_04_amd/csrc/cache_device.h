@@ -84,4 +84,45 @@ __device__ __forceinline__ uint32_t reencode4(uint32_t w, float old, const TileS
                         div_rn(d * t.sx, t.ss, t.r));
 }
 
+// A wave-uniform value that no kernel of the launch writes, through the scalar
+// cache.
+template <typename T>
+__device__ __forceinline__ T uniform_load(const T* p) {
+  return *reinterpret_cast<const __attribute__((address_space(4))) T*>(reinterpret_cast<uintptr_t>(p));
+}
+
+// cap * tanh(x / cap), y = x / cap.  For |y| < kCapSmall by the odd series of
+// tanh (its next term is under 2^-26 of the value there), so that small scores
+// keep FP32 relative accuracy; above by 1 - 2 / (e^(2y) + 1).
+// capped_small(w, y) is w * tanh(y) / y for any w proportional to x.
+constexpr float kCapSmall = 0.35f;
+
+__device__ __forceinline__ float capped_small(float w, float y) {
+  const float z = y * y;
+  float s = 0x1.226e355e6c23dp-7f;                   // 1382/155925
+  s = __builtin_fmaf(-s, z, 0x1.664f4882c10fap-6f);  // 62/2835
+  s = __builtin_fmaf(-s, z, 0x1.ba1ba1ba1ba1cp-5f);  // 17/315
+  s = __builtin_fmaf(-s, z, 0x1.1111111111111p-3f);  // 2/15
+  s = __builtin_fmaf(-s, z, 0x1.5555555555555p-2f);  // 1/3
+  return __builtin_fmaf(-s * z, w, w);
+}
+
+__device__ __forceinline__ float capped(float x, float cap, float inv_cap) {
+  const float y = x * inv_cap;
+  const float e = __builtin_amdgcn_exp2f(y * (2.0f * kLog2e));
+  const float large = __builtin_fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(e + 1.0f), cap);
+  return __builtin_fabsf(y) < kCapSmall ? capped_small(x, y) : large;
+}
+
+// Bytes of four tokens (a0..a3: the same four dims each) -> per dim the four
+// tokens' bytes.
+__device__ __forceinline__ void transpose4(const uint32_t a[4], uint32_t o[4]) {
+  const uint32_t l0 = __builtin_amdgcn_perm(a[1], a[0], 0x05010400u), h0 = __builtin_amdgcn_perm(a[1], a[0], 0x07030602u);
+  const uint32_t l1 = __builtin_amdgcn_perm(a[3], a[2], 0x05010400u), h1 = __builtin_amdgcn_perm(a[3], a[2], 0x07030602u);
+  o[0] = __builtin_amdgcn_perm(l1, l0, 0x05040100u);
+  o[1] = __builtin_amdgcn_perm(l1, l0, 0x07060302u);
+  o[2] = __builtin_amdgcn_perm(h1, h0, 0x05040100u);
+  o[3] = __builtin_amdgcn_perm(h1, h0, 0x07060302u);
+}
+
 }  // namespace fp8bs

@@ -13,11 +13,6 @@ namespace {
 constexpr int kWaves = 4, kThreads = 64 * kWaves, kTiles = 4;
 constexpr int kSlots = kWaves * kTiles * 16;         // per workgroup
 
-__device__ __forceinline__ float capped(float x, float cap) {
-  const float e = __builtin_amdgcn_exp2f(x * (2.0f * kLog2e / cap));
-  return cap * (1.0f - 2.0f / (e + 1.0f));
-}
-
 template <int D, bool CAP>
 __global__ __launch_bounds__(kThreads) void k_cache_weights(WeightArgs a, int tiles) {
   const CacheArgs& c = a.c;
@@ -33,6 +28,7 @@ __global__ __launch_bounds__(kThreads) void k_cache_weights(WeightArgs a, int ti
   const int64_t slot0 = (int64_t)tile * kSlots + wave * (kTiles * 16);
   if (slot0 >= a.acc_slots) return;
   const int rows = s.n * a.group;
+  const float inv_cap = 1.0f / a.softcap;
   float sum[kTiles] = {};
 
   if (slot0 < s.len && rows > 0) {
@@ -81,7 +77,7 @@ __global__ __launch_bounds__(kThreads) void k_cache_weights(WeightArgs a, int ti
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float y = x[j] * f[i];
-          if (CAP) y = capped(y, a.softcap);
+          if (CAP) y = capped(y, a.softcap, inv_cap);
           const float p = __builtin_amdgcn_exp2f((y - lse[j]) * kLog2e);
           sum[i] += slot < seen[j] ? p : 0.0f;
         }
