@@ -58,6 +58,8 @@ struct WeightArgs {
   float* acc_out;
   int64_t acc_slots;
   bool full;
+  int32_t chunk, splits;     // rows per split, splits; 0: k_weights_rows
+  float* part;               // [splits][batch][heads][acc_slots] when splits > 1
 };
 
 struct EvictArgs {
@@ -80,6 +82,9 @@ int64_t evict_move_grid(const EvictArgs& a);
 void attend_plan(AttendArgs& a);
 int64_t attend_workspace_bytes(const AttendArgs& a);
 int64_t attend_grid(const AttendArgs& a);
+// The same for the weights: chunk and splits, and the partial sums.
+void weights_plan(WeightArgs& a);
+int64_t weights_workspace_bytes(const WeightArgs& a);
 int64_t weights_grid(const WeightArgs& a);
 
 hipError_t launch_cache_append(const AppendArgs& a, bool pow2, hipStream_t stream);

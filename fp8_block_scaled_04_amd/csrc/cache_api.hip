@@ -119,23 +119,46 @@ fp8bs_status fp8bs_cache_attention_workspace(const fp8bs_cache* cache, int32_t q
 fp8bs_status fp8bs_cache_attention_weights(const fp8bs_cache* cache, const void* q, int64_t ld_q, int32_t q_heads,
                                            const int32_t* q_offsets, int64_t rows, int32_t max_new, int32_t max_kv,
                                            float scale, float softcap, const float* lse, const float* acc_in,
-                                           float* acc_out, int64_t acc_slots, uint32_t flags, fp8bs_stream_t stream) {
+                                           float* acc_out, int64_t acc_slots, uint32_t flags, void* workspace,
+                                           int64_t workspace_bytes, fp8bs_stream_t stream) {
   if (!cache) return FP8BS_ERR_NULL;
   const fp8bs_cache& c = *cache;
   if (!sizes_fit(c, rows, max_new, max_kv) || !query_sizes_fit(c, ld_q, q_heads, max_new)) return FP8BS_ERR_SHAPE;
   if (acc_slots < max_kv || acc_slots > kMaxCount) return FP8BS_ERR_SHAPE;
   fp8bs::WeightArgs a{args(c, q_offsets, rows, max_new, max_kv), q, ld_q, q_heads, q_heads / c.heads, scale, softcap,
-                      lse, acc_in, acc_out, acc_slots, (flags & FP8BS_MASK_FULL) != 0};
-  if (weights_grid(a) > kMaxCount) return FP8BS_ERR_SHAPE;
+                      lse, acc_in, acc_out, acc_slots, (flags & FP8BS_MASK_FULL) != 0, 0, 0, nullptr};
+  weights_plan(a);
+  const int64_t need = weights_workspace_bytes(a);
+  if (weights_grid(a) > kMaxCount || workspace_bytes < need) return FP8BS_ERR_SHAPE;
   if ((flags & ~(uint32_t)FP8BS_MASK_FULL) || bad_scalars(scale, softcap)) return FP8BS_ERR_FLAGS;
   if (c.batch == 0 || acc_slots == 0) return FP8BS_OK;
-  if ((rows > 0 && (!q || !lse)) || !q_offsets || !acc_out) return FP8BS_ERR_NULL;
+  if ((rows > 0 && (!q || !lse)) || !q_offsets || !acc_out || (need > 0 && !workspace)) return FP8BS_ERR_NULL;
   if (fp8bs_status e = cache_pointers(c, false)) return e;
-  if (!aligned16(q) || !aligned4(q_offsets) || !aligned4(lse) || !aligned4(acc_in) || !aligned4(acc_out))
+  if (!aligned16(q) || !aligned4(q_offsets) || !aligned4(lse) || !aligned4(acc_in) || !aligned4(acc_out) ||
+      (need > 0 && !aligned16(workspace)))
     return FP8BS_ERR_ALIGN;
   if (fp8bs_status e = check_device()) return e;
+  a.part = static_cast<float*>(workspace);
   (void)hipGetLastError();
   return launched(fp8bs::launch_cache_weights(a, (hipStream_t)stream));
+}
+
+fp8bs_status fp8bs_cache_attention_weights_workspace(const fp8bs_cache* cache, int32_t q_heads, int32_t max_new,
+                                                     int64_t acc_slots, int64_t* bytes) {
+  if (!cache) return FP8BS_ERR_NULL;
+  const fp8bs_cache& c = *cache;
+  if (!sizes_fit(c, 0, max_new, 0) || q_heads <= 0 || acc_slots < 0 || acc_slots > kMaxCount ||
+      !query_sizes_fit(c, (int64_t)q_heads * c.dim, q_heads, max_new))
+    return FP8BS_ERR_SHAPE;
+  if (!bytes) return FP8BS_ERR_NULL;
+  fp8bs::WeightArgs a{};
+  a.c = args(c, nullptr, 0, max_new, 0);
+  a.q_heads = q_heads;
+  a.group = q_heads / c.heads;
+  a.acc_slots = acc_slots;
+  weights_plan(a);
+  *bytes = weights_workspace_bytes(a);
+  return FP8BS_OK;
 }
 
 fp8bs_status fp8bs_cache_evict(const fp8bs_cache* cache, const float* acc, int64_t acc_slots,

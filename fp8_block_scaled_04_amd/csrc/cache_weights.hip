@@ -1,35 +1,42 @@
 // The attention weight each cached token received (include/fp8bs_cache.h,
 // fp8bs_cache_attention_weights): acc[j] (+)= sum over rows of exp(x_j - lse).
 //
-// One workgroup per (sequence, head, 256 slots) walks every row, so each
-// slot's sum has one owner and a fixed order.  Scores are formed as S = Q K^T:
-// a lane then holds one token and four rows per matrix step, and the sum over
-// rows stays in the lane.
+// Scores are formed as S = Q K^T: a lane then holds one token and several rows
+// per matrix step, and the sum over rows stays in the lane.  A workgroup owns
+// its slots (and its share of the rows): each sum has a fixed order.
+//
+// k_weights_rows (at most 16 rows, decoding): every key is read once and used
+// once, 16x16x32 products.  k_weights_tiles (more rows): 32x32x16 products, 64
+// tokens per wave with their keys in registers, Q walked through LDS 64 rows
+// at a time; the rows may be split over workgroups, whose partial sums
+// k_weights_join adds in order.
 #include "cache_device.h"
 
 namespace fp8bs {
 namespace {
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves, kTiles = 4;
-constexpr int kSlots = kWaves * kTiles * 16;         // per workgroup
+constexpr int kSlots = kWaves * kTiles * 16;         // per workgroup, both kernels
+
+__device__ __forceinline__ float old_sum(const WeightArgs& a, const Seq& s, int64_t pair, int64_t slot) {
+  return a.acc_in && slot < min(s.base, s.len) ? a.acc_in[pair * a.acc_slots + slot] : 0.0f;
+}
 
 template <int D, bool CAP>
-__global__ __launch_bounds__(kThreads) void k_cache_weights(WeightArgs a, int tiles) {
+__global__ __launch_bounds__(kThreads) void k_weights_rows(WeightArgs a, int tiles) {
   const CacheArgs& c = a.c;
   constexpr int KS = D / 32;
-  int id = blockIdx.x;
-  const int tile = id % tiles;
-  id /= tiles;
-  const int h = id % c.heads, b = id / c.heads;
+  const int tile = blockIdx.x % tiles, pair = blockIdx.x / tiles;
+  const int h = pair % c.heads, b = pair / c.heads;
   const Seq s = sequence(c, b);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, r = lane & 15;
-  const int64_t acc_at = ((int64_t)b * c.heads + h) * a.acc_slots;
   const int64_t slot0 = (int64_t)tile * kSlots + wave * (kTiles * 16);
   if (slot0 >= a.acc_slots) return;
   const int rows = s.n * a.group;
   const float inv_cap = 1.0f / a.softcap;
   float sum[kTiles] = {};
+  bool there[kTiles] = {};
 
   if (slot0 < s.len && rows > 0) {
     v8bf kf[kTiles][KS];
@@ -38,10 +45,10 @@ __global__ __launch_bounds__(kThreads) void k_cache_weights(WeightArgs a, int ti
     for (int i = 0; i < kTiles; ++i) {
       const int tt = (int)slot0 + 16 * i;
       int page = page_of(c, b, min(tt, s.len - 1));
-      const bool there = page >= 0;
+      there[i] = page >= 0;
       page = max(page, 0);
       const int64_t at = (int64_t)page * c.heads + h;
-      f[i] = there ? c.ks[at] * a.scale : 0.0f;      // an absent page's tokens are dropped at the end
+      f[i] = there[i] ? c.ks[at] * a.scale : 0.0f;
       const uint8_t* kp = c.k + (at << c.lg_page) * D + (int64_t)((tt & ((1 << c.lg_page) - 1)) + r) * D + g * (D / 4);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
@@ -50,73 +57,313 @@ __global__ __launch_bounds__(kThreads) void k_cache_weights(WeightArgs a, int ti
         unpack4(kf[i][k], 4, w.y);
       }
     }
-    // rows before the first that sees the wave's first slot add nothing
-    const int skip = a.full ? 0 : max(0, (int)slot0 - s.base) * a.group;
-    for (int row0 = skip & ~15; row0 < rows; row0 += 16) {
-      const int qrow = min(row0 + r, rows - 1);
-      const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)(s.row0 + qrow / a.group) * a.ld_q +
-                          (int64_t)(h * a.group + qrow % a.group) * D + g * (D / 4);
-      v8bf qf[KS];
+    const int qrow = min(r, rows - 1);
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)(s.row0 + qrow / a.group) * a.ld_q +
+                        (int64_t)(h * a.group + qrow % a.group) * D + g * (D / 4);
+    v8bf qf[KS];
 #pragma unroll
-      for (int k = 0; k < KS; ++k) qf[k] = *reinterpret_cast<const v8bf*>(q + 8 * k);
-      float lse[4];
-      int seen[4];
+    for (int k = 0; k < KS; ++k) qf[k] = *reinterpret_cast<const v8bf*>(q + 8 * k);
+    float lse[4];
+    int seen[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = 4 * g + j, cl = min(row, rows - 1), tok = cl / a.group;
+      lse[j] = a.lse[(int64_t)(s.row0 + tok) * a.q_heads + h * a.group + cl % a.group];
+      seen[j] = (row < rows && lse[j] != -INFINITY) ? (a.full ? s.len : min(s.len, s.base + tok + 1)) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[k], kf[i][k], x, 0, 0, 0);
+      const int slot = (int)slot0 + 16 * i + r;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int row = row0 + 4 * g + j;
-        const int cl = min(row, rows - 1), tok = cl / a.group;
-        lse[j] = a.lse[(int64_t)(s.row0 + tok) * a.q_heads + h * a.group + cl % a.group];
-        seen[j] = (row < rows && lse[j] != -INFINITY) ? (a.full ? s.len : min(s.len, s.base + tok + 1)) : 0;
-      }
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int k = 0; k < KS; ++k) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[k], kf[i][k], x, 0, 0, 0);
-        const int slot = (int)slot0 + 16 * i + r;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float y = x[j] * f[i];
-          if (CAP) y = capped(y, a.softcap, inv_cap);
-          const float p = __builtin_amdgcn_exp2f((y - lse[j]) * kLog2e);
-          sum[i] += slot < seen[j] ? p : 0.0f;
-        }
+        float y = x[j] * f[i];
+        if (CAP) y = capped(y, a.softcap, inv_cap);
+        const float p = __builtin_amdgcn_exp2f((y - lse[j]) * kLog2e);
+        sum[i] += slot < seen[j] ? p : 0.0f;
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) {
-    float x = sum[i];
+    float x = there[i] ? sum[i] : 0.0f;
     x += __shfl_xor(x, 16);
     x += __shfl_xor(x, 32);
     const int64_t slot = slot0 + 16 * i + r;
-    if (g != 0 || slot >= a.acc_slots) continue;
-    bool there = slot < s.len;
-    if (there) there = page_of(c, b, (int)slot) >= 0;
-    float old = 0.0f;
-    if (a.acc_in && slot < min(s.base, s.len)) old = a.acc_in[acc_at + slot];
-    a.acc_out[acc_at + slot] = there ? old + x : old;
+    if (g == 0 && slot < a.acc_slots) a.acc_out[(int64_t)pair * a.acc_slots + slot] = old_sum(a, s, pair, slot) + x;
   }
+}
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+constexpr int kRows = 64;                            // Q rows per step
+
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
+// Rows of the sequence before the first that sees any of the slots from slot0.
+__device__ __forceinline__ int hidden_rows(const WeightArgs& a, const Seq& s, int64_t slot0) {
+  return a.full ? 0 : (int)min((int64_t)s.n, max((int64_t)0, slot0 - s.base)) * a.group;
+}
+
+template <int D, bool CAP>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2)))
+void k_weights_tiles(WeightArgs a, int tiles) {
+  const CacheArgs& c = a.c;
+  constexpr int KS = D / 16;                         // matrix steps of a score
+  constexpr int CH = D / 8;                          // 16-byte chunks of a row
+  constexpr int QP = kRows * CH / kThreads;          // per thread and step
+  __shared__ __attribute__((aligned(16))) uint16_t s_q[2][kRows * D];
+  __shared__ __attribute__((aligned(16))) float s_lse[2][kRows];     // log2 units; +inf: the row adds nothing
+  __shared__ __attribute__((aligned(16))) int s_seen[2][kRows];
+
+  // (sequence, head) pairs go round the XCDs; a pair's first slots, which the
+  // most rows see, start first
+  const int pairs = c.batch * c.heads;
+  int pair, tile, split;
+  {
+    int id = blockIdx.x;
+    const int per = tiles * a.splits, full = pairs & ~7;
+    if (id < full * per) {
+      pair = (id / (8 * per)) * 8 + id % 8;
+      id = (id / 8) % per;
+    } else {
+      id -= full * per;
+      const int left = pairs - full;
+      pair = full + id % left;
+      id /= left;
+    }
+    split = id % a.splits;
+    tile = id / a.splits;
+  }
+  const int h = pair % c.heads, b = pair / c.heads;
+  const Seq s = sequence(c, b);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = lane >> 5, r = lane & 31;
+  const int rows = s.n * a.group;
+  const int64_t wg0 = (int64_t)tile * kSlots, slot0 = wg0 + wave * 64;
+  const int begin = max(split * a.chunk, hidden_rows(a, s, wg0) & ~(kRows - 1));
+  const int end = wg0 < s.len ? min(rows, (split + 1) * a.chunk) : 0;
+  if (a.splits > 1 && begin >= end) return;          // the join knows
+  const float fscale = a.scale * (CAP ? 1.0f : kLog2e);
+  const float inv_cap = 1.0f / a.softcap;
+  float sum[2] = {0.0f, 0.0f};
+  bool there[2] = {false, false};
+
+  if (begin < end) {                                 // uniform over the workgroup
+    // this lane's keys: token slot0 + 32 u + r, dims D / 2 x half + 8 k ..
+    v8bf kf[2][KS];
+    float f[2];
+    int mine[2];
+    bool whole = slot0 + 64 <= s.len;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int tt = (int)min(slot0 + 32 * u + r, (int64_t)s.len - 1);
+      int page = page_of(c, b, tt);
+      there[u] = page >= 0 && slot0 + 32 * u + r < s.len;
+      whole = whole && page >= 0;
+      page = max(page, 0);
+      const int64_t at = (int64_t)page * c.heads + h;
+      f[u] = c.ks[at] * fscale;
+      mine[u] = there[u] ? tt : 0x7FFFFFFF;
+      const uint8_t* kp = c.k + (at << c.lg_page) * D + (int64_t)(tt & ((1 << c.lg_page) - 1)) * D + half * (D / 2);
+#pragma unroll
+      for (int k = 0; k < KS; k += 2) {
+        const uint4 w = *reinterpret_cast<const uint4*>(kp + 8 * k);
+        unpack4(kf[u][k], 0, w.x);
+        unpack4(kf[u][k], 4, w.y);
+        unpack4(kf[u][k + 1], 0, w.z);
+        unpack4(kf[u][k + 1], 4, w.w);
+      }
+    }
+    whole = __all(whole);
+
+    // Where this thread's pieces of the next step's rows lie.  Row = token x
+    // group + head: 64 rows on is 64 / group tokens and 64 % group heads on,
+    // with a carry (no division in the loop).
+    struct Place { const uint16_t* p; int g; };
+    const int dtok = kRows / a.group, dhead = kRows % a.group;
+    const int64_t ahead = (int64_t)dtok * a.ld_q + (int64_t)dhead * D, carry = a.ld_q - (int64_t)a.group * D;
+    const uint16_t* qbase = static_cast<const uint16_t*>(a.q) + (int64_t)s.row0 * a.ld_q + (int64_t)h * a.group * D;
+    Place at[QP];
+#pragma unroll
+    for (int i = 0; i < QP; ++i) {
+      const int piece = i * kThreads + tid, row = begin + piece / CH, tok = row / a.group;
+      at[i].g = row - tok * a.group;
+      at[i].p = qbase + (int64_t)tok * a.ld_q + at[i].g * D + (piece % CH) * 8;
+    }
+    const float* lbase = a.lse + (int64_t)s.row0 * a.q_heads + h * a.group;
+    int ltok = (begin + tid) / a.group, lhead = begin + tid - ltok * a.group;   // threads below kRows
+
+    uint4 qraw[QP];
+    float lraw = 0.0f;
+    int seen_at = 0;
+    auto load = [&](int row0) {
+#pragma unroll
+      for (int i = 0; i < QP; ++i) {
+        // rows past the end read the first one and add nothing
+        const uint16_t* p = row0 + (i * kThreads + tid) / CH < rows ? at[i].p : qbase;
+        qraw[i] = *reinterpret_cast<const uint4*>(p);
+        at[i].g += dhead;
+        const bool over = at[i].g >= a.group;
+        at[i].g -= over ? a.group : 0;
+        at[i].p += ahead + (over ? carry : 0);
+      }
+      if (tid < kRows) {
+        const bool in = row0 + tid < end;
+        lraw = in ? lbase[(int64_t)ltok * a.q_heads + lhead] : -INFINITY;
+        seen_at = a.full ? s.len : min(s.len, s.base + ltok + 1);
+        lhead += dhead;
+        const bool over = lhead >= a.group;
+        lhead -= over ? a.group : 0;
+        ltok += dtok + (over ? 1 : 0);
+      }
+    };
+    auto store = [&](int buf) {
+#pragma unroll
+      for (int i = 0; i < QP; ++i) {
+        const int piece = i * kThreads + tid, row = piece / CH;
+        *reinterpret_cast<uint4*>(&s_q[buf][row * D + (((piece % CH) ^ (row & (CH - 1))) * 8)]) = qraw[i];
+      }
+      if (tid < kRows) {
+        s_lse[buf][tid] = lraw != -INFINITY ? lraw * kLog2e : INFINITY;
+        s_seen[buf][tid] = seen_at;
+      }
+    };
+    auto score = [&](v16f (&x)[2], int buf, int t) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[u][i] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const int row = 32 * t + r, chunk = half * KS + k;
+        const v8bf qf = *reinterpret_cast<const v8bf*>(&s_q[buf][row * D + ((chunk ^ (row & (CH - 1))) * 8)]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) x[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf, kf[u][k], x[u], 0, 0, 0);
+      }
+    };
+    // x[u][4 j + i] is row 32 t + 8 j + 4 half + i
+    auto add = [&](const v16f (&x)[2], int buf, int t, auto masked) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = 32 * t + 8 * j + 4 * half;
+        const v4f lse = *reinterpret_cast<const v4f*>(&s_lse[buf][row]);
+        int4 seen = {};
+        if (decltype(masked)::value) seen = *reinterpret_cast<const int4*>(&s_seen[buf][row]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float y = x[u][4 * j + i];
+            if (CAP) y = __builtin_fmaf(capped(y * f[u], a.softcap, inv_cap), kLog2e, -lse[i]);
+            else y = __builtin_fmaf(y, f[u], -lse[i]);
+            float p = __builtin_amdgcn_exp2f(y);
+            if (decltype(masked)::value) p = mine[u] < (i == 0 ? seen.x : i == 1 ? seen.y : i == 2 ? seen.z : seen.w) ? p : 0.0f;
+            sum[u] += p;
+          }
+      }
+      asm volatile("" : "+v"(sum[0]), "+v"(sum[1]));  // sums are taken here: sunk below, they would hold every score
+    };
+    auto step = [&](int buf, auto masked) {
+      v16f x0[2], x1[2];
+      score(x0, buf, 0);
+      score(x1, buf, 1);
+      add(x0, buf, 0, masked);
+      add(x1, buf, 1, masked);
+    };
+    load(begin);
+    store(0);
+    __syncthreads();
+    int buf = 0;
+    for (int row0 = begin; row0 < end; row0 += kRows, buf ^= 1) {
+      const bool more = row0 + kRows < end;
+      if (more) load(row0 + kRows);
+      // does the step's first row see all of the wave's tokens?
+      if (whole && __builtin_amdgcn_readfirstlane(s_seen[buf][0]) >= slot0 + 64) step(buf, Int<0>{});
+      else step(buf, Int<1>{});
+      if (more) store(buf ^ 1);
+      __syncthreads();
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    float x = there[u] ? sum[u] : 0.0f;
+    x += __shfl_xor(x, 32);
+    const int64_t slot = slot0 + 32 * u + r;
+    if (half != 0 || slot >= a.acc_slots) continue;
+    if (a.splits > 1) a.part[((int64_t)split * pairs + pair) * a.acc_slots + slot] = x;
+    else a.acc_out[(int64_t)pair * a.acc_slots + slot] = old_sum(a, s, pair, slot) + x;
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void k_weights_join(WeightArgs a) {
+  const CacheArgs& c = a.c;
+  const int pairs = c.batch * c.heads;
+  const int64_t per = (a.acc_slots + kThreads - 1) / kThreads;
+  const int pair = (int)(blockIdx.x / per);
+  const int64_t slot = (blockIdx.x % per) * kThreads + threadIdx.x;
+  if (slot >= a.acc_slots) return;
+  const Seq s = sequence(c, pair / c.heads);
+  const int64_t wg0 = slot & ~(int64_t)(kSlots - 1);
+  const int rows = wg0 < s.len ? s.n * a.group : 0, first = hidden_rows(a, s, wg0) & ~(kRows - 1);
+  float x = old_sum(a, s, pair, slot);
+  for (int p = first / a.chunk; p < a.splits && p * a.chunk < rows; ++p)
+    x += a.part[((int64_t)p * pairs + pair) * a.acc_slots + slot];
+  a.acc_out[(int64_t)pair * a.acc_slots + slot] = x;
 }
 
 int slot_tiles(const WeightArgs& a) { return (int)((a.acc_slots + kSlots - 1) / kSlots); }
 
+template <int D, bool CAP>
+hipError_t launch(const WeightArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)weights_grid(a));
+  if (a.splits == 0) {
+    k_weights_rows<D, CAP><<<grid, kThreads, 0, stream>>>(a, slot_tiles(a));
+    return hipGetLastError();
+  }
+  k_weights_tiles<D, CAP><<<grid, kThreads, 0, stream>>>(a, slot_tiles(a));
+  if (hipError_t e = hipGetLastError()) return e;
+  if (a.splits == 1) return hipSuccess;
+  const int64_t per = (a.acc_slots + kThreads - 1) / kThreads;
+  k_weights_join<<<dim3((unsigned)((int64_t)a.c.batch * a.c.heads * per)), kThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
 }  // namespace
 
-int64_t weights_grid(const WeightArgs& a) { return (int64_t)a.c.batch * a.c.heads * slot_tiles(a); }
+void weights_plan(WeightArgs& a) {
+  const int64_t rows = (int64_t)a.c.max_new * a.group;
+  a.splits = 0;
+  a.chunk = 0;
+  if (rows <= 16) return;
+  // several workgroups per CU (the causal rule empties up to half of them),
+  // each at least 512 rows long
+  const int64_t base = (int64_t)a.c.batch * a.c.heads * slot_tiles(a);
+  int64_t want = base > 0 ? (4096 + base - 1) / base : 1;
+  const int64_t most = (rows + 511) / 512;
+  if (want > most) want = most;
+  const int64_t per = (rows + want - 1) / want;
+  a.chunk = (int32_t)((per + kRows - 1) / kRows * kRows);
+  a.splits = (int32_t)((rows + a.chunk - 1) / a.chunk);
+}
+
+int64_t weights_workspace_bytes(const WeightArgs& a) {
+  return a.splits > 1 ? (int64_t)a.splits * a.c.batch * a.c.heads * a.acc_slots * 4 : 0;
+}
+
+int64_t weights_grid(const WeightArgs& a) {
+  return (int64_t)a.c.batch * a.c.heads * slot_tiles(a) * (a.splits > 1 ? a.splits : 1);
+}
 
 hipError_t launch_cache_weights(const WeightArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)weights_grid(a));
-  const int t = slot_tiles(a);
   const bool cap = a.softcap > 0.0f;
-  if (a.c.dim == 128) {
-    if (cap) k_cache_weights<128, true><<<grid, kThreads, 0, stream>>>(a, t);
-    else k_cache_weights<128, false><<<grid, kThreads, 0, stream>>>(a, t);
-  } else {
-    if (cap) k_cache_weights<64, true><<<grid, kThreads, 0, stream>>>(a, t);
-    else k_cache_weights<64, false><<<grid, kThreads, 0, stream>>>(a, t);
-  }
-  return hipGetLastError();
+  if (a.c.dim == 128) return cap ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
+  return cap ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
 }
 
 }  // namespace fp8bs

@@ -71,7 +71,8 @@ _cattn = _sig("fp8bs_cache_attention",
               [_CP, _P, _I64, _I32, _P, _I64, _I32, _I32, _F32, _F32, _P, _I32, _P, _U32, _P, _I64, _P])
 _cattn_ws = _sig("fp8bs_cache_attention_workspace", [_CP, _I32, _I64, _I32, _I32, _P])
 _cweights = _sig("fp8bs_cache_attention_weights",
-                 [_CP, _P, _I64, _I32, _P, _I64, _I32, _I32, _F32, _F32, _P, _P, _P, _I64, _U32, _P])
+                 [_CP, _P, _I64, _I32, _P, _I64, _I32, _I32, _F32, _F32, _P, _P, _P, _I64, _U32, _P, _I64, _P])
+_cweights_ws = _sig("fp8bs_cache_attention_weights_workspace", [_CP, _I32, _I32, _I64, _P])
 _cevict = _sig("fp8bs_cache_evict", [_CP, _P, _I64, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P])
 _lib.fp8bs_status_str.argtypes = [ctypes.c_int]
 _lib.fp8bs_status_str.restype = ctypes.c_char_p
@@ -496,6 +497,14 @@ def _float_out(t, name, shape, dev, dtype=torch.float32):
     return t
 
 
+def _workspace(workspace, need, dev):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
+    return workspace
+
+
 def cache_append(k_new, v_new, cache, table, q_offsets, kv_lens, max_new: int, pow2: bool = False):
     """Quantize new tokens' keys and values (BF16 [T][heads][D], rows may be
     strided) into the last slots of their sequences; in place.  A page's
@@ -544,23 +553,32 @@ def cache_attention(q, cache, table, q_offsets, kv_lens, max_new: int, max_kv: i
     lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
     need = ctypes.c_int64(0)
     _check(_cattn_ws(c, Hq, T, max_new, max_kv, ctypes.byref(need)), "cache_attention_workspace")
-    if workspace is None:
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
-        raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
+    workspace = _workspace(workspace, need.value, dev)
     _check(_cattn(c, _ptr(q), ld, Hq, _ptr(q_offsets), T, max_new, max_kv, scale, softcap, _ptr(out), code, _ptr(lse),
                   MASK_FULL if full else 0, _ptr(workspace), workspace.numel() if workspace is not None else 0,
                   _stream(q)), "cache_attention")
     return (out, lse) if return_lse else out
 
 
+def cache_attention_weights_workspace_bytes(cache, table, q_heads: int, max_new: int, slots: int) -> int:
+    """Workspace bytes of cache_attention_weights for these sizes (0: it would
+    not split the rows)."""
+    pages, heads, page, dim = cache[0].shape
+    c = _Cache(None, None, None, None, None, None, pages, table.shape[0], table.shape[1], heads, page, dim)
+    out = ctypes.c_int64(0)
+    _check(_cweights_ws(c, q_heads, max_new, slots, ctypes.byref(out)), "cache_attention_weights_workspace")
+    return int(out.value)
+
+
 def cache_attention_weights(q, lse, cache, table, q_offsets, kv_lens, max_new: int, max_kv: int, scale: float, acc=None,
-                            softcap: float = 0.0, full: bool = False, out=None, slots: int = None):
+                            softcap: float = 0.0, full: bool = False, out=None, slots: int = None, workspace=None):
     """The attention weight each cached token received from these rows (q and
     lse of cache_attention), per key head, added to the running sums acc [batch][heads][slots]:
     -> [batch][heads][slots] FP32, a new tensor or `out` (which may be acc).
     Sums of the call's own slots start at 0; slots past kv_len are 0.  acc
-    None starts every sum at 0 (slots then defaults to max_kv)."""
+    None starts every sum at 0 (slots then defaults to max_kv).  workspace: a
+    uint8 tensor of cache_attention_weights_workspace_bytes, allocated here
+    when not given."""
     c, dev = _cache_args(cache, table, kv_lens)
     ld = _packed(q, "q", None, c.dim, dev)
     T, Hq, _ = q.shape
@@ -576,8 +594,12 @@ def cache_attention_weights(q, lse, cache, table, q_offsets, kv_lens, max_new: i
         out = torch.empty((c.batch, c.heads, slots), dtype=torch.float32, device=dev)
     else:
         _float_out(out, "out", (c.batch, c.heads, slots), dev)
+    need = ctypes.c_int64(0)
+    _check(_cweights_ws(c, Hq, max_new, slots, ctypes.byref(need)), "cache_attention_weights_workspace")
+    workspace = _workspace(workspace, need.value, dev)
     _check(_cweights(c, _ptr(q), ld, Hq, _ptr(q_offsets), T, max_new, max_kv, scale, softcap, _ptr(lse), _ptr(acc),
-                     _ptr(out), slots, MASK_FULL if full else 0, _stream(q)), "cache_attention_weights")
+                     _ptr(out), slots, MASK_FULL if full else 0, _ptr(workspace),
+                     workspace.numel() if workspace is not None else 0, _stream(q)), "cache_attention_weights")
     return out
 
 

@@ -116,13 +116,20 @@ fp8bs_status fp8bs_cache_attention_workspace(const fp8bs_cache* cache, int32_t q
  * lse = -inf adds nothing).
  *   acc_in, acc_out : FP32 [batch][heads][acc_slots], acc_slots >= max_kv;
  *                     they may be the same array, and acc_in NULL (old = 0)
+ *   workspace : fp8bs_cache_attention_weights_workspace bytes (NULL if 0)
  * Slots from kv_lens[b] on are set to 0.  Reads k and ks of *cache only.
  */
 fp8bs_status fp8bs_cache_attention_weights(const fp8bs_cache* cache, const void* q, int64_t ld_q,
                                            int32_t q_heads, const int32_t* q_offsets, int64_t rows,
                                            int32_t max_new, int32_t max_kv, float scale, float softcap,
                                            const float* lse, const float* acc_in, float* acc_out,
-                                           int64_t acc_slots, uint32_t flags, fp8bs_stream_t stream);
+                                           int64_t acc_slots, uint32_t flags, void* workspace,
+                                           int64_t workspace_bytes, fp8bs_stream_t stream);
+
+/* Workspace bytes of fp8bs_cache_attention_weights (bytes: HOST pointer);
+ * reads only the sizes of *cache. */
+fp8bs_status fp8bs_cache_attention_weights_workspace(const fp8bs_cache* cache, int32_t q_heads,
+                                                     int32_t max_new, int64_t acc_slots, int64_t* bytes);
 
 /*
  * Evict: keep count = min(kv_lens[b], budget) tokens of each sequence and
