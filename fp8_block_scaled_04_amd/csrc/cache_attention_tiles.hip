@@ -10,9 +10,12 @@
 // P^T's operand layout once the 16 tokens of a step are stored in LDS in the
 // order 8 a + 4 half + i -> 8 half + 4 a + i.
 //
-// Software pipeline: scores of step t + 1 (matrix core) are formed beside the
-// softmax of step t (vector unit), so keys are staged two steps ahead, values
-// one.  One barrier per step.
+// Two groups of waves, one of each on every SIMD, take turns: while one group
+// runs its matrix phase (outputs of step t - 1, scores of step t), the other
+// runs its softmax phase on the vector unit, with a barrier between phases.
+// The staging rides in the matrix phase, whose vector slots are free: keys of
+// step t + 1 and values of step t are converted and written there, the codes
+// of the next ones requested.
 #include "cache_device.h"
 
 namespace fp8bs {
@@ -27,11 +30,18 @@ struct Int {
   static constexpr int value = N;
 };
 
+// Whether any lane of the wave has it (wave-uniform).
+__device__ __forceinline__ bool any_lane(bool x) { return __builtin_amdgcn_ballot_w64(x) != 0; }
+
 // Keys: row = token, 16-byte chunks of 8 dims.  A wave's reads take one chunk
-// of 32 rows, its writes whole rows: chunk ^ row spreads both over the banks.
+// of 32 rows: rows 16 bytes longer than D walk over all banks, and every read
+// of a step is one lane address plus a constant.
+template <int D>
+constexpr int kPitch = D + 8;
+
 template <int D>
 __device__ __forceinline__ int k_at(int tok, int chunk) {
-  return tok * D + ((chunk ^ (tok & (D / 8 - 1) & 15)) * 8);
+  return tok * kPitch<D> + chunk * 8;
 }
 
 // Values: row = dim, 16-byte chunks of 8 tokens.  Reads take one chunk of 32
@@ -50,7 +60,7 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
   constexpr int KP = kTok * (D / 8) / T;             // 8-byte key pieces per thread
   constexpr int VG = (kTok / 4) * (D / 4);           // 4 x 4 groups of values
   constexpr int VP = (VG + T - 1) / T;               // per thread
-  __shared__ __attribute__((aligned(16))) uint16_t s_k[2][kTok * D];
+  __shared__ __attribute__((aligned(16))) uint16_t s_k[2][kTok * kPitch<D>];
   __shared__ __attribute__((aligned(16))) uint16_t s_v[2][kTok * D];
 
   // (sequence, head) pairs go round the XCDs, so that the row tiles of a pair
@@ -115,180 +125,209 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
   const int mask = (1 << c.lg_page) - 1;
   const int32_t* table = c.table + (int64_t)b * c.width;
 
-  // Pages of a step's four 16-token groups (wave-uniform; -1: absent or past
-  // the end), looked up three steps ahead.
-  struct Pages { int p[4]; };
-  auto lookup = [&](int t) {
-    Pages g;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int tt = t + 16 * u;
-      const int p = uniform_load(table + (min(tt, s.len - 1) >> c.lg_page));
-      g.p[u] = (tt < s.len && (uint32_t)p < (uint64_t)c.pages) ? p : -1;
-    }
-    return g;
+  // Pages of a step's four 16-token groups: lane x holds group x % 4's, or -1
+  // (absent, or past the end).  Looked up four steps ahead; group g's page
+  // reaches the scalar unit by readlane.
+  const int my_group = 16 * (lane & 3);
+  auto lookup = [&](int t) { return table[min(t + my_group, s.len - 1) >> c.lg_page]; };
+  auto check = [&](int raw, int t) {
+    return t + my_group < s.len && (uint32_t)raw < (uint64_t)c.pages ? raw : -1;
   };
-  auto pick = [](const Pages& g, int u) { return u == 0 ? g.p[0] : u == 1 ? g.p[1] : u == 2 ? g.p[2] : g.p[3]; };
-  auto base_of = [&](const uint8_t* pool, int p) { return pool + ((int64_t)max(p, 0) * c.heads + h) * page_bytes; };
+  const int64_t page_stride = page_bytes * c.heads;
+  const uint8_t* const kpool = c.k + h * page_bytes;
+  const uint8_t* const vpool = c.v + h * page_bytes;
+  auto base_of = [&](const uint8_t* pool, int pages, int g) {
+    return pool + max(__builtin_amdgcn_readlane(pages, g), 0) * page_stride;
+  };
 
   // Staging: an absent group reads page 0 and is masked like one past the end.
-  uint2 kraw[KP];
-  uint32_t vraw[VP][4];
-  auto load_k = [&](const Pages& g, int t) {
+  // Two sets of codes: the one to be stored, and the one still in flight.
+  uint2 kraw[KP], knext[KP];
+  uint32_t vraw[VP][4], vnext[VP][4];
+  auto load_k = [&](int pages, int t) {
 #pragma unroll
     for (int i = 0; i < KP; ++i) {
       const int piece = i * T + tid, kt = piece / (D / 8);
-      const uint8_t* src = base_of(c.k, pick(g, __builtin_amdgcn_readfirstlane(kt >> 4))) + (t & mask) * D;
-      kraw[i] = *reinterpret_cast<const uint2*>(src + (uint32_t)((kt & mask) * D + (piece % (D / 8)) * 8));
+      const uint8_t* src = base_of(kpool, pages, __builtin_amdgcn_readfirstlane(kt >> 4)) + (t & mask) * D;
+      knext[i] = *reinterpret_cast<const uint2*>(src + (uint32_t)((kt & mask) * D + (piece % (D / 8)) * 8));
     }
   };
-  auto store_k = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < KP; ++i) {
-      const int piece = i * T + tid;
-      v8bf f;
-      unpack4(f, 0, kraw[i].x);
-      unpack4(f, 4, kraw[i].y);
-      *reinterpret_cast<v8bf*>(&s_k[buf][k_at<D>(piece / (D / 8), piece % (D / 8))]) = f;
-    }
-  };
-  auto load_v = [&](const Pages& g, int t) {
+  auto load_v = [&](int pages, int t) {
 #pragma unroll
     for (int i = 0; i < VP; ++i) {
       const int grp = i * T + tid, t4 = grp / (D / 4) * 4;
       if (VG % T != 0 && grp >= VG) break;
-      const uint8_t* src = base_of(c.v, pick(g, __builtin_amdgcn_readfirstlane(t4 >> 4))) + (t & mask) * D;
+      const uint8_t* src = base_of(vpool, pages, __builtin_amdgcn_readfirstlane(t4 >> 4)) + (t & mask) * D;
       const uint32_t at = (uint32_t)((t4 & mask) * D + (grp % (D / 4)) * 4);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) vraw[i][j] = *reinterpret_cast<const uint32_t*>(src + (at + j * D));
+      for (int j = 0; j < 4; ++j) vnext[i][j] = *reinterpret_cast<const uint32_t*>(src + (at + j * D));
     }
   };
-  // `clear`: some tokens of the step are absent or past the end, and their
-  // rows may hold anything
-  auto store_v = [&](int buf, const Pages& g, int t, bool clear) {
+  auto take = [&] {
+#pragma unroll
+    for (int i = 0; i < KP; ++i) kraw[i] = knext[i];
+#pragma unroll
+    for (int i = 0; i < VP; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) vraw[i][j] = vnext[i][j];
+  };
+  auto store_k = [&](int buf, int i) {
+    const int piece = i * T + tid;
+    v8bf f;
+    unpack4(f, 0, kraw[i].x);
+    unpack4(f, 4, kraw[i].y);
+    *reinterpret_cast<v8bf*>(&s_k[buf][k_at<D>(piece / (D / 8), piece % (D / 8))]) = f;
+  };
+  // Values of some steps: tokens that are absent or past the end become zeros
+  // (their rows may hold anything).
+  auto clear_v = [&](int pages, int t) {
+    if (t + kTok <= s.len && !any_lane(pages < 0)) return;
 #pragma unroll
     for (int i = 0; i < VP; ++i) {
-      const int grp = i * T + tid, t4 = grp / (D / 4) * 4, d0 = (grp % (D / 4)) * 4;
-      if (VG % T != 0 && grp >= VG) break;
-      if (clear) {
-        const bool there = pick(g, __builtin_amdgcn_readfirstlane(t4 >> 4)) >= 0;
+      const int t4 = (i * T + tid) / (D / 4) * 4;
+      if (VG % T != 0 && i * T + tid >= VG) break;
+      const bool there = __builtin_amdgcn_readlane(pages, __builtin_amdgcn_readfirstlane(t4 >> 4)) >= 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) vraw[i][j] = there && t + t4 + j < s.len ? vraw[i][j] : 0u;
-      }
-      uint32_t o[4];
-      transpose4(vraw[i], o);
-      // tokens 16 u + 8 a + 4 half + i sit in chunk 2 u + half at 4 a + i
-      const int chunk = 2 * (t4 / 16) + ((t4 >> 2) & 1), sub = ((t4 >> 3) & 1) * 4;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const v2bf lo = codes_to_bf16<false>(o[d]), hi = codes_to_bf16<true>(o[d]);
-        uint2 w;
-        w.x = __builtin_bit_cast(uint32_t, lo);
-        w.y = __builtin_bit_cast(uint32_t, hi);
-        *reinterpret_cast<uint2*>(&s_v[buf][v_at(d0 + d, chunk) + sub]) = w;
-      }
+      for (int j = 0; j < 4; ++j) vraw[i][j] = there && t + t4 + j < s.len ? vraw[i][j] : 0u;
     }
   };
-  struct Scales { float k[4], v[4]; };
-  auto scales_of = [&](const Pages& g) {
-    Scales x;
+  auto store_v = [&](int buf, int i) {
+    const int grp = i * T + tid, t4 = grp / (D / 4) * 4, d0 = (grp % (D / 4)) * 4;
+    if (VG % T != 0 && grp >= VG) return;
+    uint32_t o[4];
+    transpose4(vraw[i], o);
+    // tokens 16 u + 8 a + 4 half + i sit in chunk 2 u + half at 4 a + i
+    const int chunk = 2 * (t4 / 16) + ((t4 >> 2) & 1), sub = ((t4 >> 3) & 1) * 4;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t at = (int64_t)max(g.p[u], 0) * c.heads + h;
-      x.k[u] = uniform_load(c.ks + at);
-      const float v = uniform_load(c.vs + at);
-      x.v[u] = g.p[u] >= 0 ? v : 0.0f;               // its weights are 0, page 0's scale may be anything
+    for (int d = 0; d < 4; ++d) {
+      const v2bf lo = codes_to_bf16<false>(o[d]), hi = codes_to_bf16<true>(o[d]);
+      uint2 w;
+      w.x = __builtin_bit_cast(uint32_t, lo);
+      w.y = __builtin_bit_cast(uint32_t, hi);
+      *reinterpret_cast<uint2*>(&s_v[buf][v_at(d0 + d, chunk) + sub]) = w;
     }
-    return x;
   };
-  auto whole = [&](const Pages& g) { return (g.p[0] | g.p[1] | g.p[2] | g.p[3]) >= 0; };
+  // scales of a step's groups, in the lanes of their pages
+  struct Scales { float k, v; };
+  auto scales_of = [&](int pages) {
+    const int64_t at = (int64_t)max(pages, 0) * c.heads + h;
+    return Scales{c.ks[at], c.vs[at]};
+  };
+  auto lane_of = [](float x, int g) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), g));
+  };
 
-  v16f o[DT];
+  constexpr int NS = D / 32;                         // products of a 16-token group, for scores and for outputs
+  v16f o[DT], sc[2];                                 // outputs; scores: sc[u / 2][8 (u & 1) + i] is of group u
+  v8bf pf[4];                                        // weights of group u, times the value scale
 #pragma unroll
-  for (int d = 0; d < DT; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+  for (int d = 0; d < DT; ++d) o[d] = v16f{};
   float m = -INFINITY, l = 0.0f;
 
-  // a quarter of a step's scores: token tile u / 2, half of the dims
-  auto score = [&](v16f (&x)[2], int buf, int u) {
-    if ((u & 1) == 0)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[u / 2][i] = 0.0f;
-#pragma unroll
-    for (int k = (u & 1) * (KS / 2); k < ((u & 1) + 1) * (KS / 2); ++k) {
-      const v8bf kf = *reinterpret_cast<const v8bf*>(&s_k[buf][k_at<D>(32 * (u / 2) + r, 2 * k + half)]);
-      x[u / 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[k], x[u / 2], 0, 0, 0);
-    }
+  auto key = [&](int buf, int j) {                   // operand of score product j: token tile j / KS
+    return *reinterpret_cast<const v8bf*>(&s_k[buf][k_at<D>(32 * (j / KS) + r, 2 * (j % KS) + half)]);
   };
-  auto outputs = [&](const v8bf& pf, int buf, int u) {
+  auto value = [&](int buf, int j) {                 // operand of output product j: group j / NS
+    return *reinterpret_cast<const v8bf*>(&s_v[buf][v_at(32 * (j % NS) + r, 2 * (j / NS) + half)]);
+  };
+  constexpr int kAhead = 4;                          // LDS reads run this many products ahead
+  auto add_outputs = [&](int buf) {
+    v8bf ring[kAhead];
 #pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      const v8bf vf = *reinterpret_cast<const v8bf*>(&s_v[buf][v_at(32 * d + r, 2 * u + half)]);
-      o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf, o[d], 0, 0, 0);
+    for (int j = 0; j < kAhead; ++j) ring[j] = value(buf, j);
+#pragma unroll
+    for (int j = 0; j < 4 * NS; ++j) {
+      o[j % NS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[j % kAhead], pf[j / NS], o[j % NS], 0, 0, 0);
+      if (j + kAhead < 4 * NS) ring[j % kAhead] = value(buf, j + kAhead);
     }
   };
 
-  // One step: softmax of sc (step t) and the outputs it adds, beside the
-  // scores nx of step t + 1.  Buffers: keys t + 1 in PAR ^ 1, values t in PAR.
-  // g0, g1, g2: the pages of steps t, t + 1, t + 2.
-  auto step = [&](v16f (&sc)[2], v16f (&nx)[2], auto par, int t, const Pages& g0, const Pages& g1, const Pages& g2,
-                  const Scales& sl) {
-    constexpr int PAR = decltype(par)::value;
-    load_k(g2, t + 2 * kTok);
-    load_v(g1, t + kTok);
+  // Matrix phase: the scores of step t, then (not FIRST) the outputs of step
+  // t - 1, as one stream of products.  The sum so far is rescaled beside the
+  // score products, every step: the vector unit is idle there, and no branch
+  // surrounds the accumulators.  g0, g1, g2: pages of steps t, t + 1, t + 2.
+  auto matrix = [&](auto first, int t, int it, int g0, int g2, int g3) {
+    constexpr bool FIRST = decltype(first)::value != 0;
+    constexpr int ALL = FIRST ? 4 * NS : 8 * NS;
+    const int kb = it & 1, vb = kb ^ 1;              // keys t, values t - 1; keys t + 1 go to kb ^ 1, values t to kb
+    auto operand = [&](int j) { return j < 4 * NS ? key(kb, j) : value(vb, j - 4 * NS); };
+    v8bf ring[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) ring[j] = operand(j);
+    clear_v(g0, t);
+#pragma unroll
+    for (int j = 0; j < ALL; ++j) {
+      if (j < 4 * NS) {
+        const v16f zero = {};
+        sc[j / KS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[j % kAhead], qf[j % KS], j % KS ? sc[j / KS] : zero, 0, 0, 0);
+      } else {
+        const int i = j - 4 * NS;
+        o[i % NS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[j % kAhead], pf[i / NS], o[i % NS], 0, 0, 0);
+      }
+      if (j + kAhead < ALL) ring[j % kAhead] = operand(j + kAhead);
+      // the staging, a piece every few products
+      constexpr int kEvery = ALL / (KP + VP + 2);
+      if (j % kEvery == kEvery - 1) {
+        const int piece = j / kEvery;
+        if (piece < VP) store_v(kb, piece);
+        else if (piece < VP + KP) store_k(kb ^ 1, piece - VP);
+        else if (piece == VP + KP) {
+          take();
+          load_v(g2, t + 2 * kTok);
+        } else if (piece == VP + KP + 1) load_k(g3, t + 3 * kTok);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  // Softmax phase of step t.  `general`: some weights are masked, or some
+  // capped scores are past the series; those steps form their scores twice
+  // (maximum, weights), so that the common path keeps sc where the matrix core
+  // left it.
+  auto softmax = [&](int t, int g0, const Scales& sl) {
     float f[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) f[u] = sl.k[u] * fscale * (CAP ? 1.0f : kLog2e);
-    // sc[u / 2][8 (u & 1) + i] belongs to the 16 tokens of group u
-    if (CAP) {
-      // caps well above the scores need only the series (capped_small)
+    for (int u = 0; u < 4; ++u) f[u] = lane_of(sl.k * (fscale * (CAP ? 1.0f : kLog2e)), u);
+    // an absent group's weights are 0, page 0's scale may be anything
+    const float vscale = g0 >= 0 ? sl.v : 0.0f;
+    bool general = t + kTok > wave_seen || any_lane(g0 < 0);
+    if (CAP && !general) {
       float big = 0.0f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float y = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y = fmaxf(y, __builtin_fabsf(sc[u / 2][8 * (u & 1) + i]));
+        big = fmaxf(big, y * f[u]);
+      }
+      general = any_lane(!(big * inv_cap < kCapSmall));
+    }
+    auto masked = [&](int u, int i) {
+      const int at = t + 16 * u + 8 * (i / 4) + 4 * half + (i & 3);
+      float x = sc[u / 2][8 * (u & 1) + i] * f[u];
+      if (CAP) x = capped(x, a.softcap, inv_cap) * kLog2e;
+      return __builtin_amdgcn_readlane(g0, u) >= 0 && at < seen ? x : -INFINITY;
+    };
+    float top = -INFINITY;
+    if (general) {
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x = sc[u / 2][8 * (u & 1) + i] * f[u];
-          sc[u / 2][8 * (u & 1) + i] = x;
-          big = fmaxf(big, __builtin_fabsf(x));
-        }
-      if (__any(!(big * inv_cap < kCapSmall))) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) sc[u][i] = capped(sc[u][i], a.softcap, inv_cap) * kLog2e;
-      } else {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) sc[u][i] = capped_small(sc[u][i] * kLog2e, sc[u][i] * inv_cap);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) f[u] = 1.0f;
-    }
-    if (t + kTok > wave_seen || !whole(g0)) {
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, masked(u, i));
+    } else {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
+        float x = sc[u / 2][8 * (u & 1)];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int at = t + 16 * u + 8 * (i / 4) + 4 * half + (i & 3);
-          sc[u / 2][8 * (u & 1) + i] = (g0.p[u] >= 0 && at < seen) ? sc[u / 2][8 * (u & 1) + i] * f[u] : -INFINITY;
-        }
-        f[u] = 1.0f;
+        for (int i = 1; i < 8; ++i) x = fmaxf(x, sc[u / 2][8 * (u & 1) + i]);
+        top = fmaxf(top, x * f[u]);
       }
-    }
-    float top = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float x = sc[u / 2][8 * (u & 1)];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) x = fmaxf(x, sc[u / 2][8 * (u & 1) + i]);
-      top = fmaxf(top, x * f[u]);
+      if (CAP) top = capped_small(top * kLog2e, top * inv_cap);   // the cap keeps the order
     }
     top = fmaxf(top, __shfl_xor(top, 32));
     // The reference moves only when a weight would pass 2^8: the weights keep
     // their relative accuracy in BF16, and the sums theirs in FP32.
-    if (__any(top > m + 8.0f)) {
+    if (any_lane(top > m + 8.0f)) {
       const float m2 = fmaxf(m, top);
       const float alpha = __builtin_amdgcn_exp2f(m - (m2 == -INFINITY ? 0.0f : m2));
       m = m2;
@@ -299,57 +338,66 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
         for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
     }
     const float ref = m == -INFINITY ? 0.0f : m;
-    v8bf pf[4];
+    auto weigh = [&](auto how) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      score(nx, PAR ^ 1, u);
-      float sum = 0.0f;
+      for (int u = 0; u < 4; ++u) {
+        float sum = 0.0f;
+        const float vs = lane_of(vscale, u);
+        const float fl = f[u] * kLog2e, fi = f[u] * inv_cap;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u / 2][8 * (u & 1) + i], f[u], -ref));
-        sum += p;
-        pf[u][i] = (__bf16)(p * sl.v[u]);
+        for (int e = 0; e < 8; ++e) {
+          const float x = sc[u / 2][8 * (u & 1) + e];
+          float y;
+          if (decltype(how)::value) y = masked(u, e) - ref;
+          else if (CAP) y = capped_small(x * fl, x * fi) - ref;
+          else y = __builtin_fmaf(x, f[u], -ref);
+          const float p = __builtin_amdgcn_exp2f(y);
+          sum += p;
+          pf[u][e] = (__bf16)(p * vs);
+        }
+        l += sum;
+        asm volatile("" : "+v"(l));                  // the sum stays here: sunk below, it would hold every weight
       }
-      l += sum;
-      asm volatile("" : "+v"(l));                    // the sum stays here: sunk below, it would hold 32 weights
-      if (u > 0) outputs(pf[u - 1], PAR, u - 1);
-    }
-    outputs(pf[3], PAR, 3);
-    store_k(PAR);
-    store_v(PAR ^ 1, g1, t + kTok, t + 2 * kTok > s.len || !whole(g1));
-    __syncthreads();
+    };
+    if (general) weigh(Int<1>{});
+    else weigh(Int<0>{});
   };
 
   if (steps > 0) {
-    v16f sa[2], sb[2];
-    Pages g0 = lookup(begin), g1 = lookup(begin + kTok), g2 = lookup(begin + 2 * kTok);
-    Scales sl = scales_of(g0);
+    const int group = wave / (WAVES / 2);
+    int g0 = check(lookup(begin), begin), g1 = check(lookup(begin + kTok), begin + kTok);
+    int g2 = check(lookup(begin + 2 * kTok), begin + 2 * kTok), g3 = check(lookup(begin + 3 * kTok), begin + 3 * kTok);
     load_k(g0, begin);
-    load_v(g0, begin);
-    store_k(0);
-    store_v(0, g0, begin, true);
-    load_k(g1, begin + kTok);
-    store_k(1);
-    __syncthreads();
+    take();
 #pragma unroll
-    for (int u = 0; u < 4; ++u) score(sa, 0, u);
+    for (int i = 0; i < KP; ++i) store_k(0, i);
+    load_k(g1, begin + kTok);
+    load_v(g0, begin);
+    take();
+    load_v(g1, begin + kTok);
+    load_k(g2, begin + 2 * kTok);
     __syncthreads();
-    for (int t = begin;;) {
-      Pages g3 = lookup(t + 3 * kTok);
-      Scales sn = scales_of(g1);
-      step(sa, sb, Int<0>{}, t, g0, g1, g2, sl);
-      t += kTok;
-      if (t >= end) break;
-      g0 = lookup(t + 3 * kTok);
-      sl = scales_of(g2);
-      step(sb, sa, Int<1>{}, t, g1, g2, g3, sn);
-      t += kTok;
-      if (t >= end) break;
-      const Pages n1 = g3, n2 = g0;
-      g0 = g2;
-      g1 = n1;
-      g2 = n2;
+    Scales sl = scales_of(g0);
+    int raw = lookup(begin + 4 * kTok);
+    matrix(Int<1>{}, begin, 0, g0, g2, g3);
+    int t = begin;
+    for (int it = 1; it < steps; ++it, t += kTok) {
+      // one barrier a step and wave, between its group's phases
+      if (group == 1) __syncthreads();
+      softmax(t, g0, sl);
+      if (group == 0) __syncthreads();
+      g0 = g1;
+      g1 = g2;
+      g2 = g3;
+      g3 = check(raw, t + 4 * kTok);
+      sl = scales_of(g0);
+      raw = lookup(t + 5 * kTok);
+      matrix(Int<0>{}, t + kTok, it, g0, g2, g3);
     }
+    if (group == 1) __syncthreads();
+    softmax(t, g0, sl);
+    if (group == 0) __syncthreads();
+    add_outputs((steps - 1) & 1);
   }
   l += __shfl_xor(l, 32);
 

@@ -23,14 +23,17 @@ struct Seq {
   int base;   // slot of the first row (negative: more rows than cached tokens)
 };
 
+// (b is the same for the whole wave; its numbers are kept on the scalar unit.)
 __device__ __forceinline__ int cached_tokens(const CacheArgs& c, int b) {
   const int64_t room = (int64_t)c.width << c.lg_page;
-  return (int)max((int64_t)0, min((int64_t)min(c.kv_lens[b], c.max_kv), room));
+  const int n = (int)max((int64_t)0, min((int64_t)min(c.kv_lens[b], c.max_kv), room));
+  return __builtin_amdgcn_readfirstlane(n);
 }
 
 __device__ __forceinline__ Seq sequence(const CacheArgs& c, int b) {
   Seq s;
-  const int lo = c.q_offsets[b], hi = c.q_offsets[b + 1];
+  const int lo = __builtin_amdgcn_readfirstlane(c.q_offsets[b]);
+  const int hi = __builtin_amdgcn_readfirstlane(c.q_offsets[b + 1]);
   s.row0 = lo;
   const bool fits = lo >= 0 && hi >= lo && hi <= c.rows;
   s.n = fits ? min(hi - lo, c.max_new) : 0;
