@@ -10,12 +10,12 @@
 // P^T's operand layout once the 16 tokens of a step are stored in LDS in the
 // order 8 a + 4 half + i -> 8 half + 4 a + i.
 //
-// Two groups of waves, one of each on every SIMD, take turns: while one group
-// runs its matrix phase (outputs of step t - 1, scores of step t), the other
-// runs its softmax phase on the vector unit, with a barrier between phases.
-// The staging rides in the matrix phase, whose vector slots are free: keys of
-// step t + 1 and values of step t are converted and written there, the codes
-// of the next ones requested.
+// A wave alternates a matrix phase (scores of step t, outputs of step t - 1)
+// with a softmax phase on the vector unit.  Of the two waves of a SIMD one
+// meets the step's barrier before its matrix phase, the other after it, so
+// that their phases interleave.  The staging rides in the matrix phase, whose
+// vector slots are free: keys of step t + 1 and values of step t are converted
+// and written there, the codes of the next ones requested.
 #include "cache_device.h"
 
 namespace fp8bs {
@@ -126,7 +126,7 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
   const int32_t* table = c.table + (int64_t)b * c.width;
 
   // Pages of a step's four 16-token groups: lane x holds group x % 4's, or -1
-  // (absent, or past the end).  Looked up four steps ahead; group g's page
+  // (absent, or past the end).  Looked up three steps ahead; group g's page
   // reaches the scalar unit by readlane.
   const int my_group = 16 * (lane & 3);
   auto lookup = [&](int t) { return table[min(t + my_group, s.len - 1) >> c.lg_page]; };
@@ -141,15 +141,14 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
   };
 
   // Staging: an absent group reads page 0 and is masked like one past the end.
-  // Two sets of codes: the one to be stored, and the one still in flight.
-  uint2 kraw[KP], knext[KP];
-  uint32_t vraw[VP][4], vnext[VP][4];
+  uint2 kraw[KP];
+  uint32_t vraw[VP][4];
   auto load_k = [&](int pages, int t) {
 #pragma unroll
     for (int i = 0; i < KP; ++i) {
       const int piece = i * T + tid, kt = piece / (D / 8);
       const uint8_t* src = base_of(kpool, pages, __builtin_amdgcn_readfirstlane(kt >> 4)) + (t & mask) * D;
-      knext[i] = *reinterpret_cast<const uint2*>(src + (uint32_t)((kt & mask) * D + (piece % (D / 8)) * 8));
+      kraw[i] = *reinterpret_cast<const uint2*>(src + (uint32_t)((kt & mask) * D + (piece % (D / 8)) * 8));
     }
   };
   auto load_v = [&](int pages, int t) {
@@ -160,16 +159,8 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
       const uint8_t* src = base_of(vpool, pages, __builtin_amdgcn_readfirstlane(t4 >> 4)) + (t & mask) * D;
       const uint32_t at = (uint32_t)((t4 & mask) * D + (grp % (D / 4)) * 4);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) vnext[i][j] = *reinterpret_cast<const uint32_t*>(src + (at + j * D));
+      for (int j = 0; j < 4; ++j) vraw[i][j] = *reinterpret_cast<const uint32_t*>(src + (at + j * D));
     }
-  };
-  auto take = [&] {
-#pragma unroll
-    for (int i = 0; i < KP; ++i) kraw[i] = knext[i];
-#pragma unroll
-    for (int i = 0; i < VP; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) vraw[i][j] = vnext[i][j];
   };
   auto store_k = [&](int buf, int i) {
     const int piece = i * T + tid;
@@ -246,7 +237,7 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
   // t - 1, as one stream of products.  The sum so far is rescaled beside the
   // score products, every step: the vector unit is idle there, and no branch
   // surrounds the accumulators.  g0, g1, g2: pages of steps t, t + 1, t + 2.
-  auto matrix = [&](auto first, int t, int it, int g0, int g2, int g3) {
+  auto matrix = [&](auto first, int t, int it, int g0, int g1, int g2) {
     constexpr bool FIRST = decltype(first)::value != 0;
     constexpr int ALL = FIRST ? 4 * NS : 8 * NS;
     const int kb = it & 1, vb = kb ^ 1;              // keys t, values t - 1; keys t + 1 go to kb ^ 1, values t to kb
@@ -271,10 +262,8 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
         const int piece = j / kEvery;
         if (piece < VP) store_v(kb, piece);
         else if (piece < VP + KP) store_k(kb ^ 1, piece - VP);
-        else if (piece == VP + KP) {
-          take();
-          load_v(g2, t + 2 * kTok);
-        } else if (piece == VP + KP + 1) load_k(g3, t + 3 * kTok);
+        else if (piece == VP + KP) load_v(g1, t + kTok);
+        else if (piece == VP + KP + 1) load_k(g2, t + 2 * kTok);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -366,20 +355,16 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
   if (steps > 0) {
     const int group = wave / (WAVES / 2);
     int g0 = check(lookup(begin), begin), g1 = check(lookup(begin + kTok), begin + kTok);
-    int g2 = check(lookup(begin + 2 * kTok), begin + 2 * kTok), g3 = check(lookup(begin + 3 * kTok), begin + 3 * kTok);
+    int g2 = check(lookup(begin + 2 * kTok), begin + 2 * kTok);
     load_k(g0, begin);
-    take();
 #pragma unroll
     for (int i = 0; i < KP; ++i) store_k(0, i);
-    load_k(g1, begin + kTok);
     load_v(g0, begin);
-    take();
-    load_v(g1, begin + kTok);
-    load_k(g2, begin + 2 * kTok);
+    load_k(g1, begin + kTok);
     __syncthreads();
     Scales sl = scales_of(g0);
-    int raw = lookup(begin + 4 * kTok);
-    matrix(Int<1>{}, begin, 0, g0, g2, g3);
+    int raw = lookup(begin + 3 * kTok);
+    matrix(Int<1>{}, begin, 0, g0, g1, g2);
     int t = begin;
     for (int it = 1; it < steps; ++it, t += kTok) {
       // one barrier a step and wave, between its group's phases
@@ -388,11 +373,10 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
       if (group == 0) __syncthreads();
       g0 = g1;
       g1 = g2;
-      g2 = g3;
-      g3 = check(raw, t + 4 * kTok);
+      g2 = check(raw, t + 3 * kTok);
       sl = scales_of(g0);
-      raw = lookup(t + 5 * kTok);
-      matrix(Int<0>{}, t + kTok, it, g0, g2, g3);
+      raw = lookup(t + 4 * kTok);
+      matrix(Int<0>{}, t + kTok, it, g0, g1, g2);
     }
     if (group == 1) __syncthreads();
     softmax(t, g0, sl);
