@@ -97,6 +97,7 @@ __global__ __launch_bounds__(kThreads) void k_weights_rows(WeightArgs a, int til
 }
 
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRows = 64;                            // Q rows per step
 
@@ -111,7 +112,7 @@ __device__ __forceinline__ int hidden_rows(const WeightArgs& a, const Seq& s, in
 }
 
 template <int D, bool CAP>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2)))
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void k_weights_tiles(WeightArgs a, int tiles) {
   const CacheArgs& c = a.c;
   constexpr int KS = D / 16;                         // matrix steps of a score
@@ -199,7 +200,7 @@ void k_weights_tiles(WeightArgs a, int tiles) {
     const float* lbase = a.lse + (int64_t)s.row0 * a.q_heads + h * a.group;
     int ltok = (begin + tid) / a.group, lhead = begin + tid - ltok * a.group;   // threads below kRows
 
-    uint4 qraw[QP];
+    u32x4 qraw[QP];
     float lraw = 0.0f;
     int seen_at = 0;
     auto load = [&](int row0) {
@@ -207,7 +208,7 @@ void k_weights_tiles(WeightArgs a, int tiles) {
       for (int i = 0; i < QP; ++i) {
         // rows past the end read the first one and add nothing
         const uint16_t* p = row0 + (i * kThreads + tid) / CH < rows ? at[i].p : qbase;
-        qraw[i] = *reinterpret_cast<const uint4*>(p);
+        qraw[i] = *reinterpret_cast<const u32x4*>(p);
         at[i].g += dhead;
         const bool over = at[i].g >= a.group;
         at[i].g -= over ? a.group : 0;
@@ -227,7 +228,7 @@ void k_weights_tiles(WeightArgs a, int tiles) {
 #pragma unroll
       for (int i = 0; i < QP; ++i) {
         const int piece = i * kThreads + tid, row = piece / CH;
-        *reinterpret_cast<uint4*>(&s_q[buf][row * D + (((piece % CH) ^ (row & (CH - 1))) * 8)]) = qraw[i];
+        *reinterpret_cast<u32x4*>(&s_q[buf][row * D + (((piece % CH) ^ (row & (CH - 1))) * 8)]) = qraw[i];
       }
       if (tid < kRows) {
         s_lse[buf][tid] = lraw != -INFINITY ? lraw * kLog2e : INFINITY;
@@ -344,7 +345,7 @@ void weights_plan(WeightArgs& a) {
   // several workgroups per CU (the causal rule empties up to half of them),
   // each at least 512 rows long
   const int64_t base = (int64_t)a.c.batch * a.c.heads * slot_tiles(a);
-  int64_t want = base > 0 ? (4096 + base - 1) / base : 1;
+  int64_t want = base > 0 ? (2048 + base - 1) / base : 1;
   const int64_t most = (rows + 511) / 512;
   if (want > most) want = most;
   const int64_t per = (rows + want - 1) / want;
