@@ -30,13 +30,21 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(AttendArgs a, int row_
   const int split = id % a.splits;
   id /= a.splits;
   const int h = id % c.heads, b = id / c.heads;
+  const int begin = split * a.chunk;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  // Pages of this wave's steps: lane x holds that of 16-token group x % 2 of
+  // step x / 2, 32 steps at a time.  The table is read before the lengths are
+  // known (inside its row), so that one memory latency covers both.
+  const int first = begin + wave * kStep;
+  auto group_at = [&](int step) { return first + (step + lane / 2) * (kWaves * kStep) + (lane & 1) * 16; };
+  auto entry = [&](int step) { return c.table[(int64_t)b * c.width + min(group_at(step) >> c.lg_page, c.width - 1)]; };
+  int ahead = entry(0);
 
   const Seq s = sequence(c, b);
   const int rows = s.n * a.group, row0 = rt * 16;
   if (row0 >= rows) return;
-  const int begin = split * a.chunk;
   if (split > 0 && begin >= s.len) return;           // the join knows this from the length
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, r = lane & 15;
   const int last_row = min(row0 + 15, rows - 1);
   const int seen_all = a.full ? s.len : min(s.len, s.base + last_row / a.group + 1);
@@ -47,6 +55,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(AttendArgs a, int row_
   const int row = min(row0 + r, rows - 1);
   const int tok = row / a.group, hq = h * a.group + row % a.group;
   const int seen = a.full ? s.len : min(s.len, s.base + tok + 1);
+  const int all_see = a.full ? s.len : min(s.len, s.base + row0 / a.group + 1);   // slots every row sees
 
   v8bf qf[KS];
   {
@@ -61,42 +70,77 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(AttendArgs a, int row_
   for (int d = 0; d < DT; ++d) o[d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   float m = -INFINITY, l = 0.0f;
   const int64_t page_bytes = ((int64_t)D) << c.lg_page;
+  const int64_t page_stride = page_bytes * c.heads;
   const int mask = (1 << c.lg_page) - 1;
+  const uint8_t* const kpool = c.k + h * page_bytes;
+  const uint8_t* const vpool = c.v + h * page_bytes;
 
-  for (int t = begin + wave * kStep; t < end; t += kWaves * kStep) {
-    v4f x[2];
-    float vscale[2];
-    uint32_t vraw[2][4][DT / 4];
+  int pg = -1;
+  float ksc = 0.0f, vsc = 0.0f;
+  auto lookup = [&](int step) {
+    pg = group_at(step) < s.len && (uint32_t)ahead < (uint64_t)c.pages ? ahead : -1;
+    const int64_t at = (int64_t)max(pg, 0) * c.heads + h;
+    const float k = c.ks[at], v = c.vs[at];
+    ksc = k * a.scale;                               // an absent group's scores are masked
+    vsc = pg >= 0 ? v : 0.0f;
+  };
+  // Codes of one step.  An absent group reads page 0 and is masked.
+  constexpr int KD = D / 16;                         // dwords of a key per lane
+  typedef uint32_t Keys __attribute__((ext_vector_type(KD)));
+  typedef uint32_t Vals __attribute__((ext_vector_type(DT / 4)));
+  struct Raw {
+    Keys k[2];
+    Vals v[2][4];
+  };
+  const uint32_t k_off = (uint32_t)(r * D + g * (D / 4)), v_off = (uint32_t)(4 * g * D + r * DT);
+  auto load = [&](Raw& x, int step, int t) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int tt = t + 16 * i;
-      // a tile past the end reads the last cached token's page, and is masked
-      int page = page_of(c, b, min(tt, s.len - 1));
-      const bool there = page >= 0;
-      page = max(page, 0);
-      const int64_t at = (int64_t)page * c.heads + h;
-      const float f = c.ks[at] * a.scale;
-      vscale[i] = c.vs[at];
-      const uint8_t* kp = c.k + at * page_bytes + (int64_t)((tt & mask) + r) * D + g * (D / 4);
+      const int64_t page = max(__builtin_amdgcn_readlane(pg, 2 * step + i), 0);
+      const int row0 = (t + 16 * i) & mask;
+      const uint8_t* kp = kpool + page * page_stride + row0 * D;
+      const uint8_t* vp = vpool + page * page_stride + row0 * D;
+      x.k[i] = *reinterpret_cast<const Keys*>(kp + k_off);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x.v[i][j] = *reinterpret_cast<const Vals*>(vp + (v_off + j * D));
+    }
+  };
+  auto use = [&](Raw& y, int step, int t) {
+    v4f x[2];
+    float vscale[2];
+    // all tokens of the step are there and every row sees them?
+    const bool plain = t + kStep <= min(all_see, end) && __builtin_amdgcn_readlane(pg, 2 * step) >= 0 &&
+                       __builtin_amdgcn_readlane(pg, 2 * step + 1) >= 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ksc), 2 * step + i));
+      vscale[i] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, vsc), 2 * step + i));
       v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const uint2 w = *reinterpret_cast<const uint2*>(kp + 8 * k);
         v8bf kf;
-        unpack4(kf, 0, w.x);
-        unpack4(kf, 4, w.y);
+        unpack4(kf, 0, y.k[i][2 * k]);
+        unpack4(kf, 4, y.k[i][2 * k + 1]);
         acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[k], acc, 0, 0, 0);
       }
-      const uint8_t* vp = c.v + at * page_bytes + (int64_t)((tt & mask) + 4 * g) * D + r * DT;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(vp + j * D);
-        const bool in = there && tt + 4 * g + j < s.len;   // rows past the cached tokens hold anything
+        const float z = acc[j] * f;
+        x[i][j] = (CAP ? capped(z, a.softcap, inv_cap) : z) * kLog2e;
+      }
+    }
+    if (!plain) {
 #pragma unroll
-        for (int e = 0; e < DT / 4; ++e) vraw[i][j][e] = in ? p[e] : 0u;
-        float y = acc[j] * f;
-        if (CAP) y = capped(y, a.softcap, inv_cap);
-        x[i][j] = (there && tt + 4 * g + j < min(seen, end)) ? y * kLog2e : -INFINITY;
+      for (int i = 0; i < 2; ++i) {
+        const bool there = __builtin_amdgcn_readlane(pg, 2 * step + i) >= 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = t + 16 * i + 4 * g + j;
+          x[i][j] = there && at < min(seen, end) ? x[i][j] : -INFINITY;
+          const bool in = there && at < s.len;       // rows past the cached tokens hold anything
+#pragma unroll
+          for (int e = 0; e < DT / 4; ++e) y.v[i][j][e] = in ? y.v[i][j][e] : 0u;
+        }
       }
     }
     float top = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
@@ -117,14 +161,14 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(AttendArgs a, int row_
         l += p;
         // the weight meets the codes in BF16: its rounding (2^-9) is that of
         // the output
-        pf[4 * i + j] = (__bf16)(p == 0.0f ? 0.0f : p * vscale[i]);
+        pf[4 * i + j] = (__bf16)(p * vscale[i]);
       }
 #pragma unroll
     for (int e = 0; e < DT / 4; ++e) {
       uint32_t w[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t in[4] = {vraw[i][0][e], vraw[i][1][e], vraw[i][2][e], vraw[i][3][e]};
+        const uint32_t in[4] = {y.v[i][0][e], y.v[i][1][e], y.v[i][2][e], y.v[i][3][e]};
         transpose4(in, w[i]);
       }
 #pragma unroll
@@ -136,6 +180,28 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(AttendArgs a, int row_
         acc *= alpha;
         acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf, acc, 0, 0, 0);
       }
+    }
+  };
+
+  const int steps = first < end ? (end - first + kWaves * kStep - 1) / (kWaves * kStep) : 0;
+  for (int s0 = 0; s0 < steps; s0 += 32) {
+    if (s0 > 0) ahead = entry(s0);
+    lookup(s0);
+    const int n = min(32, steps - s0);
+    const int t0 = first + s0 * (kWaves * kStep);
+    // two sets of codes, the other one in flight (past the last step its codes
+    // are asked for again: no branch around the loads)
+    auto ask = [&](Raw& x, int i) {
+      i = min(i, n - 1);
+      load(x, i, t0 + i * (kWaves * kStep));
+    };
+    Raw even, odd;
+    ask(even, 0);
+    for (int i = 0; i < n; i += 2) {
+      ask(odd, i + 1);
+      use(even, i, t0 + i * (kWaves * kStep));
+      ask(even, i + 2);
+      if (i + 1 < n) use(odd, i + 1, t0 + (i + 1) * (kWaves * kStep));
     }
   }
   l += __shfl_xor(l, 16);
@@ -267,9 +333,9 @@ void attend_plan(AttendArgs& a) {
   const int64_t rows = (int64_t)a.c.max_new * a.group, pairs = (int64_t)a.c.batch * a.c.heads;
   a.tile_rows = rows <= 64 ? 16 : rows <= 1024 ? 128 : 256;
   const int unit = a.tile_rows == 16 ? kWaves * kStep : 256;
-  // workgroups that fill the GPU: four of the small ones per CU, two of 128
-  // rows, one of 256 (twice that, for an even end)
-  const int64_t target = a.tile_rows == 16 ? 1024 : a.tile_rows == 128 ? 1024 : 512;
+  // Workgroups: several times what runs at once (one of 256 rows per CU, two
+  // of 128, three to four of 16), so that unequal lengths even out.
+  const int64_t target = a.tile_rows == 256 ? 512 : a.tile_rows == 128 ? 1024 : 1536;
   const int64_t base = pairs * row_tiles(a);
   const int64_t units = ((int64_t)a.c.max_kv + unit - 1) / unit;
   int64_t want = base > 0 ? (target + base - 1) / base : 1;

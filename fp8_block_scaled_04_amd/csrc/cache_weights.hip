@@ -28,34 +28,39 @@ __global__ __launch_bounds__(kThreads) void k_weights_rows(WeightArgs a, int til
   constexpr int KS = D / 32;
   const int tile = blockIdx.x % tiles, pair = blockIdx.x / tiles;
   const int h = pair % c.heads, b = pair / c.heads;
-  const Seq s = sequence(c, b);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, r = lane & 15;
   const int64_t slot0 = (int64_t)tile * kSlots + wave * (kTiles * 16);
   if (slot0 >= a.acc_slots) return;
+  // the table entries and the old sums are asked for before the lengths are
+  // known (inside their rows): one memory latency covers all three
+  int entry[kTiles];
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i)
+    entry[i] = c.table[(int64_t)b * c.width + min(((int)slot0 + 16 * i) >> c.lg_page, c.width - 1)];
+  const int64_t mine = slot0 + lane;                 // the slot this lane writes
+  float old = 0.0f;
+  if (a.acc_in && mine < a.acc_slots) old = a.acc_in[(int64_t)pair * a.acc_slots + mine];
+  const Seq s = sequence(c, b);
   const int rows = s.n * a.group;
   const float inv_cap = 1.0f / a.softcap;
   float sum[kTiles] = {};
   bool there[kTiles] = {};
 
   if (slot0 < s.len && rows > 0) {
-    v8bf kf[kTiles][KS];
+    const int64_t page_bytes = (int64_t)D << c.lg_page;
+    uint2 raw[kTiles][KS];
     float f[kTiles];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
       const int tt = (int)slot0 + 16 * i;
-      int page = page_of(c, b, min(tt, s.len - 1));
-      there[i] = page >= 0;
-      page = max(page, 0);
+      there[i] = tt < s.len && (uint32_t)entry[i] < (uint64_t)c.pages;
+      const int page = __builtin_amdgcn_readfirstlane(there[i] ? entry[i] : 0);
       const int64_t at = (int64_t)page * c.heads + h;
-      f[i] = there[i] ? c.ks[at] * a.scale : 0.0f;
-      const uint8_t* kp = c.k + (at << c.lg_page) * D + (int64_t)((tt & ((1 << c.lg_page) - 1)) + r) * D + g * (D / 4);
+      f[i] = c.ks[at];
+      const uint8_t* kp = c.k + at * page_bytes + (int64_t)((tt & ((1 << c.lg_page) - 1)) + r) * D + g * (D / 4);
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const uint2 w = *reinterpret_cast<const uint2*>(kp + 8 * k);
-        unpack4(kf[i][k], 0, w.x);
-        unpack4(kf[i][k], 4, w.y);
-      }
+      for (int k = 0; k < KS; ++k) raw[i][k] = *reinterpret_cast<const uint2*>(kp + 8 * k);
     }
     const int qrow = min(r, rows - 1);
     const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)(s.row0 + qrow / a.group) * a.ld_q +
@@ -75,25 +80,34 @@ __global__ __launch_bounds__(kThreads) void k_weights_rows(WeightArgs a, int til
     for (int i = 0; i < kTiles; ++i) {
       v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int k = 0; k < KS; ++k) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[k], kf[i][k], x, 0, 0, 0);
+      for (int k = 0; k < KS; ++k) {
+        v8bf kf;
+        unpack4(kf, 0, raw[i][k].x);
+        unpack4(kf, 4, raw[i][k].y);
+        x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[k], kf, x, 0, 0, 0);
+      }
       const int slot = (int)slot0 + 16 * i + r;
+      const float fs = f[i] * a.scale;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float y = x[j] * f[i];
+        float y = x[j] * fs;
         if (CAP) y = capped(y, a.softcap, inv_cap);
         const float p = __builtin_amdgcn_exp2f((y - lse[j]) * kLog2e);
         sum[i] += slot < seen[j] ? p : 0.0f;
       }
     }
   }
+  // lane 16 i + r keeps tile i's slot r
+  float x = 0.0f;
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) {
-    float x = there[i] ? sum[i] : 0.0f;
-    x += __shfl_xor(x, 16);
-    x += __shfl_xor(x, 32);
-    const int64_t slot = slot0 + 16 * i + r;
-    if (g == 0 && slot < a.acc_slots) a.acc_out[(int64_t)pair * a.acc_slots + slot] = old_sum(a, s, pair, slot) + x;
+    float y = there[i] ? sum[i] : 0.0f;
+    y += __shfl_xor(y, 16);
+    y += __shfl_xor(y, 32);
+    if (g == i) x = y;
   }
+  if (mine < a.acc_slots)
+    a.acc_out[(int64_t)pair * a.acc_slots + mine] = (mine < min(s.base, s.len) ? old : 0.0f) + x;
 }
 
 typedef float v16f __attribute__((ext_vector_type(16)));
