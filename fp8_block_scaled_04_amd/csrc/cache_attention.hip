@@ -333,9 +333,10 @@ void attend_plan(AttendArgs& a) {
   const int64_t rows = (int64_t)a.c.max_new * a.group, pairs = (int64_t)a.c.batch * a.c.heads;
   a.tile_rows = rows <= 64 ? 16 : rows <= 1024 ? 128 : 256;
   const int unit = a.tile_rows == 16 ? kWaves * kStep : 256;
-  // Workgroups: several times what runs at once (one of 256 rows per CU, two
-  // of 128, three to four of 16), so that unequal lengths even out.
-  const int64_t target = a.tile_rows == 256 ? 512 : a.tile_rows == 128 ? 1024 : 1536;
+  // Workgroups: what runs at once (three of 16 rows per CU), or twice that where
+  // the causal rule leaves them unequal (one of 256 rows per CU, two
+  // of 128).
+  const int64_t target = a.tile_rows == 256 ? 512 : a.tile_rows == 128 ? 1024 : 768;
   const int64_t base = pairs * row_tiles(a);
   const int64_t units = ((int64_t)a.c.max_kv + unit - 1) / unit;
   int64_t want = base > 0 ? (target + base - 1) / base : 1;

@@ -2,10 +2,11 @@
 // (include/fp8bs_cache.h, fp8bs_cache_evict).
 //
 // k_evict_select picks the kept slots of one (sequence, head): a radix search
-// over the sums' bits, eight at a time, finds the smallest kept value and how
-// many slots of exactly that value fit; one pass in slot order then writes
-// them.  k_evict_move copies the codes, one workgroup per (destination page,
-// head, K or V).
+// over the sums' bits (11 + 11 + 10) finds the smallest kept value and how many
+// slots of exactly that value fit; ballots and a prefix over them then place
+// the kept slots in order.  The keys stay in registers where they fit.
+// k_evict_move copies the codes, one workgroup per (destination page, head, K
+// or V).
 #include "cache_device.h"
 
 namespace fp8bs {
@@ -21,33 +22,49 @@ __device__ __forceinline__ uint32_t rank_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix of a flag over the workgroup, and its total.  `scratch`
-// holds one int per wave; two barriers.
-__device__ __forceinline__ int prefix(bool flag, int* scratch, int& total) {
-  const uint64_t m = __ballot(flag);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+constexpr int kBins = 2048, kWavesSel = kSelect / 64;
+
+// Exclusive prefix over n (a multiple of 64, at most 1024) counts in LDS, and
+// their total in counts[n]; by the first wave, between two barriers.
+template <int N>
+__device__ __forceinline__ void scan_counts(int* counts) {
+  constexpr int E = N / 64;
   __syncthreads();
-  if (lane == 0) scratch[wave] = __popcll(m);
-  __syncthreads();
-  int before = 0;
-  total = 0;
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    int v[E], sum = 0;
 #pragma unroll
-  for (int w = 0; w < kSelect / 64; ++w) {
-    const int x = scratch[w];
-    before += w < wave ? x : 0;
-    total += x;
+    for (int e = 0; e < E; ++e) {
+      v[e] = counts[lane * E + e];
+      sum += v[e];
+    }
+    int up = sum;                                    // inclusive over the lanes
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) {
+      const int y = __shfl_up(up, x);
+      up += lane >= x ? y : 0;
+    }
+    int at = up - sum;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      counts[lane * E + e] = at;
+      at += v[e];
+    }
+    if (lane == 63) counts[N] = up;
   }
-  return before + __popcll(m & ((1ull << lane) - 1ull));
+  __syncthreads();
 }
 
+// NK: keys per thread that stay in registers.
+template <int NK>
 __global__ __launch_bounds__(kSelect) void k_evict_select(EvictArgs a) {
   const CacheArgs& c = a.c;
   const int h = blockIdx.x % c.heads, b = blockIdx.x / c.heads;
-  const int tid = threadIdx.x;
-  __shared__ uint32_t hist[256];
-  __shared__ int scratch[kSelect / 64];
-  __shared__ uint32_t s_digit;
-  __shared__ int s_need;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int kBlock = NK * kSelect, kCounts = NK * kWavesSel;
+  __shared__ __attribute__((aligned(16))) uint32_t hist[kBins];
+  __shared__ int counts[kCounts + 1];
+  __shared__ int s_digit, s_need, s_equal;
 
   const int len = cached_tokens(c, b);
   const int count = min(len, a.budget), recent = min(count, a.recent);
@@ -57,59 +74,139 @@ __global__ __launch_bounds__(kSelect) void k_evict_select(EvictArgs a) {
   float* acc_out = a.acc_out + ((int64_t)b * c.heads + h) * a.acc_slots;
   int32_t* kept = a.kept + ((int64_t)b * c.heads + h) * a.budget;
 
-  // smallest kept key, digit by digit; `need` becomes the slots of exactly
-  // that key to take
-  uint32_t key = 0, known = 0;
-  if (need > 0 && need < others) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kSelect) hist[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < others; i += kSelect) {
-        const uint32_t u = rank_key(acc[i]);
-        if ((u & known) == key) atomicAdd(&hist[(u >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        int left = need, d = 255;
-        while (d > 0 && (int)hist[d] < left) left -= (int)hist[d--];
-        s_digit = (uint32_t)d;
-        s_need = left;
-      }
-      __syncthreads();
-      key |= s_digit << shift;
-      known |= 255u << shift;
-      need = s_need;
-    }
-  }
-  const bool all = count - recent >= others;         // nothing is evicted
-  const bool none = count == recent;
-
-  int out = 0, equal = 0;                            // written, equal ones met so far
-  for (int i0 = 0; i0 < len; i0 += kSelect) {
-    const int i = i0 + tid;
-    bool take = i < len && (i >= others || all);
-    bool tie = false;
-    float x = 0.0f;
-    if (i < len) x = acc[i];
-    if (!all && !none && i < others) {
-      const uint32_t u = rank_key(x);
-      take = u > key;
-      tie = u == key;
-    }
-    int total;
-    const int e = prefix(tie, scratch, total);
-    if (tie && equal + e < need) take = true;
-    equal += total;
-    const int at = prefix(take, scratch, total);
-    if (take) {
-      kept[out + at] = i;
-      acc_out[out + at] = x;
-    }
-    out += total;
+  // the last ones, and what lies past the count
+  for (int i = tid; i < recent; i += kSelect) {
+    kept[need + i] = others + i;
+    acc_out[need + i] = acc[others + i];
   }
   for (int i = count + tid; i < a.budget; i += kSelect) kept[i] = -1;
   for (int64_t i = count + tid; i < a.acc_slots; i += kSelect) acc_out[i] = 0.0f;
   if (h == 0 && tid == 0) a.new_lens[b] = count;
+  if (need == 0) return;
+  if (need == others) {                              // nothing is evicted
+    for (int i = tid; i < others; i += kSelect) {
+      kept[i] = i;
+      acc_out[i] = acc[i];
+    }
+    return;
+  }
+
+  float x[NK];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      const int i = base + k * kSelect + tid;
+      x[k] = i < others ? acc[i] : 0.0f;
+    }
+  };
+  const bool resident = others <= kBlock;
+  if (resident) load(0);
+
+  // smallest kept key, digit by digit; `need` becomes the slots of exactly
+  // that key to take
+  uint32_t key = 0, known = 0;
+  int wanted = need, equal_all = 0;
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+    for (int i = tid; i < kBins; i += kSelect) hist[i] = 0;
+    __syncthreads();
+    for (int base = 0; base < others; base += kBlock) {
+      if (!resident) load(base);
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        const uint32_t u = rank_key(x[k]);
+        if (base + k * kSelect + tid < others && (u & known) == key) atomicAdd(&hist[(u >> shift) & (bins - 1)], 1u);
+      }
+    }
+    __syncthreads();
+    if (wave == 0) {
+      // lane x holds bins [32 x, 32 x + 32); counts of the larger keys come
+      // from the lanes above
+      int v[32], sum = 0;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        v[e] = (int)hist[lane * 32 + e];
+        sum += v[e];
+      }
+      int up = sum;                                  // this lane's and all above
+#pragma unroll
+      for (int y = 1; y < 64; y *= 2) {
+        const int z = __shfl_down(up, y);
+        up += lane + y < 64 ? z : 0;
+      }
+      int above = up - sum;
+      if (above < wanted && up >= wanted) {          // exactly one lane
+        bool found = false;
+#pragma unroll
+        for (int e = 31; e >= 0; --e) {
+          if (!found && above + v[e] >= wanted) {
+            found = true;
+            s_digit = lane * 32 + e;
+            s_need = wanted - above;
+            s_equal = v[e];
+          }
+          above += v[e];
+        }
+      }
+    }
+    __syncthreads();
+    key |= (uint32_t)s_digit << shift;
+    known |= (uint32_t)(bins - 1) << shift;
+    wanted = s_need;
+    equal_all = s_equal;
+    __syncthreads();
+  }
+
+  // Kept candidates, in slot order.  Equal keys: the first `wanted` of them
+  // (usually all there are, and no ranks are needed).
+  int out = 0, met = 0;
+  for (int base = 0; base < others; base += kBlock) {
+    if (!resident) load(base);
+    const int slot0 = base + tid;
+    if (wanted < equal_all) {
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        const uint64_t m = __ballot(slot0 + k * kSelect < others && rank_key(x[k]) == key);
+        if (lane == 0) counts[k * kWavesSel + wave] = __popcll(m);
+      }
+      scan_counts<kCounts>(counts);
+    }
+    uint32_t take = 0;
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      const uint32_t u = rank_key(x[k]);
+      const bool in = slot0 + k * kSelect < others, tie = in && u == key;
+      bool t = tie;
+      if (wanted < equal_all) {
+        const uint64_t m = __ballot(tie);
+        t = tie && met + counts[k * kWavesSel + wave] + __popcll(m & ((1ull << lane) - 1ull)) < wanted;
+      }
+      if (t || (in && u > key)) take |= 1u << k;
+    }
+    if (wanted < equal_all) {
+      met += counts[kCounts];
+      __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      const uint64_t m = __ballot((take >> k) & 1u);
+      if (lane == 0) counts[k * kWavesSel + wave] = __popcll(m);
+    }
+    scan_counts<kCounts>(counts);
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      const bool t = (take >> k) & 1u;
+      const uint64_t m = __ballot(t);
+      if (t) {
+        const int at = out + counts[k * kWavesSel + wave] + __popcll(m & ((1ull << lane) - 1ull));
+        kept[at] = slot0 + k * kSelect;
+        acc_out[at] = x[k];
+      }
+    }
+    out += counts[kCounts];
+    __syncthreads();
+  }
 }
 
 template <int D>
@@ -188,7 +285,11 @@ int dst_blocks(const EvictArgs& a) {
 int64_t evict_move_grid(const EvictArgs& a) { return 2 * (int64_t)a.c.batch * a.c.heads * dst_blocks(a); }
 
 hipError_t launch_cache_evict(const EvictArgs& a, hipStream_t stream) {
-  k_evict_select<<<dim3((unsigned)(a.c.batch * a.c.heads)), kSelect, 0, stream>>>(a);
+  // up to 4096 or 16384 slots stay in registers; more are read again from
+  // cache by each pass
+  const dim3 pairs((unsigned)(a.c.batch * a.c.heads));
+  if (a.c.max_kv <= 4 * kSelect) k_evict_select<4><<<pairs, kSelect, 0, stream>>>(a);
+  else k_evict_select<16><<<pairs, kSelect, 0, stream>>>(a);
   if (hipError_t e = hipGetLastError()) return e;
   const dim3 grid((unsigned)evict_move_grid(a));
   if (grid.x == 0) return hipSuccess;

@@ -446,63 +446,77 @@ def cast_to_e4m3(x: torch.Tensor) -> torch.Tensor:
 # [batch] are int32 GPU tensors.  kv_lens counts a call's own rows.
 
 
+def _on(t, name, dtype, ndim, dev):
+    """A dense tensor of this type and rank on GPU `dev` (one test on the way in
+    a serving loop takes; the reasons are found only if it fails)."""
+    if t.dtype is not dtype or t.dim() != ndim or t.get_device() != dev or not t.is_contiguous():
+        _need(t, name, dtype, ndim)
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
 def _cache_args(cache, table, kv_lens):
     k, ks, v, vs = cache
     _codes(k, "k"); _codes(v, "v")
-    _need(k, "k", None, 4)
-    _need(v, "v", None, 4)
-    _need(ks, "ks", torch.float32, 2)
-    _need(vs, "vs", torch.float32, 2)
-    _need(table, "table", torch.int32, 2)
-    _need(kv_lens, "kv_lens", torch.int32, 1)
+    dev = k.get_device()
+    _on(k, "k", k.dtype, 4, dev if dev >= 0 else 0)
+    _on(v, "v", v.dtype, 4, dev)
+    _on(ks, "ks", torch.float32, 2, dev)
+    _on(vs, "vs", torch.float32, 2, dev)
+    _on(table, "table", torch.int32, 2, dev)
+    _on(kv_lens, "kv_lens", torch.int32, 1, dev)
     pages, heads, page, dim = k.shape
-    if v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != k.shape[:2]:
+    if v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != ks.shape:
         raise ValueError("cache shapes do not match: codes [pages][heads][P][D], scales [pages][heads]")
     batch, width = table.shape
     if kv_lens.shape[0] != batch:
         raise ValueError(f"kv_lens must have {batch} entries, got {kv_lens.shape[0]}")
-    dev = k.device
-    for t, n in ((ks, "ks"), (v, "v"), (vs, "vs"), (table, "table"), (kv_lens, "kv_lens")):
-        if t.device != dev:
-            raise ValueError(f"{n} must be on {dev}")
-    c = _Cache(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), table.data_ptr(), kv_lens.data_ptr(),
-               pages, batch, width, heads, page, dim)
-    return c, dev
+    return _Cache(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), table.data_ptr(), kv_lens.data_ptr(),
+                  pages, batch, width, heads, page, dim), dev
 
 
 def _packed(t, name, heads, dim, dev):
     """BF16 rows [T][heads][dim], heads and dim dense, rows a stride apart."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{name} must be [rows][{heads if heads is not None else 'heads'}][{dim}], "
                          f"got {tuple(t.shape)}")
-    if t.shape[0] and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim)):
+    rows, n, _ = t.shape
+    if rows == 0:
+        return n * dim
+    ld, per, one = t.stride()
+    if one != 1 or (n > 1 and per != dim):
         raise ValueError(f"{name}: the heads of a row must be dense")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim
+    return ld if rows > 1 else n * dim
 
 
 def _row_offsets(q_offsets, batch, dev):
-    _need(q_offsets, "q_offsets", torch.int32, 1)
-    if q_offsets.shape[0] != batch + 1 or q_offsets.device != dev:
-        raise ValueError(f"q_offsets must have {batch + 1} entries on {dev}")
+    _on(q_offsets, "q_offsets", torch.int32, 1, dev)
+    if q_offsets.shape[0] != batch + 1:
+        raise ValueError(f"q_offsets must have {batch + 1} entries, got {q_offsets.shape[0]}")
 
 
 def _float_out(t, name, shape, dev, dtype=torch.float32):
-    _need(t, name, dtype)
-    if tuple(t.shape) != shape or t.device != dev:
-        raise ValueError(f"{name} must have shape {shape} on {dev}, got {tuple(t.shape)}")
+    _on(t, name, dtype, len(shape), dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     return t
 
 
+_stream_of = torch._C._cuda_getCurrentRawStream      # current HIP stream of a device, as an integer
+
+
 def _workspace(workspace, need, dev):
+    """(tensor that keeps it alive, address, bytes)"""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        if not need:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
-    return workspace
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def cache_append(k_new, v_new, cache, table, q_offsets, kv_lens, max_new: int, pow2: bool = False):
@@ -517,8 +531,8 @@ def cache_append(k_new, v_new, cache, table, q_offsets, kv_lens, max_new: int, p
     if v_new.shape[0] != T or ldv != ld:
         raise ValueError("k_new and v_new must have the same rows and row stride")
     _row_offsets(q_offsets, c.batch, dev)
-    _check(_cappend(c, _ptr(k_new), _ptr(v_new), ld, _ptr(q_offsets), T, max_new, SCALE_POW2 if pow2 else 0,
-                    _stream(k_new)), "cache_append")
+    _check(_cappend(c, k_new.data_ptr(), v_new.data_ptr(), ld, q_offsets.data_ptr(), T, max_new,
+                    SCALE_POW2 if pow2 else 0, _stream_of(dev)), "cache_append")
 
 
 def cache_attention_workspace_bytes(cache, table, q_heads: int, rows: int, max_new: int, max_kv: int) -> int:
@@ -553,10 +567,10 @@ def cache_attention(q, cache, table, q_offsets, kv_lens, max_new: int, max_kv: i
     lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
     need = ctypes.c_int64(0)
     _check(_cattn_ws(c, Hq, T, max_new, max_kv, ctypes.byref(need)), "cache_attention_workspace")
-    workspace = _workspace(workspace, need.value, dev)
-    _check(_cattn(c, _ptr(q), ld, Hq, _ptr(q_offsets), T, max_new, max_kv, scale, softcap, _ptr(out), code, _ptr(lse),
-                  MASK_FULL if full else 0, _ptr(workspace), workspace.numel() if workspace is not None else 0,
-                  _stream(q)), "cache_attention")
+    workspace, ws, ws_bytes = _workspace(workspace, need.value, dev)
+    _check(_cattn(c, q.data_ptr(), ld, Hq, q_offsets.data_ptr(), T, max_new, max_kv, scale, softcap, out.data_ptr(),
+                  code, lse.data_ptr() if return_lse else None, MASK_FULL if full else 0, ws, ws_bytes,
+                  _stream_of(dev)), "cache_attention")
     return (out, lse) if return_lse else out
 
 
@@ -596,10 +610,10 @@ def cache_attention_weights(q, lse, cache, table, q_offsets, kv_lens, max_new: i
         _float_out(out, "out", (c.batch, c.heads, slots), dev)
     need = ctypes.c_int64(0)
     _check(_cweights_ws(c, Hq, max_new, slots, ctypes.byref(need)), "cache_attention_weights_workspace")
-    workspace = _workspace(workspace, need.value, dev)
-    _check(_cweights(c, _ptr(q), ld, Hq, _ptr(q_offsets), T, max_new, max_kv, scale, softcap, _ptr(lse), _ptr(acc),
-                     _ptr(out), slots, MASK_FULL if full else 0, _ptr(workspace),
-                     workspace.numel() if workspace is not None else 0, _stream(q)), "cache_attention_weights")
+    workspace, ws, ws_bytes = _workspace(workspace, need.value, dev)
+    _check(_cweights(c, q.data_ptr(), ld, Hq, q_offsets.data_ptr(), T, max_new, max_kv, scale, softcap,
+                     lse.data_ptr(), acc.data_ptr() if acc is not None else None, out.data_ptr(), slots,
+                     MASK_FULL if full else 0, ws, ws_bytes, _stream_of(dev)), "cache_attention_weights")
     return out
 
 
@@ -614,14 +628,14 @@ def cache_evict(acc, cache, table, dst_table, kv_lens, max_kv: int, budget: int,
     _need(acc, "acc", torch.float32, 3)
     slots = acc.shape[2]
     _float_out(acc, "acc", (c.batch, c.heads, slots), dev)
-    _need(dst_table, "dst_table", torch.int32, 2)
-    if dst_table.shape[0] != c.batch or dst_table.device != dev:
-        raise ValueError(f"dst_table must have {c.batch} rows on {dev}")
+    _on(dst_table, "dst_table", torch.int32, 2, dev)
+    if dst_table.shape[0] != c.batch:
+        raise ValueError(f"dst_table must have {c.batch} rows, got {dst_table.shape[0]}")
     kept = torch.empty((c.batch, c.heads, budget), dtype=torch.int32, device=dev)
     lens = torch.empty((c.batch,), dtype=torch.int32, device=dev)
     acc_out = torch.empty_like(acc)
-    _check(_cevict(c, _ptr(acc), slots, _ptr(dst_table), dst_table.shape[1], max_kv, budget, recent, _ptr(kept),
-                   _ptr(lens), _ptr(acc_out), _stream(acc)), "cache_evict")
+    _check(_cevict(c, acc.data_ptr(), slots, dst_table.data_ptr(), dst_table.shape[1], max_kv, budget, recent,
+                   kept.data_ptr(), lens.data_ptr(), acc_out.data_ptr(), _stream_of(dev)), "cache_evict")
     return kept, lens, acc_out
 
 
