@@ -4,6 +4,8 @@
 // One workgroup per (sequence, touched page, head, K or V): it owns the page's
 // scale and codes of that head, so the largest value, the new scale, the older
 // codes' re-encoding and the new codes need no other workgroup.
+//
+// HBM bound: 3 bytes move per value.
 #include "cache_device.h"
 
 namespace fp8bs {
@@ -15,7 +17,11 @@ __host__ __device__ int pages_touched(int max_new, int lg_page) {
   return (int)(((int64_t)max_new + (1 << lg_page) - 2) >> lg_page) + 1;  // any alignment of the first slot
 }
 
-template <int D, bool POW2>
+// NP: 8-value pieces per thread of a whole page; the new values stay in
+// registers between the maximum and the codes.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <int D, int NP, bool POW2>
 __global__ __launch_bounds__(kThreads) void k_cache_append(AppendArgs a, int blocks) {
   const CacheArgs& c = a.c;
   constexpr int kPieces = D / 8;                     // 8-value pieces of a token
@@ -43,14 +49,19 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(AppendArgs a, int blo
                         (int64_t)(s.row0 + (lo - s.base)) * a.ld_new + (int64_t)h * D;
 
   const int items = (hi - lo) * kPieces;
+  u32x4 x[NP];
   float amax = 0.0f;
-  for (int i = threadIdx.x; i < items; i += kThreads) {
-    const uint4 x = *reinterpret_cast<const uint4*>(src + (int64_t)(i / kPieces) * a.ld_new + (i % kPieces) * 8);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int n = 0; n < NP; ++n) {
+    const int i = n * kThreads + threadIdx.x;
+    x[n] = u32x4{0u, 0u, 0u, 0u};
+    if (i < items) x[n] = *reinterpret_cast<const u32x4*>(src + (int64_t)(i / kPieces) * a.ld_new + (i % kPieces) * 8);
+  }
+#pragma unroll
+  for (int n = 0; n < NP; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      amax = fmaxf(amax, fmaxf(__builtin_fabsf(bf16_lo(w[e])), __builtin_fabsf(bf16_hi(w[e]))));
-  }
+      amax = fmaxf(amax, fmaxf(__builtin_fabsf(bf16_lo(x[n][e])), __builtin_fabsf(bf16_hi(x[n][e]))));
   __shared__ float red[kThreads / 16];
   amax = row16_max(amax);
   if (threadIdx.x % 16 == 0) red[threadIdx.x / 16] = amax;
@@ -66,16 +77,24 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(AppendArgs a, int blo
     uint32_t* row = reinterpret_cast<uint32_t*>(codes);
     for (int i = threadIdx.x; i < (lo - start) * (D / 4); i += kThreads) row[i] = reencode4(row[i], old, t);
   }
-  for (int i = threadIdx.x; i < items; i += kThreads) {
-    const uint4 x = *reinterpret_cast<const uint4*>(src + (int64_t)(i / kPieces) * a.ld_new + (i % kPieces) * 8);
+#pragma unroll
+  for (int n = 0; n < NP; ++n) {
+    const int i = n * kThreads + threadIdx.x;
+    if (i >= items) break;
     uint2 q = {0u, 0u};
     if (now > 0.0f) {
-      q.x = pack4_e4m3_sat(div_rn(bf16_lo(x.x) * t.sx, t.ss, t.r), div_rn(bf16_hi(x.x) * t.sx, t.ss, t.r),
-                           div_rn(bf16_lo(x.y) * t.sx, t.ss, t.r), div_rn(bf16_hi(x.y) * t.sx, t.ss, t.r));
-      q.y = pack4_e4m3_sat(div_rn(bf16_lo(x.z) * t.sx, t.ss, t.r), div_rn(bf16_hi(x.z) * t.sx, t.ss, t.r),
-                           div_rn(bf16_lo(x.w) * t.sx, t.ss, t.r), div_rn(bf16_hi(x.w) * t.sx, t.ss, t.r));
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // (a division also with power-of-two scales: an older scale of the
+        // page may be any number)
+        y[2 * e] = div_rn(bf16_lo(x[n][e]) * t.sx, t.ss, t.r);
+        y[2 * e + 1] = div_rn(bf16_hi(x[n][e]) * t.sx, t.ss, t.r);
+      }
+      q.x = pack4_e4m3_sat(y[0], y[1], y[2], y[3]);
+      q.y = pack4_e4m3_sat(y[4], y[5], y[6], y[7]);
     }
-    *reinterpret_cast<uint2*>(codes + (int64_t)(lo - start + i / kPieces) * D + (i % kPieces) * 8) = q;
+    *reinterpret_cast<uint2*>(codes + (int64_t)(lo - start) * D + (int64_t)i * 8) = q;
   }
 }
 
@@ -85,16 +104,33 @@ int64_t append_grid(const CacheArgs& c) {
   return 2 * (int64_t)c.batch * c.heads * pages_touched(c.max_new, c.lg_page);
 }
 
-hipError_t launch_cache_append(const AppendArgs& a, bool pow2, hipStream_t stream) {
+namespace {
+
+template <int D, int NP>
+void launch(const AppendArgs& a, bool pow2, hipStream_t stream) {
   const dim3 grid((unsigned)append_grid(a.c));
   const int blocks = pages_touched(a.c.max_new, a.c.lg_page);
-  if (a.c.dim == 128) {
-    if (pow2) k_cache_append<128, true><<<grid, kThreads, 0, stream>>>(a, blocks);
-    else k_cache_append<128, false><<<grid, kThreads, 0, stream>>>(a, blocks);
-  } else {
-    if (pow2) k_cache_append<64, true><<<grid, kThreads, 0, stream>>>(a, blocks);
-    else k_cache_append<64, false><<<grid, kThreads, 0, stream>>>(a, blocks);
-  }
+  if (pow2) k_cache_append<D, NP, true><<<grid, kThreads, 0, stream>>>(a, blocks);
+  else k_cache_append<D, NP, false><<<grid, kThreads, 0, stream>>>(a, blocks);
+}
+
+template <int D>
+void launch(const AppendArgs& a, bool pow2, hipStream_t stream) {
+  // pieces of a page: P D / 8 (at most 2048); one decoded token needs only the
+  // first
+  const int pieces = (1 << a.c.lg_page) * D / 8;
+  const int np = a.c.max_new == 1 || pieces <= kThreads ? 1 : pieces / kThreads;
+  if (np == 1) launch<D, 1>(a, pow2, stream);
+  else if (np == 2) launch<D, 2>(a, pow2, stream);
+  else if (np == 4) launch<D, 4>(a, pow2, stream);
+  else if constexpr (D == 128) launch<D, 8>(a, pow2, stream);
+}
+
+}  // namespace
+
+hipError_t launch_cache_append(const AppendArgs& a, bool pow2, hipStream_t stream) {
+  if (a.c.dim == 128) launch<128>(a, pow2, stream);
+  else launch<64>(a, pow2, stream);
   return hipGetLastError();
 }
 

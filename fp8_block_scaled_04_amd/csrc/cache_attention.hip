@@ -331,7 +331,7 @@ hipError_t launch(const AttendArgs& a, hipStream_t stream) {
 
 void attend_plan(AttendArgs& a) {
   const int64_t rows = (int64_t)a.c.max_new * a.group, pairs = (int64_t)a.c.batch * a.c.heads;
-  a.tile_rows = rows <= 64 ? 16 : rows <= 1024 ? 128 : 256;
+  a.tile_rows = rows <= 64 ? 16 : rows <= 1024 || a.c.dim == 64 ? 128 : 256;
   const int unit = a.tile_rows == 16 ? kWaves * kStep : 256;
   // Workgroups: what runs at once (three of 16 rows per CU), or twice that where
   // the causal rule leaves them unequal (one of 256 rows per CU, two

@@ -50,8 +50,15 @@ __device__ __forceinline__ int v_at(int dim, int chunk) {
   return dim * kTok + ((chunk ^ ((dim ^ (dim >> 2)) & 7)) * 8);
 }
 
+// Waves per SIMD.  D = 128: two; a wave's accumulators, queries and scores take
+// 239 of 256 registers.  D = 64 is bound by the vector unit (a score costs the
+// same there, its products half): three, as workgroups of their own, whose
+// phases drift apart (513-token chunks 273 -> 213 us).
+template <int D>
+constexpr int kPerSimd = D == 64 ? 3 : 2;
+
 template <int D, bool CAP, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(2, 2)))
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(kPerSimd<D>, kPerSimd<D>)))
 void k_attend_tiles(AttendArgs a, int row_tiles) {
   const CacheArgs& c = a.c;
   constexpr int T = 64 * WAVES, BM = 32 * WAVES;
@@ -242,6 +249,7 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
     constexpr int ALL = FIRST ? 4 * NS : 8 * NS;
     const int kb = it & 1, vb = kb ^ 1;              // keys t, values t - 1; keys t + 1 go to kb ^ 1, values t to kb
     auto operand = [&](int j) { return j < 4 * NS ? key(kb, j) : value(vb, j - 4 * NS); };
+    __builtin_amdgcn_s_setprio(1);                   // ahead of the other wave's softmax: 504 -> 464 us on long prompts
     v8bf ring[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) ring[j] = operand(j);
@@ -267,6 +275,7 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    __builtin_amdgcn_s_setprio(0);
   };
 
   // Softmax phase of step t.  `general`: some weights are masked, or some
@@ -280,17 +289,6 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
     // an absent group's weights are 0, page 0's scale may be anything
     const float vscale = g0 >= 0 ? sl.v : 0.0f;
     bool general = t + kTok > wave_seen || any_lane(g0 < 0);
-    if (CAP && !general) {
-      float big = 0.0f;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        float y = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y = fmaxf(y, __builtin_fabsf(sc[u / 2][8 * (u & 1) + i]));
-        big = fmaxf(big, y * f[u]);
-      }
-      general = any_lane(!(big * inv_cap < kCapSmall));
-    }
     auto masked = [&](int u, int i) {
       const int at = t + 16 * u + 8 * (i / 4) + 4 * half + (i & 3);
       float x = sc[u / 2][8 * (u & 1) + i] * f[u];
@@ -298,20 +296,30 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
       return __builtin_amdgcn_readlane(g0, u) >= 0 && at < seen ? x : -INFINITY;
     };
     float top = -INFINITY;
+    if (!general) {
+      float low = INFINITY;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float x = sc[u / 2][8 * (u & 1)], y = x;
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+          x = fmaxf(x, sc[u / 2][8 * (u & 1) + i]);
+          if (CAP) y = fminf(y, sc[u / 2][8 * (u & 1) + i]);
+        }
+        top = fmaxf(top, x * f[u]);
+        if (CAP) low = fminf(low, y * f[u]);
+      }
+      if (CAP) {
+        general = any_lane(!(fmaxf(top, -low) * inv_cap < kCapSmall));
+        top = capped_small(top * kLog2e, top * inv_cap);   // the cap keeps the order
+      }
+    }
     if (general) {
+      top = -INFINITY;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, masked(u, i));
-    } else {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        float x = sc[u / 2][8 * (u & 1)];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) x = fmaxf(x, sc[u / 2][8 * (u & 1) + i]);
-        top = fmaxf(top, x * f[u]);
-      }
-      if (CAP) top = capped_small(top * kLog2e, top * inv_cap);   // the cap keeps the order
     }
     top = fmaxf(top, __shfl_xor(top, 32));
     // The reference moves only when a weight would pass 2^8: the weights keep
@@ -353,7 +361,7 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
   };
 
   if (steps > 0) {
-    const int group = wave / (WAVES / 2);
+    const int group = WAVES == 8 ? wave / 4 : 0;     // the two waves of a SIMD
     int g0 = check(lookup(begin), begin), g1 = check(lookup(begin + kTok), begin + kTok);
     int g2 = check(lookup(begin + 2 * kTok), begin + 2 * kTok);
     load_k(g0, begin);
@@ -414,8 +422,13 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
 template <int D, bool CAP>
 void launch(const AttendArgs& a, int row_tiles, hipStream_t stream) {
   const dim3 grid((unsigned)((int64_t)a.c.batch * a.c.heads * row_tiles * a.splits));
-  if (a.tile_rows == 256) k_attend_tiles<D, CAP, 8><<<grid, 512, 0, stream>>>(a, row_tiles);
-  else k_attend_tiles<D, CAP, 4><<<grid, 256, 0, stream>>>(a, row_tiles);
+  if constexpr (D == 128) {
+    if (a.tile_rows == 256) {
+      k_attend_tiles<D, CAP, 8><<<grid, 512, 0, stream>>>(a, row_tiles);
+      return;
+    }
+  }
+  k_attend_tiles<D, CAP, 4><<<grid, 256, 0, stream>>>(a, row_tiles);
 }
 
 }  // namespace
