@@ -259,53 +259,43 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(AttendArgs a, int row_
   if (a.lse && d0 == 0) a.lse[at] = total == 0.0f ? -INFINITY : (top + __builtin_log2f(total)) * kLn2;
 }
 
-// Joins the splits of one (row, query head) per wave.
+// Joins the splits: D / 4 lanes per (row, query head), four dims each.
 template <int D>
 __global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a) {
   const CacheArgs& c = a.c;
-  const int64_t id = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
+  constexpr int L = D / 4, kRowsPerGroup = kThreads / L;
+  const int64_t id = (int64_t)blockIdx.x * kRowsPerGroup + threadIdx.x / L;
+  const int lane = threadIdx.x % L;
   const int hq = (int)(id % a.q_heads);
   const int64_t rest = id / a.q_heads;
   const int tok = (int)(rest % c.max_new), b = (int)(rest / c.max_new);
   if (b >= c.batch) return;
-  const Seq s = sequence(c, b);
-  if (tok >= s.n) return;
-  const int parts = max(1, min(a.splits, (s.len + a.chunk - 1) / a.chunk));
-  const int64_t at = (int64_t)(s.row0 + tok) * a.q_heads + hq, stride = c.rows * a.q_heads;
+  const int lo = c.q_offsets[b], hi = c.q_offsets[b + 1];
+  if (lo < 0 || hi < lo || hi > c.rows || tok >= hi - lo) return;
+  const int64_t room = (int64_t)c.width << c.lg_page;
+  const int len = (int)max((int64_t)0, min((int64_t)min(c.kv_lens[b], c.max_kv), room));
+  const int parts = max(1, min(a.splits, (len + a.chunk - 1) / a.chunk));
+  const int64_t at = (int64_t)(lo + tok) * a.q_heads + hq, stride = c.rows * a.q_heads;
 
-  float m = -INFINITY, l = 0.0f;                     // lane: one split (at most 64)
-  if (lane < parts) {
-    const float2 st = a.stat[lane * stride + at];
-    m = st.x;
-    l = st.y;
-  }
-  float top = m;
+  float top = -INFINITY;
+  for (int p = lane; p < parts; p += L) top = fmaxf(top, a.stat[p * stride + at].x);
 #pragma unroll
-  for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
-  const float f = __builtin_amdgcn_exp2f(m - (top == -INFINITY ? 0.0f : top));
-  float total = l * f;
-#pragma unroll
-  for (int x = 1; x < 64; x *= 2) total += __shfl_xor(total, x);
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-
-  constexpr int E = D / 64;
-  float y[E] = {};
+  for (int x = 1; x < L; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
+  const float ref = top == -INFINITY ? 0.0f : top;
+  float total = 0.0f;
+  v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
   for (int p = 0; p < parts; ++p) {
-    const float w = __shfl(f, p);
-    const float* part = a.part + (p * stride + at) * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) y[e] += w * part[e];
+    const float2 st = a.stat[p * stride + at];
+    const v4f part = *reinterpret_cast<const v4f*>(a.part + (p * stride + at) * D + 4 * lane);
+    const float w = __builtin_amdgcn_exp2f(st.x - ref);
+    total += w * st.y;
+    y += w * part;
   }
-  if (a.out_f32) {
-    float* out = static_cast<float*>(a.out) + at * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = y[e] * inv;
-  } else {
-    __bf16* out = static_cast<__bf16*>(a.out) + at * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = (__bf16)(y[e] * inv);
-  }
+  y *= total == 0.0f ? 0.0f : 1.0f / total;
+  const int64_t e = at * D + 4 * lane;
+  if (a.out_f32) *reinterpret_cast<v4f*>(static_cast<float*>(a.out) + e) = y;
+  else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + e) = make_uint2(pack2_bf16(y[0], y[1]), pack2_bf16(y[2], y[3]));
   if (a.lse && lane == 0) a.lse[at] = total == 0.0f ? -INFINITY : (top + __builtin_log2f(total)) * kLn2;
 }
 
@@ -323,7 +313,8 @@ hipError_t launch(const AttendArgs& a, hipStream_t stream) {
   if (hipError_t e = hipGetLastError()) return e;
   if (a.splits == 1) return hipSuccess;
   const int64_t rows = (int64_t)a.c.batch * a.c.max_new * a.q_heads;
-  k_attend_join<D><<<dim3((unsigned)((rows + kWaves - 1) / kWaves)), kThreads, 0, stream>>>(a);
+  constexpr int per = kThreads / (D / 4);
+  k_attend_join<D><<<dim3((unsigned)((rows + per - 1) / per)), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -331,7 +322,13 @@ hipError_t launch(const AttendArgs& a, hipStream_t stream) {
 
 void attend_plan(AttendArgs& a) {
   const int64_t rows = (int64_t)a.c.max_new * a.group, pairs = (int64_t)a.c.batch * a.c.heads;
-  a.tile_rows = rows <= 64 ? 16 : rows <= 1024 || a.c.dim == 64 ? 128 : 256;
+  // 16-row tiles read the codes once per 16 rows and bring the most workgroups;
+  // the larger ones convert them once per tile.  Measured at 4096 cached
+  // tokens, 8 heads: 64 rows of D = 128 in 86 us (16) or 63 us (128) for 16
+  // sequences, 16 or 20 us for one; 256 rows 111 (128) or 104 us (256); 128
+  // rows of D = 64 83 (16) or 64 us (128).
+  if (a.c.dim == 64) a.tile_rows = rows <= 64 ? 16 : 128;
+  else a.tile_rows = rows <= 32 || (rows <= 64 && pairs < 64) ? 16 : rows <= 128 ? 128 : 256;
   const int unit = a.tile_rows == 16 ? kWaves * kStep : 256;
   // Workgroups: what runs at once (three of 16 rows per CU), or twice that where
   // the causal rule leaves them unequal (one of 256 rows per CU, two
