@@ -152,16 +152,19 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(AttendArgs a, int row_
     const float alpha = __builtin_amdgcn_exp2f(m - ref);
     m = m2;
     l *= alpha;
-    v8bf pf;
+    // The weight meets the codes as two BF16 parts (2^-17 of it is lost): the
+    // matrix core has time to spare here, and few rows leave no other error to
+    // hide a single rounding behind.
+    v8bf pf, pl;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float p = __builtin_amdgcn_exp2f(x[i][j] - ref);
         l += p;
-        // the weight meets the codes in BF16: its rounding (2^-9) is that of
-        // the output
-        pf[4 * i + j] = (__bf16)(p * vscale[i]);
+        const float w = p * vscale[i];
+        pf[4 * i + j] = (__bf16)w;
+        pl[4 * i + j] = (__bf16)(w - (float)pf[4 * i + j]);
       }
 #pragma unroll
     for (int e = 0; e < DT / 4; ++e) {
@@ -179,6 +182,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(AttendArgs a, int row_
         v4f& acc = o[4 * e + d];
         acc *= alpha;
         acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf, acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pl, acc, 0, 0, 0);
       }
     }
   };

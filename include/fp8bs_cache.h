@@ -93,7 +93,7 @@ fp8bs_status fp8bs_cache_append(const fp8bs_cache* cache, const void* k_new, con
  *   workspace : fp8bs_cache_attention_workspace bytes (NULL if 0)
  * Requires q_heads % heads == 0, scale finite, softcap >= 0.  Scores and
  * softmax sums are FP32; the weights enter the product with the values as
- * BF16.
+ * BF16, in calls of few rows as two BF16 parts.
  */
 fp8bs_status fp8bs_cache_attention(const fp8bs_cache* cache, const void* q, int64_t ld_q, int32_t q_heads,
                                    const int32_t* q_offsets, int64_t rows, int32_t max_new, int32_t max_kv,
