@@ -296,6 +296,7 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
       return __builtin_amdgcn_readlane(g0, u) >= 0 && at < seen ? x : -INFINITY;
     };
     float top = -INFINITY;
+    bool tiny = false;                               // all capped scores are within three terms of the series
     if (!general) {
       float low = INFINITY;
 #pragma unroll
@@ -310,8 +311,10 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
         if (CAP) low = fminf(low, y * f[u]);
       }
       if (CAP) {
-        general = any_lane(!(fmaxf(top, -low) * inv_cap < kCapSmall));
-        top = capped_small(top * kLog2e, top * inv_cap);   // the cap keeps the order
+        const float big = fmaxf(top, -low) * inv_cap;
+        general = any_lane(!(big < kCapSmall));
+        tiny = !any_lane(!(big < kCapTiny));
+        top *= kLog2e * tanh_ratio<5>(top * inv_cap);      // the cap keeps the order
       }
     }
     if (general) {
@@ -345,8 +348,8 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
         for (int e = 0; e < 8; ++e) {
           const float x = sc[u / 2][8 * (u & 1) + e];
           float y;
-          if (decltype(how)::value) y = masked(u, e) - ref;
-          else if (CAP) y = capped_small(x * fl, x * fi) - ref;
+          if (decltype(how)::value == 0) y = masked(u, e) - ref;
+          else if (CAP) y = __builtin_fmaf(x * fl, tanh_ratio<decltype(how)::value>(x * fi), -ref);
           else y = __builtin_fmaf(x, f[u], -ref);
           const float p = __builtin_amdgcn_exp2f(y);
           sum += p;
@@ -356,8 +359,9 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
         asm volatile("" : "+v"(l));                  // the sum stays here: sunk below, it would hold every weight
       }
     };
-    if (general) weigh(Int<1>{});
-    else weigh(Int<0>{});
+    if (general) weigh(Int<0>{});
+    else if (CAP && !tiny) weigh(Int<5>{});
+    else weigh(Int<3>{});
   };
 
   if (steps > 0) {

@@ -95,26 +95,31 @@ __device__ __forceinline__ T uniform_load(const T* p) {
 }
 
 // cap * tanh(x / cap), y = x / cap.  For |y| < kCapSmall by the odd series of
-// tanh (its next term is under 2^-26 of the value there), so that small scores
-// keep FP32 relative accuracy; above by 1 - 2 / (e^(2y) + 1).
-// capped_small(w, y) is w * tanh(y) / y for any w proportional to x.
-constexpr float kCapSmall = 0.35f;
+// tanh, so that small scores keep FP32 relative accuracy; above by
+// 1 - 2 / (e^(2y) + 1).  tanh_ratio<TERMS>(y) is tanh(y) / y: three terms past
+// the first serve |y| < kCapTiny, five |y| < kCapSmall (the next term is under
+// 2^-26 there).
+constexpr float kCapTiny = 0.16f, kCapSmall = 0.35f;
 
-__device__ __forceinline__ float capped_small(float w, float y) {
+template <int TERMS>
+__device__ __forceinline__ float tanh_ratio(float y) {
   const float z = y * y;
-  float s = 0x1.226e355e6c23dp-7f;                   // 1382/155925
-  s = __builtin_fmaf(-s, z, 0x1.664f4882c10fap-6f);  // 62/2835
-  s = __builtin_fmaf(-s, z, 0x1.ba1ba1ba1ba1cp-5f);  // 17/315
+  float s = 0x1.ba1ba1ba1ba1cp-5f;                   // 17/315
+  if (TERMS == 5) {
+    s = 0x1.226e355e6c23dp-7f;                       // 1382/155925
+    s = __builtin_fmaf(-s, z, 0x1.664f4882c10fap-6f);  // 62/2835
+    s = __builtin_fmaf(-s, z, 0x1.ba1ba1ba1ba1cp-5f);
+  }
   s = __builtin_fmaf(-s, z, 0x1.1111111111111p-3f);  // 2/15
   s = __builtin_fmaf(-s, z, 0x1.5555555555555p-2f);  // 1/3
-  return __builtin_fmaf(-s * z, w, w);
+  return __builtin_fmaf(-s, z, 1.0f);
 }
 
 __device__ __forceinline__ float capped(float x, float cap, float inv_cap) {
   const float y = x * inv_cap;
   const float e = __builtin_amdgcn_exp2f(y * (2.0f * kLog2e));
   const float large = __builtin_fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(e + 1.0f), cap);
-  return __builtin_fabsf(y) < kCapSmall ? capped_small(x, y) : large;
+  return __builtin_fabsf(y) < kCapSmall ? x * tanh_ratio<5>(y) : large;
 }
 
 // Bytes of four tokens (a0..a3: the same four dims each) -> per dim the four
