@@ -58,8 +58,8 @@ struct WeightArgs {
   float* acc_out;
   int64_t acc_slots;
   bool full;
-  int32_t chunk, splits;     // rows per split, splits; 0: k_weights_rows
-  float* part;               // [splits][batch][heads][acc_slots] when splits > 1
+  int32_t splits;            // runs per (sequence, head); 0: k_weights_rows
+  float* part;               // [batch][heads][splits + 256-slot tiles][256] when splits > 0
 };
 
 struct EvictArgs {
@@ -82,7 +82,7 @@ int64_t evict_move_grid(const EvictArgs& a);
 void attend_plan(AttendArgs& a);
 int64_t attend_workspace_bytes(const AttendArgs& a);
 int64_t attend_grid(const AttendArgs& a);
-// The same for the weights: chunk and splits, and the partial sums.
+// The same for the weights: splits, and the partial sums.
 void weights_plan(WeightArgs& a);
 int64_t weights_workspace_bytes(const WeightArgs& a);
 int64_t weights_grid(const WeightArgs& a);

@@ -126,7 +126,7 @@ fp8bs_status fp8bs_cache_attention_weights(const fp8bs_cache* cache, const void*
   if (!sizes_fit(c, rows, max_new, max_kv) || !query_sizes_fit(c, ld_q, q_heads, max_new)) return FP8BS_ERR_SHAPE;
   if (acc_slots < max_kv || acc_slots > kMaxCount) return FP8BS_ERR_SHAPE;
   fp8bs::WeightArgs a{args(c, q_offsets, rows, max_new, max_kv), q, ld_q, q_heads, q_heads / c.heads, scale, softcap,
-                      lse, acc_in, acc_out, acc_slots, (flags & FP8BS_MASK_FULL) != 0, 0, 0, nullptr};
+                      lse, acc_in, acc_out, acc_slots, (flags & FP8BS_MASK_FULL) != 0, 0, nullptr};
   weights_plan(a);
   const int64_t need = weights_workspace_bytes(a);
   if (weights_grid(a) > kMaxCount || workspace_bytes < need) return FP8BS_ERR_SHAPE;

@@ -8,8 +8,10 @@
 // k_weights_rows (at most 16 rows, decoding): every key is read once and used
 // once, 16x16x32 products.  k_weights_tiles (more rows): 32x32x16 products, 64
 // tokens per wave with their keys in registers, Q walked through LDS 64 rows
-// at a time; the rows may be split over workgroups, whose partial sums
-// k_weights_join adds in order.
+// at a time.  Under the causal rule the first slots are seen by every row and
+// the last ones by few, so the work of a (sequence, head) is cut into equal
+// runs of (256-slot tile, 64-row step) pairs, one run per workgroup; the
+// partial sums meet in k_weights_join, in order.
 #include "cache_device.h"
 
 namespace fp8bs {
@@ -120,9 +122,35 @@ struct Int {
   static constexpr int value = N;
 };
 
-// Rows of the sequence before the first that sees any of the slots from slot0.
-__device__ __forceinline__ int hidden_rows(const WeightArgs& a, const Seq& s, int64_t slot0) {
-  return a.full ? 0 : (int)min((int64_t)s.n, max((int64_t)0, slot0 - s.base)) * a.group;
+// Steps of tile t: 64 rows each, from the step of the first row that sees any of
+// its slots.
+struct Steps {
+  int first, count;                                  // first row (a multiple of 64), steps
+};
+__device__ __forceinline__ Steps tile_steps(const WeightArgs& a, const Seq& s, int t) {
+  const int rows = s.n * a.group;
+  const int hidden = a.full ? 0 : min(s.n, max(0, t * kSlots - s.base)) * a.group;
+  Steps x;
+  x.first = hidden & ~(kRows - 1);
+  x.count = (rows - x.first + kRows - 1) / kRows;    // (rows >= hidden)
+  return x;
+}
+
+__device__ __forceinline__ int live_tiles(const Seq& s) { return (s.len + kSlots - 1) / kSlots; }
+
+__device__ __forceinline__ int64_t all_steps(const WeightArgs& a, const Seq& s) {
+  int64_t n = 0;
+  for (int t = 0; t < live_tiles(s); ++t) n += tile_steps(a, s, t).count;
+  return n;
+}
+
+// Run r of `all` steps cut into a.splits runs begins here.
+__device__ __forceinline__ int64_t run_begin(const WeightArgs& a, int64_t all, int r) { return all * r / a.splits; }
+
+// Where run r leaves its sums of tile t: r + t differs between any two of the
+// (run, tile) pairs of one (sequence, head) that share work.
+__device__ __forceinline__ float* partial(const WeightArgs& a, int tiles, int64_t pair, int r, int t) {
+  return a.part + ((pair * (a.splits + tiles)) + r + t) * kSlots;
 }
 
 template <int D, bool CAP>
@@ -136,40 +164,42 @@ void k_weights_tiles(WeightArgs a, int tiles) {
   __shared__ __attribute__((aligned(16))) float s_lse[2][kRows];     // log2 units; +inf: the row adds nothing
   __shared__ __attribute__((aligned(16))) int s_seen[2][kRows];
 
-  // (sequence, head) pairs go round the XCDs; a pair's first slots, which the
-  // most rows see, start first
+  // (sequence, head) pairs go round the XCDs, so that a pair's queries stay in
+  // one L2
   const int pairs = c.batch * c.heads;
-  int pair, tile, split;
+  int pair, run;
   {
     int id = blockIdx.x;
-    const int per = tiles * a.splits, full = pairs & ~7;
-    if (id < full * per) {
-      pair = (id / (8 * per)) * 8 + id % 8;
-      id = (id / 8) % per;
+    const int full = pairs & ~7;
+    if (id < full * a.splits) {
+      pair = (id / (8 * a.splits)) * 8 + id % 8;
+      run = (id / 8) % a.splits;
     } else {
-      id -= full * per;
+      id -= full * a.splits;
       const int left = pairs - full;
       pair = full + id % left;
-      id /= left;
+      run = id / left;
     }
-    split = id % a.splits;
-    tile = id / a.splits;
   }
   const int h = pair % c.heads, b = pair / c.heads;
   const Seq s = sequence(c, b);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, r = lane & 31;
   const int rows = s.n * a.group;
-  const int64_t wg0 = (int64_t)tile * kSlots, slot0 = wg0 + wave * 64;
-  const int begin = max(split * a.chunk, hidden_rows(a, s, wg0) & ~(kRows - 1));
-  const int end = wg0 < s.len ? min(rows, (split + 1) * a.chunk) : 0;
-  if (a.splits > 1 && begin >= end) return;          // the join knows
   const float fscale = a.scale * (CAP ? 1.0f : kLog2e);
   const float inv_cap = 1.0f / a.softcap;
-  float sum[2] = {0.0f, 0.0f};
-  bool there[2] = {false, false};
+  const int64_t all = all_steps(a, s), from = run_begin(a, all, run), to = run_begin(a, all, run + 1);
 
-  if (begin < end) {                                 // uniform over the workgroup
+  int64_t before = 0;                                // steps of the tiles so far
+  for (int tile = 0; tile < live_tiles(s) && before < to; ++tile) {
+    const Steps ts = tile_steps(a, s, tile);
+    const int64_t lo = max(from - before, (int64_t)0), hi = min(to - before, (int64_t)ts.count);
+    before += ts.count;
+    if (lo >= hi) continue;
+    const int begin = ts.first + (int)lo * kRows, end = min(rows, ts.first + (int)hi * kRows);
+    const int64_t slot0 = (int64_t)tile * kSlots + wave * 64;
+    float sum[2] = {0.0f, 0.0f};
+    bool there[2] = {false, false};
     // this lane's keys: token slot0 + 32 u + r, dims D / 2 x half + 8 k ..
     v8bf kf[2][KS];
     float f[2];
@@ -304,75 +334,76 @@ void k_weights_tiles(WeightArgs a, int tiles) {
       if (more) store(buf ^ 1);
       __syncthreads();
     }
-  }
+    float* part = partial(a, tiles, pair, run, tile) + wave * 64;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    float x = there[u] ? sum[u] : 0.0f;
-    x += __shfl_xor(x, 32);
-    const int64_t slot = slot0 + 32 * u + r;
-    if (half != 0 || slot >= a.acc_slots) continue;
-    if (a.splits > 1) a.part[((int64_t)split * pairs + pair) * a.acc_slots + slot] = x;
-    else a.acc_out[(int64_t)pair * a.acc_slots + slot] = old_sum(a, s, pair, slot) + x;
+    for (int u = 0; u < 2; ++u) {
+      float x = there[u] ? sum[u] : 0.0f;
+      x += __shfl_xor(x, 32);
+      if (half == 0) part[32 * u + r] = x;
+    }
   }
 }
 
-__global__ __launch_bounds__(kThreads) void k_weights_join(WeightArgs a) {
+// One workgroup per (sequence, head, tile): every slot of acc_out is written.
+__global__ __launch_bounds__(kSlots) void k_weights_join(WeightArgs a, int tiles) {
   const CacheArgs& c = a.c;
-  const int pairs = c.batch * c.heads;
-  const int64_t per = (a.acc_slots + kThreads - 1) / kThreads;
-  const int pair = (int)(blockIdx.x / per);
-  const int64_t slot = (blockIdx.x % per) * kThreads + threadIdx.x;
-  if (slot >= a.acc_slots) return;
-  const Seq s = sequence(c, pair / c.heads);
-  const int64_t wg0 = slot & ~(int64_t)(kSlots - 1);
-  const int rows = wg0 < s.len ? s.n * a.group : 0, first = hidden_rows(a, s, wg0) & ~(kRows - 1);
-  float x = old_sum(a, s, pair, slot);
-  for (int p = first / a.chunk; p < a.splits && p * a.chunk < rows; ++p)
-    x += a.part[((int64_t)p * pairs + pair) * a.acc_slots + slot];
-  a.acc_out[(int64_t)pair * a.acc_slots + slot] = x;
+  const int64_t pair = blockIdx.x / tiles;
+  const int tile = blockIdx.x % tiles;
+  const int64_t slot = (int64_t)tile * kSlots + threadIdx.x;
+  const Seq s = sequence(c, (int)(pair / c.heads));
+  float x = 0.0f;
+  if (slot < a.acc_slots) x = old_sum(a, s, pair, slot);
+  if (tile < live_tiles(s) && s.n > 0) {
+    int64_t before = 0;
+    for (int t = 0; t < tile; ++t) before += tile_steps(a, s, t).count;
+    const int64_t all = all_steps(a, s), after = before + tile_steps(a, s, tile).count;
+    int run = (int)(before * a.splits / all);        // its end is past `before`, or the next one's is
+    while (run > 0 && run_begin(a, all, run) > before) --run;
+    for (; run < a.splits && run_begin(a, all, run) < after; ++run)
+      if (max(run_begin(a, all, run), before) < min(run_begin(a, all, run + 1), after))
+        x += partial(a, tiles, pair, run, tile)[threadIdx.x];
+  }
+  if (slot < a.acc_slots) a.acc_out[pair * a.acc_slots + slot] = x;
 }
 
 int slot_tiles(const WeightArgs& a) { return (int)((a.acc_slots + kSlots - 1) / kSlots); }
 
 template <int D, bool CAP>
 hipError_t launch(const WeightArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)weights_grid(a));
+  const int64_t pairs = (int64_t)a.c.batch * a.c.heads;
+  const dim3 tiles((unsigned)(pairs * slot_tiles(a)));
   if (a.splits == 0) {
-    k_weights_rows<D, CAP><<<grid, kThreads, 0, stream>>>(a, slot_tiles(a));
+    k_weights_rows<D, CAP><<<tiles, kThreads, 0, stream>>>(a, slot_tiles(a));
     return hipGetLastError();
   }
-  k_weights_tiles<D, CAP><<<grid, kThreads, 0, stream>>>(a, slot_tiles(a));
+  k_weights_tiles<D, CAP><<<dim3((unsigned)(pairs * a.splits)), kThreads, 0, stream>>>(a, slot_tiles(a));
   if (hipError_t e = hipGetLastError()) return e;
-  if (a.splits == 1) return hipSuccess;
-  const int64_t per = (a.acc_slots + kThreads - 1) / kThreads;
-  k_weights_join<<<dim3((unsigned)((int64_t)a.c.batch * a.c.heads * per)), kThreads, 0, stream>>>(a);
+  k_weights_join<<<tiles, kSlots, 0, stream>>>(a, slot_tiles(a));
   return hipGetLastError();
 }
 
 }  // namespace
 
 void weights_plan(WeightArgs& a) {
-  const int64_t rows = (int64_t)a.c.max_new * a.group;
+  const int64_t rows = (int64_t)a.c.max_new * a.group, pairs = (int64_t)a.c.batch * a.c.heads;
   a.splits = 0;
-  a.chunk = 0;
   if (rows <= 16) return;
-  // several workgroups per CU (the causal rule empties up to half of them),
-  // each at least 512 rows long
-  const int64_t base = (int64_t)a.c.batch * a.c.heads * slot_tiles(a);
-  int64_t want = base > 0 ? (2048 + base - 1) / base : 1;
-  const int64_t most = (rows + 511) / 512;
+  // What runs at once (two workgroups per CU) for one sequence, whose runs are
+  // all alike; twice that for several, whose lengths differ.  At least eight
+  // steps a run.
+  int64_t want = pairs > 0 ? ((a.c.batch == 1 ? 512 : 1024) + pairs - 1) / pairs : 1;
+  const int64_t most = (int64_t)slot_tiles(a) * ((rows + kRows - 1) / kRows) / 8;
   if (want > most) want = most;
-  const int64_t per = (rows + want - 1) / want;
-  a.chunk = (int32_t)((per + kRows - 1) / kRows * kRows);
-  a.splits = (int32_t)((rows + a.chunk - 1) / a.chunk);
+  a.splits = want < 1 ? 1 : (int32_t)want;
 }
 
 int64_t weights_workspace_bytes(const WeightArgs& a) {
-  return a.splits > 1 ? (int64_t)a.splits * a.c.batch * a.c.heads * a.acc_slots * 4 : 0;
+  return a.splits > 0 ? (int64_t)a.c.batch * a.c.heads * (a.splits + slot_tiles(a)) * kSlots * 4 : 0;
 }
 
 int64_t weights_grid(const WeightArgs& a) {
-  return (int64_t)a.c.batch * a.c.heads * slot_tiles(a) * (a.splits > 1 ? a.splits : 1);
+  const int64_t tiles = slot_tiles(a);               // also the join's
+  return (int64_t)a.c.batch * a.c.heads * (a.splits > tiles ? a.splits : tiles);
 }
 
 hipError_t launch_cache_weights(const WeightArgs& a, hipStream_t stream) {

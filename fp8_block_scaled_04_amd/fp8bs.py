@@ -575,8 +575,8 @@ def cache_attention(q, cache, table, q_offsets, kv_lens, max_new: int, max_kv: i
 
 
 def cache_attention_weights_workspace_bytes(cache, table, q_heads: int, max_new: int, slots: int) -> int:
-    """Workspace bytes of cache_attention_weights for these sizes (0: it would
-    not split the rows)."""
+    """Workspace bytes of cache_attention_weights for these sizes (0 for few
+    rows)."""
     pages, heads, page, dim = cache[0].shape
     c = _Cache(None, None, None, None, None, None, pages, table.shape[0], table.shape[1], heads, page, dim)
     out = ctypes.c_int64(0)

@@ -98,7 +98,7 @@ def check_attention(w, out, lse, scale, cap, full, what):
     if lse is not None:
         z = lse.cpu().numpy().astype(np.float64)
         assert np.array_equal(np.isneginf(z), none), f"{what}: lse of empty rows"
-        assert (np.abs(z - ref_lse)[~none] <= e + 2.0 ** -21 * np.abs(ref_lse[~none])).all(), f"{what}: lse"
+        assert (np.abs(z[~none] - ref_lse[~none]) <= e + 2.0 ** -21 * np.abs(ref_lse[~none])).all(), f"{what}: lse"
     return ref_lse
 
 
@@ -181,6 +181,17 @@ def test_attention_many_rows_behind_a_prefix(G, D):
         check_attention(w, out, lse, D ** -0.5, cap, False, f"many rows G={G} D={D}")
 
 
+def test_attention_long_splits():
+    # a bound far above the lengths makes splits of more than 32 steps a wave
+    # (pages and scales are looked up 32 steps at a time)
+    w = cache_util.make([6000, 4300, 5121], [1, 2, 1], 2, 2, 64, 16, seed=8, table_extra=0)
+    d = cache_util.dev(w)
+    out, lse = fp8bs.cache_attention(d["q"], cache_dev(d), d["table"], d["q_offsets"], d["kv_lens"], 2, 400000, 0.125,
+                                     return_lse=True)
+    torch.cuda.synchronize()
+    check_attention(w, out, lse, 0.125, 0.0, False, "long splits")
+
+
 def test_attention_large_scores_and_strided_queries():
     # scores in the hundreds (the running maximum moves late), negative scale,
     # queries as a slice of a wider projection, a bound far above the lengths
@@ -248,6 +259,59 @@ def test_attention_weights(lens, H, G, D, P):
                                               slots=slots)
         ref0 = oracle.weights(w["q"], lse, cache_util.cache_of(w), *args, None, slots, cap, full)
         assert (np.abs(out_host_f64(fresh) - ref0) <= e * ref0 + 1e-30).all(), what
+
+
+@pytest.mark.parametrize("G,D", [(1, 128), (4, 64), (6, 128)])
+def test_attention_weights_many_rows(G, D):
+    # rows split over workgroups, slots that no early row sees, steps whose first
+    # rows see only some of a wave's tokens
+    w = cache_util.make([1500, 777, 600], [1100, 500, 600], 1, G, D, 64, seed=G + D)
+    d = cache_util.dev(w)
+    scale = D ** -0.5
+    for cap, full in ((0.0, False), (4.0, False), (0.0, True)):
+        print(f"weights many rows G={G} D={D} cap={cap} full={full}", flush=True)
+        args = (w["table"], w["q_offsets"], w["kv_lens"], scale)
+        _, lse = oracle.attention(w["q"], cache_util.cache_of(w), *args, cap, full)
+        lse = lse.astype(np.float32)
+        ref = oracle.weights(w["q"], lse, cache_util.cache_of(w), *args, None, 1600, cap, full)
+        assert fp8bs.cache_attention_weights_workspace_bytes(cache_dev(d), d["table"], G, 1100, 1600) > 0
+        out = fp8bs.cache_attention_weights(d["q"], f32_dev(lse), cache_dev(d), d["table"], d["q_offsets"],
+                                            d["kv_lens"], 1100, 1500, scale, softcap=cap, full=full, slots=1600)
+        torch.cuda.synchronize()
+        # FP32 sums of up to 1100 G weights: 2^-24 of the running sum a step
+        e = 2 * score_error(w, scale, cap) + 2.0 ** -19 + 2.0 ** -24 * 1100 * G / 2
+        err = np.abs(out_host_f64(out) - ref)
+        assert (err <= e * ref + 1e-30).all(), f"worst {np.max(err / (e * ref + 1e-30)):.3g}"
+
+
+@pytest.mark.parametrize("kv,budget,recent", [([5000, 9000], 3000, 100), ([20000, 17000, 40], 6000, 0),
+                                              ([16384, 16385, 4096], 4096, 4000)])
+def test_evict_long(kv, budget, recent):
+    # sums that stay in registers in one or several blocks, and ones that are
+    # read again by each pass; many ties
+    H, D, P = 1, 64, 128
+    w = cache_util.make(kv, [0] * len(kv), H, 1, D, P, seed=1, spare=sum(-(-min(t, budget) // P) for t in kv) + 3)
+    used = set(w["table"][w["table"] >= 0].tolist())
+    free = [p for p in range(w["k"].shape[0]) if p not in used]
+    dst = np.full((len(kv), -(-budget // P)), -1, np.int32)
+    for b, t in enumerate(kv):
+        n = -(-min(t, budget) // P)
+        dst[b, :n], free = free[:n], free[n:]
+    rng = np.random.default_rng(7)
+    for kind in ("spread", "ties"):
+        print(f"evict long {kind} kv={kv}", flush=True)
+        acc = np.exp(3 * rng.standard_normal((len(kv), H, max(kv)))).astype(np.float32)
+        if kind == "ties":
+            acc = np.floor(acc).astype(np.float32)
+        wk = {n: (v.copy() if isinstance(v, np.ndarray) else v) for n, v in w.items()}
+        d = cache_util.dev(wk)
+        kept, lens, out = fp8bs.cache_evict(f32_dev(acc), cache_dev(d), d["table"], torch.from_numpy(dst).cuda(),
+                                            d["kv_lens"], max(kv), budget, recent)
+        torch.cuda.synchronize()
+        rk, rl, ra = oracle.evict(acc, cache_util.cache_of(wk), w["table"], dst, w["kv_lens"], budget, recent)
+        assert np.array_equal(kept.cpu().numpy(), rk) and np.array_equal(lens.cpu().numpy(), rl)
+        assert np.array_equal(f32_bits_host(out), ra.view(np.uint32))
+        same_cache(d, wk, "evict long")
 
 
 @pytest.mark.parametrize("H,D,P", [(1, 64, 16), (2, 128, 32), (3, 64, 64), (2, 128, 128)])
