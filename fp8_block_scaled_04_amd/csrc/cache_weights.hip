@@ -279,17 +279,26 @@ void k_weights_tiles(WeightArgs a, int tiles) {
         s_seen[buf][tid] = seen_at;
       }
     };
-    auto score = [&](v16f (&x)[2], int buf, int t) {
+    // Scores of the step's two 32-row tiles, as one stream of products; LDS
+    // reads run kAhead operands (two products each) ahead.
+    constexpr int kAhead = 4;
+    auto scores = [&](v16f (&x0)[2], v16f (&x1)[2], int buf) {
+      auto operand = [&](int j) {
+        const int row = 32 * (j / KS) + r, chunk = half * KS + j % KS;
+        return *reinterpret_cast<const v8bf*>(&s_q[buf][row * D + ((chunk ^ (row & (CH - 1))) * 8)]);
+      };
+      v8bf ring[kAhead];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int j = 0; j < kAhead; ++j) ring[j] = operand(j);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[u][i] = 0.0f;
+      for (int j = 0; j < 2 * KS; ++j) {
+        v16f(&x)[2] = j < KS ? x0 : x1;
+        const v16f zero = {};
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const int row = 32 * t + r, chunk = half * KS + k;
-        const v8bf qf = *reinterpret_cast<const v8bf*>(&s_q[buf][row * D + ((chunk ^ (row & (CH - 1))) * 8)]);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) x[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf, kf[u][k], x[u], 0, 0, 0);
+        for (int u = 0; u < 2; ++u)
+          x[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[j % kAhead], kf[u][j % KS], j % KS ? x[u] : zero, 0, 0, 0);
+        if (j + kAhead < 2 * KS) ring[j % kAhead] = operand(j + kAhead);
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
     // x[u][4 j + i] is row 32 t + 8 j + 4 half + i
@@ -316,8 +325,7 @@ void k_weights_tiles(WeightArgs a, int tiles) {
     };
     auto step = [&](int buf, auto masked) {
       v16f x0[2], x1[2];
-      score(x0, buf, 0);
-      score(x1, buf, 1);
+      scores(x0, x1, buf);
       add(x0, buf, 0, masked);
       add(x1, buf, 1, masked);
     };
