@@ -288,7 +288,11 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
     for (int u = 0; u < 4; ++u) f[u] = lane_of(sl.k * (fscale * (CAP ? 1.0f : kLog2e)), u);
     // an absent group's weights are 0, page 0's scale may be anything
     const float vscale = g0 >= 0 ? sl.v : 0.0f;
-    bool general = t + kTok > wave_seen || any_lane(g0 < 0);
+    // The common path takes the value scale into the exponent and out of the sum
+    // again, once per group instead of once per weight; scales near the ends of
+    // the FP32 range (zero among them) go the general way.
+    const float vlog = __builtin_amdgcn_logf(vscale), vinv = __builtin_amdgcn_rcpf(vscale);
+    bool general = t + kTok > wave_seen || any_lane(!(vscale >= 0x1p-60f && vscale <= 0x1p60f));
     auto masked = [&](int u, int i) {
       const int at = t + 16 * u + 8 * (i / 4) + 4 * half + (i & 3);
       float x = sc[u / 2][8 * (u & 1) + i] * f[u];
@@ -341,21 +345,23 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
     auto weigh = [&](auto how) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
+        constexpr bool kGeneral = decltype(how)::value == 0;
         float sum = 0.0f;
-        const float vs = lane_of(vscale, u);
+        const float vs = lane_of(kGeneral ? vscale : vinv, u);
+        const float to = kGeneral ? ref : ref - lane_of(vlog, u);
         const float fl = f[u] * kLog2e, fi = f[u] * inv_cap;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float x = sc[u / 2][8 * (u & 1) + e];
           float y;
-          if (decltype(how)::value == 0) y = masked(u, e) - ref;
-          else if (CAP) y = __builtin_fmaf(x * fl, tanh_ratio<decltype(how)::value>(x * fi), -ref);
-          else y = __builtin_fmaf(x, f[u], -ref);
+          if (kGeneral) y = masked(u, e) - to;
+          else if (CAP) y = __builtin_fmaf(x * fl, tanh_ratio<decltype(how)::value>(x * fi), -to);
+          else y = __builtin_fmaf(x, f[u], -to);
           const float p = __builtin_amdgcn_exp2f(y);
           sum += p;
-          pf[u][e] = (__bf16)(p * vs);
+          pf[u][e] = (__bf16)(kGeneral ? p * vs : p);
         }
-        l += sum;
+        l = kGeneral ? l + sum : __builtin_fmaf(sum, vs, l);
         asm volatile("" : "+v"(l));                  // the sum stays here: sunk below, it would hold every weight
       }
     };

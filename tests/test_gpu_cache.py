@@ -207,6 +207,26 @@ def test_attention_large_scores_and_strided_queries():
         check_attention(w, out, lse, scale, 0.0, False, f"large scores {scale}")
 
 
+@pytest.mark.parametrize("D,new", [(128, 140), (64, 140), (128, 20), (64, 1)])
+def test_attention_extreme_value_scales(D, new):
+    # pages of zeros (scale 0), and scales near both ends of the FP32 range,
+    # beside ordinary ones; every sequence has one kind, the last a mix
+    w = cache_util.make([200, 333, 150, 400], [new, new, new, new], 1, 2, D, 32, seed=D + new)
+    sizes = [0.0, 2.0 ** -120, 2.0 ** 100]
+    for b in range(4):
+        for j, page in enumerate(w["table"][b][:-(-int(w["kv_lens"][b]) // 32)]):
+            size = sizes[b] if b < 3 else sizes[:2][j % 2] if j % 3 else 1.0
+            w["vs"][page] = size
+            if size == 0.0:
+                w["v"][page][w["v"][page] != 0x7F] = 0
+    d = cache_util.dev(w)
+    for cap in (0.0, 9.0):
+        out, lse = fp8bs.cache_attention(d["q"], cache_dev(d), d["table"], d["q_offsets"], d["kv_lens"], new, 400,
+                                         D ** -0.5, softcap=cap, return_lse=True)
+        torch.cuda.synchronize()
+        check_attention(w, out, lse, D ** -0.5, cap, False, f"extreme scales D={D} new={new} cap={cap}")
+
+
 def test_attention_absent_pages_and_all_absent_rows():
     # tokens of a table entry outside the pool do not exist; a sequence with
     # only such tokens has empty rows
