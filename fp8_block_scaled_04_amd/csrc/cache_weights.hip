@@ -302,7 +302,8 @@ void k_weights_tiles(WeightArgs a, int tiles) {
       }
     };
     // x[u][4 j + i] is row 32 t + 8 j + 4 half + i
-    auto add = [&](const v16f (&x)[2], int buf, int t, auto masked) {
+    // SERIES (capped scores): every one is within the series of tanh.
+    auto add_tile = [&](const v16f (&x)[2], int buf, int t, auto masked, auto series) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int row = 32 * t + 8 * j + 4 * half;
@@ -314,7 +315,8 @@ void k_weights_tiles(WeightArgs a, int tiles) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float y = x[u][4 * j + i];
-            if (CAP) y = __builtin_fmaf(capped(y * f[u], a.softcap, inv_cap), kLog2e, -lse[i]);
+            if (CAP && decltype(series)::value) y = __builtin_fmaf(y * (f[u] * kLog2e), tanh_ratio<5>(y * (f[u] * inv_cap)), -lse[i]);
+            else if (CAP) y = __builtin_fmaf(capped(y * f[u], a.softcap, inv_cap), kLog2e, -lse[i]);
             else y = __builtin_fmaf(y, f[u], -lse[i]);
             float p = __builtin_amdgcn_exp2f(y);
             if (decltype(masked)::value) p = mine[u] < (i == 0 ? seen.x : i == 1 ? seen.y : i == 2 ? seen.z : seen.w) ? p : 0.0f;
@@ -322,6 +324,22 @@ void k_weights_tiles(WeightArgs a, int tiles) {
           }
       }
       asm volatile("" : "+v"(sum[0]), "+v"(sum[1]));  // sums are taken here: sunk below, they would hold every score
+    };
+    auto add = [&](const v16f (&x)[2], int buf, int t, auto masked) {
+      bool small = false;
+      if (CAP) {
+        float big = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float y = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y = fmaxf(y, __builtin_fabsf(x[u][i]));
+          big = fmaxf(big, y * __builtin_fabsf(f[u]));
+        }
+        small = __builtin_amdgcn_ballot_w64(!(big * inv_cap < kCapSmall)) == 0;
+      }
+      if (small) add_tile(x, buf, t, masked, Int<1>{});
+      else add_tile(x, buf, t, masked, Int<0>{});
     };
     auto step = [&](int buf, auto masked) {
       v16f x0[2], x1[2];
