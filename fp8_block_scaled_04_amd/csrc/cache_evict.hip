@@ -102,12 +102,12 @@ __global__ __launch_bounds__(kSelect) void k_evict_select(EvictArgs a) {
   const bool resident = others <= kBlock;
   if (resident) load(0);
 
-  // smallest kept key, digit by digit; `need` becomes the slots of exactly
-  // that key to take
+  // Smallest kept key, digit by digit: `wanted` of the `equal_all` keys that
+  // agree with it in the known digits are kept, and all larger ones.  Done as
+  // soon as all of them are (two digits usually tell real sums apart).
   uint32_t key = 0, known = 0;
   int wanted = need, equal_all = 0;
-#pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
+  for (int pass = 0; pass < 3 && wanted != equal_all; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
     for (int i = tid; i < kBins; i += kSelect) hist[i] = 0;
     __syncthreads();
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(kSelect) void k_evict_select(EvictArgs a) {
   }
 
   // Kept candidates, in slot order.  Equal keys: the first `wanted` of them
-  // (usually all there are, and no ranks are needed).
+  // (unless those are all there are, and no ranks are needed).
   int out = 0, met = 0;
   for (int base = 0; base < others; base += kBlock) {
     if (!resident) load(base);
@@ -167,7 +167,7 @@ __global__ __launch_bounds__(kSelect) void k_evict_select(EvictArgs a) {
     if (wanted < equal_all) {
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
-        const uint64_t m = __ballot(slot0 + k * kSelect < others && rank_key(x[k]) == key);
+        const uint64_t m = __ballot(slot0 + k * kSelect < others && (rank_key(x[k]) & known) == key);
         if (lane == 0) counts[k * kWavesSel + wave] = __popcll(m);
       }
       scan_counts<kCounts>(counts);
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(kSelect) void k_evict_select(EvictArgs a) {
     uint32_t take = 0;
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
-      const uint32_t u = rank_key(x[k]);
+      const uint32_t u = rank_key(x[k]) & known;
       const bool in = slot0 + k * kSelect < others, tie = in && u == key;
       bool t = tie;
       if (wanted < equal_all) {
