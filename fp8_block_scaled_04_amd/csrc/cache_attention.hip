@@ -11,6 +11,12 @@
 // core's result layout of S^T (lane = row, four consecutive tokens per lane)
 // is then its operand layout of P^T, if the 32 tokens of a step are numbered
 // 16 x tile + 4 x lane group + i, and no value moves between lanes.
+//
+// HBM bound: 2 D bytes of codes per cached token and head against 4 D flops
+// per row.  Two waves' worth of steps in flight per wave and three workgroups
+// per CU keep the reads coming: 446 MB of a 48-sequence step in 101 us, 444 MB
+// of two 131,000-token contexts in 89 us (4.4 and 5.0 TB/s; a plain read of
+// that size reaches 5.5).  Splits are joined by a kernel of its own (5 us).
 #include "cache_device.h"
 
 namespace fp8bs {
@@ -24,7 +30,8 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(AttendArgs a, int row_
   const CacheArgs& c = a.c;
   constexpr int DT = D / 16;                         // dims per lane of V, output tiles
   constexpr int KS = D / 32;                         // matrix steps of a score
-  int id = blockIdx.x;
+  // several row tiles of a split run on one XCD, whose L2 then holds its codes
+  int id = row_tiles > 1 ? xcd_remap(blockIdx.x, gridDim.x) : blockIdx.x;
   const int rt = id % row_tiles;
   id /= row_tiles;
   const int split = id % a.splits;
@@ -330,8 +337,12 @@ void attend_plan(AttendArgs& a) {
   // the larger ones convert them once per tile.  Measured at 4096 cached
   // tokens, 8 heads: 64 rows of D = 128 in 86 us (16) or 63 us (128) for 16
   // sequences, 16 or 20 us for one; 256 rows 111 (128) or 104 us (256); 128
-  // rows of D = 64 83 (16) or 64 us (128).
-  if (a.c.dim == 64) a.tile_rows = rows <= 64 ? 16 : 128;
+  // rows of D = 64 83 (16) or 64 us (128).  Few rows in all stay on 16-row
+  // tiles, which round the weights to 2^-17: over a thousand (row, head) pairs
+  // the single BF16 rounding of the larger ones averages out to that of the
+  // output, over a few dozen it may not (1.55 times the error of exact weights).
+  if (a.c.rows * a.q_heads <= 1024) a.tile_rows = 16;
+  else if (a.c.dim == 64) a.tile_rows = rows <= 64 ? 16 : 128;
   else a.tile_rows = rows <= 32 || (rows <= 64 && pairs < 64) ? 16 : rows <= 128 ? 128 : 256;
   const int unit = a.tile_rows == 16 ? kWaves * kStep : 256;
   // Workgroups: what runs at once (three of 16 rows per CU), or twice that where
