@@ -5,7 +5,10 @@
 // scale and codes of that head, so the largest value, the new scale, the older
 // codes' re-encoding and the new codes need no other workgroup.
 //
-// HBM bound: 3 bytes move per value.
+// HBM bound: 3 bytes move per value.  The 13,600 new tokens of six prompts (8
+// heads of 128, pages of 128) take 18.4 us a call, 87 MB at 4.7 TB/s; a plain
+// copy moves 5.0.  (Reading the new values a second time instead of holding
+// them: 24 us.)
 #include "cache_device.h"
 
 namespace fp8bs {

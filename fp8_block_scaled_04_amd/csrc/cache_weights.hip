@@ -12,6 +12,13 @@
 // the last ones by few, so the work of a (sequence, head) is cut into equal
 // runs of (256-slot tile, 64-row step) pairs, one run per workgroup; the
 // partial sums meet in k_weights_join, in order.
+//
+// k_weights_rows is HBM bound (D bytes of codes per cached token and head): 165
+// MB of a 32-sequence step in 43 us, 3.8 TB/s; its workgroups live for one
+// round of loads, whose latency the table entries and old sums no longer add
+// to (56 us before).  k_weights_tiles takes the matrix core 2 D flops and the
+// vector unit a multiply-add, an exponential and an addition per pair: 67
+// GFLOP of a 3500-token prompt in 96 us with the join, 700 TFLOP/s.
 #include "cache_device.h"
 
 namespace fp8bs {
