@@ -3,14 +3,15 @@
 //
 // k_evict_select picks the kept slots of one (sequence, head): a radix search
 // over the sums' bits (11 + 11 + 10) finds the smallest kept value and how many
-// slots of exactly that value fit; ballots and a prefix over them then place
-// the kept slots in order.  The keys stay in registers where they fit.
+// slots of exactly that value fit; ballots then place the kept slots in order, in
+// LDS first, so that they are written (and their sums read) side by side.  The
+// keys stay in registers where they fit.
 // k_evict_move copies the codes, one workgroup per (destination page, head, K
 // or V).
 //
 // The move is HBM bound: 16 sequences cut to 4096 tokens (8 heads of 128) in 59
-// us, 262 MB at 4.4 TB/s; the search before it takes 20 us of latency (barriers
-// of 16 waves, three rounds of LDS counts).
+// us, 262 MB at 4.4 TB/s; the search before it takes 18 us of latency (its reads
+// 2, each counted digit 3, ranks 4, what it writes 6), 7.5 us for 3 short ones.
 #include "cache_device.h"
 
 namespace fp8bs {
@@ -21,42 +22,16 @@ constexpr int kSelect = 1024, kMove = 256;
 // Order-preserving map of a float to an unsigned key: larger value, larger
 // key; -0 equals +0; NaN below every number.
 __device__ __forceinline__ uint32_t rank_key(float x) {
-  if (x != x) return 0u;
   const uint32_t u = __builtin_bit_cast(uint32_t, x + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t key = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return x != x ? 0u : key;
 }
 
 constexpr int kBins = 2048, kWavesSel = kSelect / 64;
 
-// Exclusive prefix over n (a multiple of 64, at most 1024) counts in LDS, and
-// their total in counts[n]; by the first wave, between two barriers.
-template <int N>
-__device__ __forceinline__ void scan_counts(int* counts) {
-  constexpr int E = N / 64;
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
-    int v[E], sum = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      v[e] = counts[lane * E + e];
-      sum += v[e];
-    }
-    int up = sum;                                    // inclusive over the lanes
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) {
-      const int y = __shfl_up(up, x);
-      up += lane >= x ? y : 0;
-    }
-    int at = up - sum;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      counts[lane * E + e] = at;
-      at += v[e];
-    }
-    if (lane == 63) counts[N] = up;
-  }
-  __syncthreads();
+// Lanes below this one that are set in m.
+__device__ __forceinline__ int lanes_below(uint64_t m) {
+  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
 }
 
 // NK: keys per thread that stay in registers.
@@ -64,44 +39,43 @@ template <int NK>
 __global__ __launch_bounds__(kSelect) void k_evict_select(EvictArgs a) {
   const CacheArgs& c = a.c;
   const int h = blockIdx.x % c.heads, b = blockIdx.x / c.heads;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  constexpr int kBlock = NK * kSelect, kCounts = NK * kWavesSel;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr int kBlock = NK * kSelect;
   __shared__ __attribute__((aligned(16))) uint32_t hist[kBins];
-  __shared__ int counts[kCounts + 1];
+  __shared__ uint16_t picked[kBlock];                // kept slots of a block of keys, in order
+  __shared__ int s_wave[kWavesSel], s_ties[kWavesSel];
   __shared__ int s_digit, s_need, s_equal;
 
   const int len = cached_tokens(c, b);
   const int count = min(len, a.budget), recent = min(count, a.recent);
   const int others = len - recent;                   // candidates: slots [0, others)
-  int need = count - recent;                         // of which this many stay
+  const int need = count - recent;                   // of which this many stay
   const float* acc = a.acc + ((int64_t)b * c.heads + h) * a.acc_slots;
   float* acc_out = a.acc_out + ((int64_t)b * c.heads + h) * a.acc_slots;
   int32_t* kept = a.kept + ((int64_t)b * c.heads + h) * a.budget;
 
-  // the last ones, and what lies past the count
-  for (int i = tid; i < recent; i += kSelect) {
-    kept[need + i] = others + i;
-    acc_out[need + i] = acc[others + i];
-  }
+  // what lies past the count, here where the reads of the keys hide it
   for (int i = count + tid; i < a.budget; i += kSelect) kept[i] = -1;
   for (int64_t i = count + tid; i < a.acc_slots; i += kSelect) acc_out[i] = 0.0f;
   if (h == 0 && tid == 0) a.new_lens[b] = count;
-  if (need == 0) return;
-  if (need == others) {                              // nothing is evicted
-    for (int i = tid; i < others; i += kSelect) {
-      kept[i] = i;
-      acc_out[i] = acc[i];
+  if (need == 0 || need == others) {                 // the last ones, or nothing is evicted
+    for (int i = tid; i < count; i += kSelect) {
+      kept[i] = len - count + i;
+      acc_out[i] = acc[len - count + i];
     }
     return;
   }
 
-  float x[NK];
+  // A wave holds a run of slots, 64 per key: counts inside it stay in the scalar
+  // unit, and slot order is (wave, key, lane).
+  const int run = wave * (NK * 64) + lane;
+  uint32_t u[NK];
   auto load = [&](int base) {
+    float x[NK];                                     // all reads first, past the end the last one
 #pragma unroll
-    for (int k = 0; k < NK; ++k) {
-      const int i = base + k * kSelect + tid;
-      x[k] = i < others ? acc[i] : 0.0f;
-    }
+    for (int k = 0; k < NK; ++k) x[k] = acc[min(base + run + 64 * k, others - 1)];
+#pragma unroll
+    for (int k = 0; k < NK; ++k) u[k] = rank_key(x[k]);
   };
   const bool resident = others <= kBlock;
   if (resident) load(0);
@@ -117,49 +91,37 @@ __global__ __launch_bounds__(kSelect) void k_evict_select(EvictArgs a) {
     __syncthreads();
     for (int base = 0; base < others; base += kBlock) {
       if (!resident) load(base);
+      const int left = others - base - run;
 #pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        const uint32_t u = rank_key(x[k]);
-        if (base + k * kSelect + tid < others && (u & known) == key) atomicAdd(&hist[(u >> shift) & (bins - 1)], 1u);
-      }
+      for (int k = 0; k < NK; ++k)
+        if (left > 64 * k && (u[k] & known) == key) atomicAdd(&hist[(u[k] >> shift) & (bins - 1)], 1u);
     }
     __syncthreads();
-    if (wave == 0) {
-      // lane x holds bins [32 x, 32 x + 32); counts of the larger keys come
-      // from the lanes above
-      int v[32], sum = 0;
+    // a thread holds two bins; counts of the larger keys come from the lanes and
+    // waves above
+    const int v0 = (int)hist[2 * tid], v1 = (int)hist[2 * tid + 1];
+    int up = v0 + v1;                                // its own and all above
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        v[e] = (int)hist[lane * 32 + e];
-        sum += v[e];
-      }
-      int up = sum;                                  // this lane's and all above
+    for (int y = 1; y < 64; y *= 2) {
+      const int z = __shfl_down(up, y);
+      up += lane + y < 64 ? z : 0;
+    }
+    if (lane == 0) s_wave[wave] = up;
+    __syncthreads();
 #pragma unroll
-      for (int y = 1; y < 64; y *= 2) {
-        const int z = __shfl_down(up, y);
-        up += lane + y < 64 ? z : 0;
-      }
-      int above = up - sum;
-      if (above < wanted && up >= wanted) {          // exactly one lane
-        bool found = false;
-#pragma unroll
-        for (int e = 31; e >= 0; --e) {
-          if (!found && above + v[e] >= wanted) {
-            found = true;
-            s_digit = lane * 32 + e;
-            s_need = wanted - above;
-            s_equal = v[e];
-          }
-          above += v[e];
-        }
-      }
+    for (int w = 1; w < kWavesSel; ++w) up += w > wave ? s_wave[w] : 0;
+    const int above = up - v0 - v1;
+    if (above < wanted && up >= wanted) {            // exactly one thread
+      const bool high = above + v1 >= wanted;
+      s_digit = 2 * tid + high;
+      s_need = wanted - above - (high ? 0 : v1);
+      s_equal = high ? v1 : v0;
     }
     __syncthreads();
     key |= (uint32_t)s_digit << shift;
     known |= (uint32_t)(bins - 1) << shift;
     wanted = s_need;
     equal_all = s_equal;
-    __syncthreads();
   }
 
   // Kept candidates, in slot order.  Equal keys: the first `wanted` of them
@@ -167,49 +129,71 @@ __global__ __launch_bounds__(kSelect) void k_evict_select(EvictArgs a) {
   int out = 0, met = 0;
   for (int base = 0; base < others; base += kBlock) {
     if (!resident) load(base);
-    const int slot0 = base + tid;
+    const int left = others - base - run;
+    uint64_t take[NK];
     if (wanted < equal_all) {
+      int ties = 0;
+#pragma unroll
+      for (int k = 0; k < NK; ++k) ties += __popcll(__ballot(left > 64 * k && (u[k] & known) == key));
+      if (lane == 0) s_ties[wave] = ties;
+      __syncthreads();
+      int rank = met;
+#pragma unroll
+      for (int w = 0; w < kWavesSel; ++w) {
+        rank += w < wave ? s_ties[w] : 0;
+        met += s_ties[w];
+      }
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
-        const uint64_t m = __ballot(slot0 + k * kSelect < others && (rank_key(x[k]) & known) == key);
-        if (lane == 0) counts[k * kWavesSel + wave] = __popcll(m);
-      }
-      scan_counts<kCounts>(counts);
-    }
-    uint32_t take = 0;
-#pragma unroll
-    for (int k = 0; k < NK; ++k) {
-      const uint32_t u = rank_key(x[k]) & known;
-      const bool in = slot0 + k * kSelect < others, tie = in && u == key;
-      bool t = tie;
-      if (wanted < equal_all) {
+        const uint32_t x = u[k] & known;
+        const bool in = left > 64 * k, tie = in && x == key;
         const uint64_t m = __ballot(tie);
-        t = tie && met + counts[k * kWavesSel + wave] + __popcll(m & ((1ull << lane) - 1ull)) < wanted;
+        take[k] = __ballot((in && x > key) || (tie && rank + lanes_below(m) < wanted));
+        rank += __popcll(m);
       }
-      if (t || (in && u > key)) take |= 1u << k;
-    }
-    if (wanted < equal_all) {
-      met += counts[kCounts];
-      __syncthreads();
-    }
+    } else {
 #pragma unroll
-    for (int k = 0; k < NK; ++k) {
-      const uint64_t m = __ballot((take >> k) & 1u);
-      if (lane == 0) counts[k * kWavesSel + wave] = __popcll(m);
+      for (int k = 0; k < NK; ++k) take[k] = __ballot(left > 64 * k && (u[k] & known) >= key);
     }
-    scan_counts<kCounts>(counts);
+    int mine = 0;
 #pragma unroll
-    for (int k = 0; k < NK; ++k) {
-      const bool t = (take >> k) & 1u;
-      const uint64_t m = __ballot(t);
-      if (t) {
-        const int at = out + counts[k * kWavesSel + wave] + __popcll(m & ((1ull << lane) - 1ull));
-        kept[at] = slot0 + k * kSelect;
-        acc_out[at] = x[k];
-      }
-    }
-    out += counts[kCounts];
+    for (int k = 0; k < NK; ++k) mine += __popcll(take[k]);
+    if (lane == 0) s_wave[wave] = mine;
     __syncthreads();
+    int at = 0, n = 0;
+#pragma unroll
+    for (int w = 0; w < kWavesSel; ++w) {
+      at += w < wave ? s_wave[w] : 0;
+      n += s_wave[w];
+    }
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      if ((take[k] >> lane) & 1u) picked[at + lanes_below(take[k])] = (uint16_t)(run + 64 * k);
+      at += __popcll(take[k]);
+    }
+    __syncthreads();
+    // the last block's are followed by the recent ones; four reads in flight
+    const int all = n + (base + kBlock >= others ? recent : 0);
+    for (int i = tid; i < all; i += 4 * kSelect) {
+      int slot[4];
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int from = min(i + e * kSelect, all - 1);
+        slot[e] = from < n ? base + picked[from] : others + from - n;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = acc[slot[e]];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int to = i + e * kSelect;
+        if (to < all) {
+          kept[out + to] = slot[e];
+          acc_out[out + to] = x[e];
+        }
+      }
+    }
+    out += n;
   }
 }
 
