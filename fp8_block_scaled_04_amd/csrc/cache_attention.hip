@@ -337,13 +337,17 @@ void attend_plan(AttendArgs& a) {
   // the larger ones convert them once per tile.  Measured at 4096 cached
   // tokens, 8 heads: 64 rows of D = 128 in 86 us (16) or 63 us (128) for 16
   // sequences, 16 or 20 us for one; 256 rows 111 (128) or 104 us (256); 128
-  // rows of D = 64 83 (16) or 64 us (128).  Few rows in all over a short
-  // cache stay on 16-row tiles, which fill the chip sooner (1024 (row, head)
-  // pairs of D = 128: 6 against 12 us at 128 cached tokens, 23 and 23 at 4096, 63
-  // and 40 at 32768) and round the weights to 2^-17: over more pairs the single
-  // BF16 rounding of the larger ones averages out to that of the output, over a
-  // few dozen tokens it may not (1.55 times the error of exact weights).
-  if (a.c.rows * a.q_heads <= 1024 && a.c.max_kv <= 8192) a.tile_rows = 16;
+  // rows of D = 64 83 (16) or 64 us (128).
+  // Little work in all stays on 16-row tiles, which fill the chip sooner and
+  // round the weights to 2^-17 (the larger ones' single BF16 rounding averages
+  // out to that of the output over many rows, over a few dozen tokens it may
+  // not: 1.55 times the error of exact weights).  16 against larger, (row, head)
+  // pairs / cached tokens, D = 128: 4096/128 in 6 or 13 us, 4096/1024 20 or 24,
+  // 8192/256 20 or 17, 1024/32768 63 or 40; D = 64: 16384/512 11 or 20,
+  // 8192/4096 37 or 44, 32768/1024 25 or 42, 65536/128 21 or 13, 1024/131072 125
+  // or 93.
+  const int64_t all = a.c.rows * a.q_heads, few = a.c.dim == 64 ? 1 << 15 : 1 << 12;
+  if (all <= few && all * a.c.max_kv <= few * (a.c.dim == 64 ? 1024 : 2048)) a.tile_rows = 16;
   else if (a.c.dim == 64) a.tile_rows = rows <= 64 ? 16 : 128;
   else a.tile_rows = rows <= 32 || (rows <= 64 && pairs < 64) ? 16 : rows <= 128 ? 128 : 256;
   const int unit = a.tile_rows == 16 ? kWaves * kStep : 256;

@@ -181,6 +181,49 @@ def test_attention_many_rows_behind_a_prefix(G, D):
         check_attention(w, out, lse, D ** -0.5, cap, False, f"many rows G={G} D={D}")
 
 
+BOUND = 1 << 16                                      # of cached tokens: with it few rows go to the larger row tiles
+
+
+@pytest.mark.parametrize("lens", ["ragged", "overrun", "prompt"])
+@pytest.mark.parametrize("H,G,D,P", SHAPES)
+def test_attention_on_larger_row_tiles(lens, H, G, D, P):
+    kv, new = LENS[lens]
+    w = cache_util.make(kv, new, H, G, D, P, seed=H + G + D + 1)
+    d = cache_util.dev(w)
+    for cap, full, max_new in ((0.0, False, 130), (3.0, False, 257), (0.0, True, 129)):
+        what = f"larger tiles {lens} H={H} G={G} D={D} P={P} cap={cap} full={full}"
+        print(what, flush=True)
+        out, lse = fp8bs.cache_attention(d["q"], cache_dev(d), d["table"], d["q_offsets"], d["kv_lens"], max_new, BOUND,
+                                         D ** -0.5, softcap=cap, full=full, out_dtype=torch.float32, return_lse=True)
+        torch.cuda.synchronize()
+        check_attention(w, out, lse, D ** -0.5, cap, full, what)
+
+
+@pytest.mark.parametrize("D,bound", [(64, 6000), (128, 6000), (128, 1400), (64, 700)])
+def test_attention_larger_row_tiles_in_splits(D, bound):
+    # 6016 (row, head) pairs: several splits hold tokens, others none
+    w = cache_util.make([700, 513, 260, 129], [150, 64, 33, 129], 1, 16, D, 64, seed=bound)
+    d = cache_util.dev(w)
+    for cap in (0.0, 20.0):
+        print(f"larger tiles in splits D={D} bound={bound} cap={cap}", flush=True)
+        out, lse = fp8bs.cache_attention(d["q"], cache_dev(d), d["table"], d["q_offsets"], d["kv_lens"], 150, bound,
+                                         D ** -0.5, softcap=cap, return_lse=True)
+        torch.cuda.synchronize()
+        check_attention(w, out, lse, D ** -0.5, cap, False, f"larger tiles in splits D={D} bound={bound}")
+
+
+@pytest.mark.parametrize("kv,new,G", [([250, 200], [250, 200], 40), ([640, 300], [520, 300], 24)])
+def test_attention_many_pairs(kv, new, G):
+    # more (row, head) pairs than 16-row tiles take at D = 64, in one split and in three
+    w = cache_util.make(kv, new, 2, G, 64, 64, seed=G)
+    d = cache_util.dev(w)
+    print(f"many pairs G={G}", flush=True)
+    out, lse = fp8bs.cache_attention(d["q"], cache_dev(d), d["table"], d["q_offsets"], d["kv_lens"], max(new), max(kv),
+                                     0.125, return_lse=True)
+    torch.cuda.synchronize()
+    check_attention(w, out, lse, 0.125, 0.0, False, f"many pairs G={G}")
+
+
 def test_attention_long_splits():
     # a bound far above the lengths makes splits of more than 32 steps a wave
     # (pages and scales are looked up 32 steps at a time)
@@ -225,6 +268,26 @@ def test_attention_extreme_value_scales(D, new):
                                          D ** -0.5, softcap=cap, return_lse=True)
         torch.cuda.synchronize()
         check_attention(w, out, lse, D ** -0.5, cap, False, f"extreme scales D={D} new={new} cap={cap}")
+
+
+@pytest.mark.parametrize("D,new", [(128, 140), (64, 140), (128, 40)])
+def test_attention_extreme_value_scales_on_larger_row_tiles(D, new):
+    # pages of zeros (scale 0), and scales near both ends of the FP32 range,
+    # beside ordinary ones; every sequence has one kind, the last a mix
+    w = cache_util.make([200, 333, 150, 400], [new, new, new, new], 1, 2, D, 32, seed=D + new)
+    sizes = [0.0, 2.0 ** -120, 2.0 ** 100]
+    for b in range(4):
+        for j, page in enumerate(w["table"][b][:-(-int(w["kv_lens"][b]) // 32)]):
+            size = sizes[b] if b < 3 else sizes[:2][j % 2] if j % 3 else 1.0
+            w["vs"][page] = size
+            if size == 0.0:
+                w["v"][page][w["v"][page] != 0x7F] = 0
+    d = cache_util.dev(w)
+    for cap in (0.0, 9.0):
+        out, lse = fp8bs.cache_attention(d["q"], cache_dev(d), d["table"], d["q_offsets"], d["kv_lens"], new, BOUND,
+                                         D ** -0.5, softcap=cap, return_lse=True)
+        torch.cuda.synchronize()
+        check_attention(w, out, lse, D ** -0.5, cap, False, f"extreme scales, larger tiles D={D} new={new} cap={cap}")
 
 
 def test_attention_absent_pages_and_all_absent_rows():
