@@ -36,9 +36,9 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(AppendArgs a, int blo
   const int j = id % blocks, b = id / blocks;
 
   const Seq s = sequence(c, b);
-  if (s.n == 0) return;
   const int first = max(s.base, 0);
-  const int end = min(s.base + s.n, s.len);          // new slots [first, end)
+  const int end = min(s.base + s.n, s.len);          // new slots [first, end); past the table there are none
+  if (first >= end) return;
   const int blk = (first >> c.lg_page) + j;
   const int P = 1 << c.lg_page, start = blk << c.lg_page;
   const int lo = max(first, start), hi = min(end, start + P);

@@ -13,14 +13,15 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// One sequence of a call.  Lengths come from device memory: they are clamped
+// One sequence of a call.  Lengths come from device memory: `len` is clamped
 // to what the launch and the table cover, so no value of them reads or writes
-// out of range.
+// out of range.  `base` is not: rows keep their slots whatever is left out, and
+// every use of it takes the smaller of it and len.
 struct Seq {
   int row0;   // first packed row
   int n;      // rows processed (at most max_new, all inside [0, rows))
-  int len;    // cached tokens
-  int base;   // slot of the first row (negative: more rows than cached tokens)
+  int len;    // cached tokens within the bounds
+  int base;   // slot of the first row (negative: more rows than cached tokens; may pass len)
 };
 
 // (b is the same for the whole wave; its numbers are kept on the scalar unit.)
@@ -38,7 +39,8 @@ __device__ __forceinline__ Seq sequence(const CacheArgs& c, int b) {
   const bool fits = lo >= 0 && hi >= lo && hi <= c.rows;
   s.n = fits ? min(hi - lo, c.max_new) : 0;
   s.len = cached_tokens(c, b);
-  s.base = s.len - (fits ? hi - lo : 0);
+  const int all = __builtin_amdgcn_readfirstlane(c.kv_lens[b]);
+  s.base = min(max(all, 0) - (fits ? hi - lo : 0), 1 << 30);   // (no slot lies past 2^30)
   return s;
 }
 

@@ -24,7 +24,8 @@
  * are its last tokens: row i of n is slot kv_lens[b] - n + i.  max_new is a
  * host-side upper bound of the rows of one sequence, max_kv of kv_lens; they
  * size the launch.  A sequence's rows past max_new and cached tokens past
- * max_kv are left out.
+ * max_kv or past its table_width * P slots are left out, as if they were not
+ * there: nothing is read or written for them, and the others keep their slots.
  *
  * Checks.  Sizes (FP8BS_ERR_SHAPE): batch, rows, max_new, max_kv >= 0; pages,
  * table_width, heads >= 1; rows, table_width * P and max_new * q_heads at most
@@ -117,7 +118,8 @@ fp8bs_status fp8bs_cache_attention_workspace(const fp8bs_cache* cache, int32_t q
  *   acc_in, acc_out : FP32 [batch][heads][acc_slots], acc_slots >= max_kv;
  *                     they may be the same array, and acc_in NULL (old = 0)
  *   workspace : fp8bs_cache_attention_weights_workspace bytes (NULL if 0)
- * Slots from kv_lens[b] on are set to 0.  Reads k and ks of *cache only.
+ * Slots from kv_lens[b] on, and those left out, are set to 0.  Reads k and ks
+ * of *cache only.
  */
 fp8bs_status fp8bs_cache_attention_weights(const fp8bs_cache* cache, const void* q, int64_t ld_q,
                                            int32_t q_heads, const int32_t* q_offsets, int64_t rows,
@@ -132,11 +134,11 @@ fp8bs_status fp8bs_cache_attention_weights_workspace(const fp8bs_cache* cache, i
                                                      int32_t max_new, int64_t acc_slots, int64_t* bytes);
 
 /*
- * Evict: keep count = min(kv_lens[b], budget) tokens of each sequence and
- * head: the last min(recent, count) ones, and of the others those with the
- * largest acc (ties: the lowest slot; NaN ranks below every number).  Kept
- * tokens keep their order and move to slots 0 .. count - 1 of pages
- * dst_table[b]; heads of one sequence may keep different tokens.
+ * Evict: keep count = min(kv_lens[b], budget) tokens (of those within the
+ * bounds) of each sequence and head: the last min(recent, count) ones, and of
+ * the others those with the largest acc (ties: the lowest slot; NaN ranks below
+ * every number).  Kept tokens keep their order and move to slots 0 .. count - 1
+ * of pages dst_table[b]; heads of one sequence may keep different tokens.
  *   acc       : FP32 [batch][heads][acc_slots]
  *   dst_table : INT32 [batch][dst_width], dst_width * P >= min(budget,
  *               max_kv); pages of the same pools that no source sequence of the call holds and

@@ -3,6 +3,10 @@
 Follows the definitions of include/fp8bs_cache.h, one sequence, head and token
 at a time.  Codes and scales are exact functions of their inputs; attention,
 weights and lse are computed in float64.
+
+max_new and max_kv (None: no bound) leave out a sequence's rows and cached tokens
+past them, as the end of its table does; results of rows that are left out stay
+0 (lse -inf).
 """
 
 import numpy as np
@@ -38,7 +42,13 @@ def reencode(codes, old, new):
         return encode((e4m3.decode(codes).astype(F32) * F32(old)).astype(F32), new)
 
 
-def append(cache, k_bits, v_bits, table, q_offsets, kv_lens, pow2=False):
+def held(cache, table, kv_len, max_kv=None):
+    """Cached tokens of a sequence that a call takes into account."""
+    room = table.shape[1] * cache[0].shape[2]
+    return max(0, min(int(kv_len), room, room if max_kv is None else max_kv))
+
+
+def append(cache, k_bits, v_bits, table, q_offsets, kv_lens, pow2=False, max_new=None):
     """cache = (k, ks, v, vs) arrays (uint8 codes, FP32 scales), changed in
     place; k_bits, v_bits: BF16 bits [T][heads][D]."""
     P = cache[0].shape[2]
@@ -47,7 +57,8 @@ def append(cache, k_bits, v_bits, table, q_offsets, kv_lens, pow2=False):
         for b in range(len(kv_lens)):
             lo, hi = int(q_offsets[b]), int(q_offsets[b + 1])
             base = int(kv_lens[b]) - (hi - lo)
-            slots = np.arange(max(base, 0), int(kv_lens[b]))
+            end = base + (hi - lo if max_new is None else min(hi - lo, max_new))
+            slots = np.arange(max(base, 0), min(end, held(cache, table, kv_lens[b])))
             for blk in np.unique(slots // P):
                 page = int(table[b][blk])
                 if not 0 <= page < codes.shape[0]:
@@ -89,18 +100,20 @@ def scores(q, k, there, scale, softcap, base, full):
     return np.where(seen & there[None, :], x, -np.inf)
 
 
-def attention(q_bits, cache, table, q_offsets, kv_lens, scale, softcap=0.0, full=False):
+def attention(q_bits, cache, table, q_offsets, kv_lens, scale, softcap=0.0, full=False, max_new=None, max_kv=None):
     """-> out [T][q_heads][D], lse [T][q_heads] in float64."""
     q = bf16.to_f32(q_bits).astype(np.float64)
     T, Hq, D = q.shape
     G = Hq // cache[0].shape[1]
     out, lse = np.zeros((T, Hq, D)), np.full((T, Hq), -np.inf)
     for b in range(len(kv_lens)):
-        lo, hi, length = int(q_offsets[b]), int(q_offsets[b + 1]), int(kv_lens[b])
+        lo, hi, length = int(q_offsets[b]), int(q_offsets[b + 1]), held(cache, table, kv_lens[b], max_kv)
+        base = int(kv_lens[b]) - (hi - lo)
+        hi = hi if max_new is None else min(hi, lo + max_new)
         for hq in range(Hq):
             k, there = values(cache[0], cache[1], table[b], length, hq // G)
             v, _ = values(cache[2], cache[3], table[b], length, hq // G)
-            x = scores(q[lo:hi, hq], k, there, scale, softcap, length - (hi - lo), full)
+            x = scores(q[lo:hi, hq], k, there, scale, softcap, base, full)
             if x.size == 0:
                 continue
             top = x.max(axis=1, keepdims=True)
@@ -113,18 +126,21 @@ def attention(q_bits, cache, table, q_offsets, kv_lens, scale, softcap=0.0, full
     return out, lse
 
 
-def weights(q_bits, lse, cache, table, q_offsets, kv_lens, scale, acc, slots, softcap=0.0, full=False):
+def weights(q_bits, lse, cache, table, q_offsets, kv_lens, scale, acc, slots, softcap=0.0, full=False, max_new=None,
+            max_kv=None):
     """-> [batch][heads][slots] float64; acc may be None."""
     q = bf16.to_f32(q_bits).astype(np.float64)
     H = cache[0].shape[1]
     G = q.shape[1] // H
     out = np.zeros((len(kv_lens), H, slots))
     for b in range(len(kv_lens)):
-        lo, hi, length = int(q_offsets[b]), int(q_offsets[b + 1]), int(kv_lens[b])
-        base = length - (hi - lo)
+        lo, hi, length = int(q_offsets[b]), int(q_offsets[b + 1]), held(cache, table, kv_lens[b], max_kv)
+        base = int(kv_lens[b]) - (hi - lo)
+        hi = hi if max_new is None else min(hi, lo + max_new)
+        old = max(0, min(base, length))
         for h in range(H):
-            if acc is not None and base > 0:
-                out[b, h, :base] = acc[b, h, :base]
+            if acc is not None:
+                out[b, h, :old] = acc[b, h, :old]
             k, there = values(cache[0], cache[1], table[b], length, h)
             for hq in range(h * G, (h + 1) * G):
                 x = scores(q[lo:hi, hq], k, there, scale, softcap, base, full)
@@ -134,15 +150,16 @@ def weights(q_bits, lse, cache, table, q_offsets, kv_lens, scale, acc, slots, so
     return out
 
 
-def evict(acc, cache, table, dst_table, kv_lens, budget, recent):
+def evict(acc, cache, table, dst_table, kv_lens, budget, recent, max_kv=None):
     """Changes the cache's destination pages in place; -> kept, new_lens, acc_out."""
     B, H, S = acc.shape
     P = cache[0].shape[2]
     kept = np.full((B, H, budget), -1, np.int32)
     acc_out = np.zeros_like(acc)
-    lens = np.minimum(np.asarray(kv_lens), budget).astype(np.int32)
+    there = [held(cache, table, n, max_kv) for n in kv_lens]
+    lens = np.minimum(there, budget).astype(np.int32)
     for b in range(B):
-        length, count = int(kv_lens[b]), int(lens[b])
+        length, count = there[b], int(lens[b])
         near = min(count, recent)
         for h in range(H):
             a = acc[b, h, :length - near]
