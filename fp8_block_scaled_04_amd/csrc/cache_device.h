@@ -24,11 +24,14 @@ struct Seq {
   int base;   // slot of the first row (negative: more rows than cached tokens; may pass len)
 };
 
+__device__ __forceinline__ int cached_tokens_of(const CacheArgs& c, int b) {
+  const int64_t room = (int64_t)c.width << c.lg_page;
+  return (int)max((int64_t)0, min((int64_t)min(c.kv_lens[b], c.max_kv), room));
+}
+
 // (b is the same for the whole wave; its numbers are kept on the scalar unit.)
 __device__ __forceinline__ int cached_tokens(const CacheArgs& c, int b) {
-  const int64_t room = (int64_t)c.width << c.lg_page;
-  const int n = (int)max((int64_t)0, min((int64_t)min(c.kv_lens[b], c.max_kv), room));
-  return __builtin_amdgcn_readfirstlane(n);
+  return __builtin_amdgcn_readfirstlane(cached_tokens_of(c, b));
 }
 
 __device__ __forceinline__ Seq sequence(const CacheArgs& c, int b) {

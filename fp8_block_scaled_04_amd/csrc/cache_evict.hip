@@ -7,7 +7,9 @@
 // LDS first, so that they are written (and their sums read) side by side.  The
 // keys stay in registers where they fit.
 // k_evict_move copies the codes, one workgroup per (destination page, head, K
-// or V).
+// or V), and writes the new lengths.  Every search has read the old ones by
+// then, and the copies take their counts from the kept slots, so both may be one
+// array.
 //
 // The move is HBM bound: 16 sequences cut to 4096 tokens (8 heads of 128) in 59
 // us, 262 MB at 4.4 TB/s; the search before it takes 18 us of latency (its reads
@@ -57,7 +59,6 @@ __global__ __launch_bounds__(kSelect) void k_evict_select(EvictArgs a) {
   // what lies past the count, here where the reads of the keys hide it
   for (int i = count + tid; i < a.budget; i += kSelect) kept[i] = -1;
   for (int64_t i = count + tid; i < a.acc_slots; i += kSelect) acc_out[i] = 0.0f;
-  if (h == 0 && tid == 0) a.new_lens[b] = count;
   if (need == 0 || need == others) {                 // the last ones, or nothing is evicted
     for (int i = tid; i < count; i += kSelect) {
       kept[i] = len - count + i;
@@ -198,23 +199,28 @@ __global__ __launch_bounds__(kSelect) void k_evict_select(EvictArgs a) {
 }
 
 template <int D>
-__global__ __launch_bounds__(kMove) void k_evict_move(EvictArgs a, int blocks) {
+__global__ __launch_bounds__(kMove) void k_evict_move(EvictArgs a, int blocks, int copies) {
   const CacheArgs& c = a.c;
+  const int tid = threadIdx.x;
   int id = blockIdx.x;
+  if (id >= copies) {                                // the last workgroups: 256 lengths each
+    const int b = (id - copies) * kMove + tid;
+    if (b < c.batch) a.new_lens[b] = min(cached_tokens_of(c, b), a.budget);
+    return;
+  }
   const int h = id % c.heads;
   id /= c.heads;
   const bool is_v = id & 1;
   id >>= 1;
   const int j = id % blocks, b = id / blocks;
-  const int count = min(cached_tokens(c, b), a.budget);
   const int P = 1 << c.lg_page, start = j << c.lg_page;
-  if (start >= count) return;
-  const int to = a.dst_table[(int64_t)b * a.dst_width + j];
-  if ((uint32_t)to >= (uint64_t)c.pages) return;
   const int32_t* kept = a.kept + ((int64_t)b * c.heads + h) * a.budget + start;
+  // (asked for together)
+  const int first = kept[0], slot = tid < min(P, a.budget - start) ? kept[tid] : -1;
+  const int to = a.dst_table[(int64_t)b * a.dst_width + j];
+  if (first < 0 || (uint32_t)to >= (uint64_t)c.pages) return;   // past the kept ones, or nowhere to go
   const uint8_t* codes = is_v ? c.v : c.k;
   const float* scales = is_v ? c.vs : c.ks;
-  const int n = min(P, count - start), tid = threadIdx.x;
 
   __shared__ int s_page[128];
   __shared__ int s_row[128];
@@ -224,8 +230,7 @@ __global__ __launch_bounds__(kMove) void k_evict_move(EvictArgs a, int blocks) {
   if (tid < P) {
     int page = -1, row = 0;
     float s = 0.0f;
-    if (tid < n) {
-      const int slot = kept[tid];
+    if (slot >= 0) {
       page = page_of(c, b, slot);
       row = slot & (P - 1);
       if (page >= 0) s = scales[(int64_t)page * c.heads + h];
@@ -268,9 +273,11 @@ int dst_blocks(const EvictArgs& a) {
   return (int)(((int64_t)most + (1 << a.c.lg_page) - 1) >> a.c.lg_page);
 }
 
+int64_t copies(const EvictArgs& a) { return 2 * (int64_t)a.c.batch * a.c.heads * dst_blocks(a); }
+
 }  // namespace
 
-int64_t evict_move_grid(const EvictArgs& a) { return 2 * (int64_t)a.c.batch * a.c.heads * dst_blocks(a); }
+int64_t evict_move_grid(const EvictArgs& a) { return copies(a) + ((int64_t)a.c.batch + kMove - 1) / kMove; }
 
 hipError_t launch_cache_evict(const EvictArgs& a, hipStream_t stream) {
   // up to 4096 or 16384 slots stay in registers; more are read again from
@@ -280,9 +287,8 @@ hipError_t launch_cache_evict(const EvictArgs& a, hipStream_t stream) {
   else k_evict_select<16><<<pairs, kSelect, 0, stream>>>(a);
   if (hipError_t e = hipGetLastError()) return e;
   const dim3 grid((unsigned)evict_move_grid(a));
-  if (grid.x == 0) return hipSuccess;
-  if (a.c.dim == 128) k_evict_move<128><<<grid, kMove, 0, stream>>>(a, dst_blocks(a));
-  else k_evict_move<64><<<grid, kMove, 0, stream>>>(a, dst_blocks(a));
+  if (a.c.dim == 128) k_evict_move<128><<<grid, kMove, 0, stream>>>(a, dst_blocks(a), (int)copies(a));
+  else k_evict_move<64><<<grid, kMove, 0, stream>>>(a, dst_blocks(a), (int)copies(a));
   return hipGetLastError();
 }
 

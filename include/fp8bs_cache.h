@@ -144,7 +144,7 @@ fp8bs_status fp8bs_cache_attention_weights_workspace(const fp8bs_cache* cache, i
  *               max_kv); pages of the same pools that no source sequence of the call holds and
  *               that appear once
  *   kept      : INT32 [batch][heads][budget], the source slots, then -1
- *   new_lens  : INT32 [batch]
+ *   new_lens  : INT32 [batch]; may be the cache's kv_lens (in place)
  *   acc_out   : FP32 [batch][heads][acc_slots] (not acc), the kept tokens'
  *               sums, then 0
  * A destination page's scale is the largest scale of the pages its tokens come
