@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 namespace fp8bs {
 
 // The cache and the sequences of one call, as the kernels take it.
@@ -73,19 +75,59 @@ struct EvictArgs {
   float* acc_out;
 };
 
-// Workgroups of the launches (the ABI layer bounds them below 2^30).
-int64_t append_grid(const CacheArgs& c);
-int64_t evict_move_grid(const EvictArgs& a);
+// Work-items of the largest launch per sequence (at most kMaxItems; the ABI
+// layer checks it).  Longer calls are launched in runs of sequences: a launch
+// holds fewer than 2^32 work-items, and what passes that may be dropped without
+// an error.
+constexpr int64_t kMaxItems = ((int64_t)1 << 32) - 1;
+int64_t append_items(const CacheArgs& c);
+int64_t attend_items(const AttendArgs& a);
+int64_t weights_items(const WeightArgs& a);
+int64_t evict_items(const EvictArgs& a);
+
+// Moves the arguments to sequences [first, first + n).
+inline void take_run(CacheArgs& c, int first, int n) {
+  c.table += (int64_t)first * c.width;
+  c.kv_lens += first;
+  if (c.q_offsets) c.q_offsets += first;
+  c.batch = n;
+}
+inline void take_run(AppendArgs& a, int first, int n) { take_run(a.c, first, n); }
+inline void take_run(AttendArgs& a, int first, int n) { take_run(a.c, first, n); }   // partial results go by row
+inline void take_run(WeightArgs& a, int first, int n) {                             // each run uses the workspace anew
+  take_run(a.c, first, n);
+  const int64_t at = (int64_t)first * a.c.heads * a.acc_slots;
+  if (a.acc_in) a.acc_in += at;
+  a.acc_out += at;
+}
+inline void take_run(EvictArgs& a, int first, int n) {
+  take_run(a.c, first, n);
+  const int64_t pair = (int64_t)first * a.c.heads;
+  a.acc += pair * a.acc_slots;
+  a.acc_out += pair * a.acc_slots;
+  a.kept += pair * a.budget;
+  a.dst_table += (int64_t)first * a.dst_width;
+  a.new_lens += first;
+}
+
+template <class Args, class Launch>
+hipError_t launch_in_runs(const Args& a, int64_t items, Launch launch) {
+  const int most = (int)std::min<int64_t>(a.c.batch, kMaxItems / std::max<int64_t>(items, 1));
+  for (int first = 0; first < a.c.batch; first += most) {
+    Args run = a;
+    take_run(run, first, std::min(most, a.c.batch - first));
+    if (hipError_t e = launch(run)) return e;
+  }
+  return hipSuccess;
+}
 
 // Sets tile_rows, chunk and splits from the sizes; the workspace is
 // splits * rows * q_heads * (D + 2) floats when splits > 1, else none.
 void attend_plan(AttendArgs& a);
 int64_t attend_workspace_bytes(const AttendArgs& a);
-int64_t attend_grid(const AttendArgs& a);
 // The same for the weights: splits, and the partial sums.
 void weights_plan(WeightArgs& a);
 int64_t weights_workspace_bytes(const WeightArgs& a);
-int64_t weights_grid(const WeightArgs& a);
 
 hipError_t launch_cache_append(const AppendArgs& a, bool pow2, hipStream_t stream);
 hipError_t launch_attend_tiles(const AttendArgs& a, int row_tiles, hipStream_t stream);

@@ -14,7 +14,7 @@ using fp8bs::CacheArgs;
 using fp8bs::check_device;
 using fp8bs::launched;
 
-constexpr int64_t kMaxCount = int64_t(1) << 30;      // slots, rows, workgroups: 32-bit indexes in the kernels
+constexpr int64_t kMaxCount = int64_t(1) << 30;      // slots, rows: 32-bit indexes in the kernels
 
 bool sizes_fit(const fp8bs_cache& c, int64_t rows, int64_t max_new, int64_t max_kv) {
   if (c.batch < 0 || c.heads <= 0 || c.pages <= 0 || c.table_width <= 0) return false;
@@ -59,7 +59,7 @@ fp8bs_status fp8bs_cache_append(const fp8bs_cache* cache, const void* k_new, con
   const fp8bs_cache& c = *cache;
   if (!sizes_fit(c, rows, max_new, 0) || ld_new < (int64_t)c.heads * c.dim || ld_new % 8) return FP8BS_ERR_SHAPE;
   fp8bs::AppendArgs a{args(c, q_offsets, rows, max_new, (int32_t)kMaxCount), k_new, v_new, ld_new};
-  if (append_grid(a.c) > kMaxCount) return FP8BS_ERR_SHAPE;
+  if (append_items(a.c) > fp8bs::kMaxItems) return FP8BS_ERR_SHAPE;
   if (flags & ~(uint32_t)FP8BS_SCALE_POW2) return FP8BS_ERR_FLAGS;
   if (c.batch == 0 || rows == 0 || max_new == 0) return FP8BS_OK;
   if (!k_new || !v_new || !q_offsets) return FP8BS_ERR_NULL;
@@ -82,7 +82,7 @@ fp8bs_status fp8bs_cache_attention(const fp8bs_cache* cache, const void* q, int6
                       nullptr};
   attend_plan(a);
   const int64_t need = attend_workspace_bytes(a);
-  if (attend_grid(a) > kMaxCount || workspace_bytes < need) return FP8BS_ERR_SHAPE;
+  if (attend_items(a) > fp8bs::kMaxItems || workspace_bytes < need) return FP8BS_ERR_SHAPE;
   if (out_dtype != FP8BS_OUT_BF16 && out_dtype != FP8BS_OUT_FP32) return FP8BS_ERR_FLAGS;
   if ((flags & ~(uint32_t)FP8BS_MASK_FULL) || bad_scalars(scale, softcap)) return FP8BS_ERR_FLAGS;
   if (c.batch == 0 || rows == 0 || max_new == 0) return FP8BS_OK;
@@ -129,7 +129,7 @@ fp8bs_status fp8bs_cache_attention_weights(const fp8bs_cache* cache, const void*
                       lse, acc_in, acc_out, acc_slots, (flags & FP8BS_MASK_FULL) != 0, 0, nullptr};
   weights_plan(a);
   const int64_t need = weights_workspace_bytes(a);
-  if (weights_grid(a) > kMaxCount || workspace_bytes < need) return FP8BS_ERR_SHAPE;
+  if (weights_items(a) > fp8bs::kMaxItems || workspace_bytes < need) return FP8BS_ERR_SHAPE;
   if ((flags & ~(uint32_t)FP8BS_MASK_FULL) || bad_scalars(scale, softcap)) return FP8BS_ERR_FLAGS;
   if (c.batch == 0 || acc_slots == 0) return FP8BS_OK;
   if ((rows > 0 && (!q || !lse)) || !q_offsets || !acc_out || (need > 0 && !workspace)) return FP8BS_ERR_NULL;
@@ -173,7 +173,7 @@ fp8bs_status fp8bs_cache_evict(const fp8bs_cache* cache, const float* acc, int64
   if (acc && acc == acc_out) return FP8BS_ERR_SHAPE;
   fp8bs::EvictArgs a{args(c, nullptr, 0, 0, max_kv), acc, acc_slots, dst_table, dst_width, budget, recent, kept,
                      new_lens, acc_out};
-  if (evict_move_grid(a) > kMaxCount) return FP8BS_ERR_SHAPE;
+  if (evict_items(a) > fp8bs::kMaxItems) return FP8BS_ERR_SHAPE;
   if (c.batch == 0) return FP8BS_OK;
   if (!kept || !new_lens || (acc_slots > 0 && (!acc || !acc_out)) || (dst_width > 0 && !dst_table)) return FP8BS_ERR_NULL;
   if (fp8bs_status e = cache_pointers(c, true)) return e;

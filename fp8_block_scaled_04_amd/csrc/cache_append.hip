@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__host__ __device__ int pages_touched(int max_new, int lg_page) {
+int pages_touched(int max_new, int lg_page) {
   return (int)(((int64_t)max_new + (1 << lg_page) - 2) >> lg_page) + 1;  // any alignment of the first slot
 }
 
@@ -103,16 +103,20 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(AppendArgs a, int blo
 
 }  // namespace
 
-int64_t append_grid(const CacheArgs& c) {
-  return 2 * (int64_t)c.batch * c.heads * pages_touched(c.max_new, c.lg_page);
-}
+namespace {
+
+int64_t page_blocks(const CacheArgs& c) { return pages_touched((int)std::min<int64_t>(c.max_new, c.rows), c.lg_page); }
+
+}  // namespace
+
+int64_t append_items(const CacheArgs& c) { return 2 * (int64_t)c.heads * page_blocks(c) * kThreads; }
 
 namespace {
 
 template <int D, int NP>
 void launch(const AppendArgs& a, bool pow2, hipStream_t stream) {
-  const dim3 grid((unsigned)append_grid(a.c));
-  const int blocks = pages_touched(a.c.max_new, a.c.lg_page);
+  const int blocks = (int)page_blocks(a.c);
+  const dim3 grid((unsigned)(2 * (int64_t)a.c.batch * a.c.heads * blocks));
   if (pow2) k_cache_append<D, NP, true><<<grid, kThreads, 0, stream>>>(a, blocks);
   else k_cache_append<D, NP, false><<<grid, kThreads, 0, stream>>>(a, blocks);
 }
@@ -132,9 +136,11 @@ void launch(const AppendArgs& a, bool pow2, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_cache_append(const AppendArgs& a, bool pow2, hipStream_t stream) {
-  if (a.c.dim == 128) launch<128>(a, pow2, stream);
-  else launch<64>(a, pow2, stream);
-  return hipGetLastError();
+  return launch_in_runs(a, append_items(a.c), [&](const AppendArgs& run) {
+    if (run.c.dim == 128) launch<128>(run, pow2, stream);
+    else launch<64>(run, pow2, stream);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace fp8bs

@@ -310,17 +310,21 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a) {
   if (a.lse && lane == 0) a.lse[at] = total == 0.0f ? -INFINITY : (top + __builtin_log2f(total)) * kLn2;
 }
 
-int row_tiles(const AttendArgs& a) {
-  return (int)(((int64_t)a.c.max_new * a.group + a.tile_rows - 1) / a.tile_rows);
+int row_tiles(const AttendArgs& a, int64_t new_tokens) {
+  return (int)((new_tokens * a.group + a.tile_rows - 1) / a.tile_rows);
 }
+
+// max_new may be far above what the call's rows allow a sequence.
+int launched_row_tiles(const AttendArgs& a) { return row_tiles(a, std::min<int64_t>(a.c.max_new, a.c.rows)); }
 
 template <int D>
 hipError_t launch(const AttendArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)attend_grid(a));
+  const int tiles = launched_row_tiles(a);
+  const dim3 grid((unsigned)((int64_t)a.c.batch * a.c.heads * tiles * a.splits));
   if (a.tile_rows > 16) {
-    if (hipError_t e = launch_attend_tiles(a, row_tiles(a), stream)) return e;
-  } else if (a.softcap > 0.0f) k_attend_rows<D, true><<<grid, kThreads, 0, stream>>>(a, row_tiles(a));
-  else k_attend_rows<D, false><<<grid, kThreads, 0, stream>>>(a, row_tiles(a));
+    if (hipError_t e = launch_attend_tiles(a, tiles, stream)) return e;
+  } else if (a.softcap > 0.0f) k_attend_rows<D, true><<<grid, kThreads, 0, stream>>>(a, tiles);
+  else k_attend_rows<D, false><<<grid, kThreads, 0, stream>>>(a, tiles);
   if (hipError_t e = hipGetLastError()) return e;
   if (a.splits == 1) return hipSuccess;
   const int64_t rows = (int64_t)a.c.batch * a.c.max_new * a.q_heads;
@@ -355,7 +359,7 @@ void attend_plan(AttendArgs& a) {
   // the causal rule leaves them unequal (one of 256 rows per CU, two
   // of 128).
   const int64_t target = a.tile_rows == 256 ? 512 : a.tile_rows == 128 ? 1024 : 768;
-  const int64_t base = pairs * row_tiles(a);
+  const int64_t base = pairs * row_tiles(a, a.c.max_new);
   const int64_t units = ((int64_t)a.c.max_kv + unit - 1) / unit;
   int64_t want = base > 0 ? (target + base - 1) / base : 1;
   if (want > kMaxSplits) want = kMaxSplits;
@@ -370,10 +374,16 @@ int64_t attend_workspace_bytes(const AttendArgs& a) {
   return a.splits > 1 ? (int64_t)a.splits * a.c.rows * a.q_heads * (a.c.dim + 2) * 4 : 0;
 }
 
-int64_t attend_grid(const AttendArgs& a) { return (int64_t)a.c.batch * a.c.heads * row_tiles(a) * a.splits; }
+int64_t attend_items(const AttendArgs& a) {
+  const int64_t tiles = (int64_t)a.c.heads * launched_row_tiles(a) * a.splits * (a.tile_rows == 256 ? 512 : kThreads);
+  const int64_t join = a.splits > 1 ? (int64_t)a.c.max_new * a.q_heads * (a.c.dim / 4) + kThreads : 0;
+  return std::max(tiles, join);
+}
 
 hipError_t launch_cache_attention(const AttendArgs& a, hipStream_t stream) {
-  return a.c.dim == 128 ? launch<128>(a, stream) : launch<64>(a, stream);
+  return launch_in_runs(a, attend_items(a), [&](const AttendArgs& run) {
+    return run.c.dim == 128 ? launch<128>(run, stream) : launch<64>(run, stream);
+  });
 }
 
 }  // namespace fp8bs

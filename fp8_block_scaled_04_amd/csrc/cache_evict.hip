@@ -277,19 +277,24 @@ int64_t copies(const EvictArgs& a) { return 2 * (int64_t)a.c.batch * a.c.heads *
 
 }  // namespace
 
-int64_t evict_move_grid(const EvictArgs& a) { return copies(a) + ((int64_t)a.c.batch + kMove - 1) / kMove; }
+int64_t evict_items(const EvictArgs& a) {
+  return std::max<int64_t>((int64_t)a.c.heads * kSelect, (2 * (int64_t)a.c.heads * dst_blocks(a) + 1) * kMove);
+}
 
-hipError_t launch_cache_evict(const EvictArgs& a, hipStream_t stream) {
-  // up to 4096 or 16384 slots stay in registers; more are read again from
-  // cache by each pass
-  const dim3 pairs((unsigned)(a.c.batch * a.c.heads));
-  if (a.c.max_kv <= 4 * kSelect) k_evict_select<4><<<pairs, kSelect, 0, stream>>>(a);
-  else k_evict_select<16><<<pairs, kSelect, 0, stream>>>(a);
-  if (hipError_t e = hipGetLastError()) return e;
-  const dim3 grid((unsigned)evict_move_grid(a));
-  if (a.c.dim == 128) k_evict_move<128><<<grid, kMove, 0, stream>>>(a, dst_blocks(a), (int)copies(a));
-  else k_evict_move<64><<<grid, kMove, 0, stream>>>(a, dst_blocks(a), (int)copies(a));
-  return hipGetLastError();
+hipError_t launch_cache_evict(const EvictArgs& call, hipStream_t stream) {
+  return launch_in_runs(call, evict_items(call), [&](const EvictArgs& a) {
+    // up to 4096 or 16384 slots stay in registers; more are read again from
+    // cache by each pass
+    const dim3 pairs((unsigned)(a.c.batch * a.c.heads));
+    if (a.c.max_kv <= 4 * kSelect) k_evict_select<4><<<pairs, kSelect, 0, stream>>>(a);
+    else k_evict_select<16><<<pairs, kSelect, 0, stream>>>(a);
+    if (hipError_t e = hipGetLastError()) return e;
+    const int n = (int)copies(a);
+    const dim3 grid((unsigned)(n + (a.c.batch + kMove - 1) / kMove));
+    if (a.c.dim == 128) k_evict_move<128><<<grid, kMove, 0, stream>>>(a, dst_blocks(a), n);
+    else k_evict_move<64><<<grid, kMove, 0, stream>>>(a, dst_blocks(a), n);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace fp8bs

@@ -434,15 +434,16 @@ int64_t weights_workspace_bytes(const WeightArgs& a) {
   return a.splits > 0 ? (int64_t)a.c.batch * a.c.heads * (a.splits + slot_tiles(a)) * kSlots * 4 : 0;
 }
 
-int64_t weights_grid(const WeightArgs& a) {
-  const int64_t tiles = slot_tiles(a);               // also the join's
-  return (int64_t)a.c.batch * a.c.heads * (a.splits > tiles ? a.splits : tiles);
+int64_t weights_items(const WeightArgs& a) {
+  return (int64_t)a.c.heads * std::max(a.splits, slot_tiles(a)) * kThreads;   // (the join's among them)
 }
 
 hipError_t launch_cache_weights(const WeightArgs& a, hipStream_t stream) {
   const bool cap = a.softcap > 0.0f;
-  if (a.c.dim == 128) return cap ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
-  return cap ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
+  return launch_in_runs(a, weights_items(a), [&](const WeightArgs& run) {
+    if (run.c.dim == 128) return cap ? launch<128, true>(run, stream) : launch<128, false>(run, stream);
+    return cap ? launch<64, true>(run, stream) : launch<64, false>(run, stream);
+  });
 }
 
 }  // namespace fp8bs

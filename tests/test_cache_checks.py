@@ -1,0 +1,65 @@
+"""Checks of the cache calls and their binding that need no GPU."""
+
+import ctypes
+
+import pytest
+
+from tests.test_cache_abi import DEVICE, F32, FAKE, I32, I64, NO_DEVICE, OK, P, SHAPE, U32, cache, fn
+
+
+@pytest.fixture(scope="module")
+def lib(lib_path):
+    return ctypes.CDLL(lib_path)
+
+
+# A launch holds fewer than 2^32 work-items; a call is launched in runs of
+# sequences, so only one sequence's own work is bounded by that.
+
+
+def test_work_of_one_sequence_append(lib):
+    f = fn(lib, "fp8bs_cache_append", [P, P, P, I64, P, I64, I32, U32, P])
+
+    def call(rows, new, **kw):
+        return f(cache(page=16, heads=16, table_width=1 << 26, **kw), FAKE, FAKE, 2048, FAKE, rows, new, 0, None)
+    assert call(1 << 24, 1 << 24) == SHAPE
+    if NO_DEVICE:
+        assert call(1 << 22, 1 << 22) == DEVICE
+        assert call(1 << 22, 1 << 22, batch=4096) == DEVICE                # more than one launch
+        assert call(5, 1 << 24) == DEVICE                                  # max_new far above the rows
+
+
+def test_work_of_one_sequence_attention(lib):
+    f = fn(lib, "fp8bs_cache_attention", [P, P, I64, I32, P, I64, I32, I32, F32, F32, P, I32, P, U32, P, I64, P])
+
+    def call(rows, new, **kw):
+        return f(cache(dim=64, **kw), FAKE, 512, 8, FAKE, rows, new, 512, 0.1, 0.0, FAKE, 0, None, 0, FAKE, 1 << 50, None)
+    if NO_DEVICE:
+        assert call(1 << 27, 1 << 27) == DEVICE
+        assert call(1 << 27, 1 << 27, batch=4096) == DEVICE
+        assert call(5, 1 << 27) == DEVICE
+
+
+def test_work_of_one_sequence_weights(lib):
+    f = fn(lib, "fp8bs_cache_attention_weights",
+           [P, P, I64, I32, P, I64, I32, I32, F32, F32, P, P, P, I64, U32, P, I64, P])
+
+    def call(slots, **kw):
+        return f(cache(**kw), FAKE, 4096, 32, FAKE, 5, 1, 512, 0.1, 0.0, FAKE, FAKE, FAKE, slots, 0, None, 0, None)
+    assert call(1 << 28, heads=32) == SHAPE
+    if NO_DEVICE:
+        assert call(1 << 25, heads=32) == DEVICE
+        assert call(1 << 25, heads=32, batch=4096) == DEVICE
+
+
+def test_work_of_one_sequence_evict(lib):
+    f = fn(lib, "fp8bs_cache_evict", [P, P, I64, P, I32, I32, I32, I32, P, P, P, P])
+
+    def call(budget, **kw):
+        c = cache(page=16, table_width=1 << 26, **kw)
+        return f(c, FAKE, 1 << 30, FAKE, 1 << 26, 1 << 30, budget, 0, FAKE, FAKE, 0x20000, None)
+    assert call(1 << 26, heads=16) == SHAPE
+    assert call(1 << 26, heads=16, batch=0) == SHAPE
+    assert call(1 << 20, heads=16, batch=0) == OK
+    if NO_DEVICE:
+        assert call(1 << 22, heads=16) == DEVICE
+        assert call(1 << 22, heads=16, batch=4096) == DEVICE

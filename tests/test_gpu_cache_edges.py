@@ -51,3 +51,117 @@ def test_evict_of_empty_sequences():
         torch.cuda.synchronize()
         assert (kept == -1).all() and lens.tolist() == [0, 0] and (out == 0).all()
         assert torch.equal(d["k"].view(torch.uint8), before)
+
+
+# A launch holds fewer than 2^32 work-items; these calls need more.
+
+
+def pool(pages, H, D, P):
+    return (torch.zeros((pages, H, P, D), dtype=torch.float8_e4m3fn, device="cuda"),
+            torch.zeros((pages, H), device="cuda"),
+            torch.zeros((pages, H, P, D), dtype=torch.float8_e4m3fn, device="cuda"),
+            torch.zeros((pages, H), device="cuda"))
+
+
+def offsets(new):
+    return i32_dev(np.concatenate([[0], np.cumsum(new)]))
+
+
+def bits_of(t):
+    return t.contiguous().view(torch.uint8)
+
+
+def test_append_of_a_long_prompt_among_many_sequences():
+    # 256 sequences of 16 heads, pages of 16: 2^26 workgroups of 256 by max_new
+    B, H, D, P, long = 256, 16, 64, 16, 131072
+    new = [1 + b % 3 for b in range(B)]
+    new[200] = long
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(sum(new), H, D, generator=g, device="cuda").to(torch.bfloat16)
+    table = torch.full((B, long // P), -1, dtype=torch.int32, device="cuda")
+    table[:, 0] = torch.arange(B, dtype=torch.int32)
+    table[200] = B + torch.arange(long // P, dtype=torch.int32)
+    lens, off = i32_dev(new), offsets(new)
+    got, want = pool(B + long // P, H, D, P), pool(B + long // P, H, D, P)
+    print("append, one call", flush=True)
+    fp8bs.cache_append(x, -x, got, table, off, lens, long)
+    print("append, three calls", flush=True)
+    for lo, hi, most in ((0, 200, 3), (200, 201, long), (201, 256, 3)):
+        fp8bs.cache_append(x, -x, want, table[lo:hi], off[lo:hi + 1], lens[lo:hi], most)
+    torch.cuda.synchronize()
+    assert float(got[1].min(1)[0][table[table >= 0].long()].min()) > 0
+    for a, b in zip(got, want):
+        assert torch.equal(bits_of(a), bits_of(b))
+
+
+@pytest.mark.parametrize("D,H,G", [(128, 2, 8), (64, 2, 8)])
+def test_attention_and_weights_of_very_many_row_tiles(D, H, G):
+    # 4096 sequences of 32 tokens, max_new the rows of the whole call
+    B, n, P = 4096, 32, 32
+    g = torch.Generator(device="cuda").manual_seed(D)
+    k = torch.randn(B * n, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    q = torch.randn(B * n, H * G, D, generator=g, device="cuda").to(torch.bfloat16)
+    cache = pool(B, H, D, P)
+    table, lens, off = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous(), i32_dev([n] * B), offsets([n] * B)
+    fp8bs.cache_append(k, -k, cache, table, off, lens, n)
+    print(f"attention D={D}, one call", flush=True)
+    out, lse = fp8bs.cache_attention(q, cache, table, off, lens, B * n, n, 0.1, return_lse=True)
+    print(f"weights D={D}, one call", flush=True)
+    acc = fp8bs.cache_attention_weights(q, lse, cache, table, off, lens, B * n, n, 0.1)
+    torch.cuda.synchronize()
+    for b in (0, 1, 1023, 1024, 2047, 2048, 2049, 4094):
+        print(f"sequences {b}, {b + 1}", flush=True)
+        rows = slice(b * n, (b + 2) * n)
+        # the same kernels: a bound far above the rows, and of the cached tokens as above
+        o, z = fp8bs.cache_attention(q[rows], cache, table[b:b + 2], off[:3], lens[:2], 4 * n, n, 0.1, return_lse=True)
+        a = fp8bs.cache_attention_weights(q[rows], z, cache, table[b:b + 2], off[:3], lens[:2], 4 * n, n, 0.1)
+        torch.cuda.synchronize()
+        e = (out[rows].float() - o.float()).abs().max() / o.float().abs().max()
+        assert float(e) < 2.0 ** -6 and torch.allclose(lse[rows], z, rtol=0, atol=2.0 ** -12)
+        assert torch.allclose(acc[b:b + 2], a, rtol=2.0 ** -10, atol=1e-6)
+
+
+def test_weights_over_very_many_slots():
+    # 2048 sequences, 4 heads, 2^19 + 256 slots of sums: 2^32 of them and more
+    B, H, D, P, slots = 2048, 4, 64, 16, (1 << 19) + 256
+    n = 20
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k = torch.randn(B * n, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    cache = pool(2 * B, H, D, P)
+    table, lens, off = torch.arange(2 * B, dtype=torch.int32, device="cuda").view(B, 2), i32_dev([n] * B), offsets([n] * B)
+    fp8bs.cache_append(k, k, cache, table, off, lens, n)
+    ones = offsets([1] * B)
+    q = torch.randn(B, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    _, lse = fp8bs.cache_attention(q, cache, table, ones, lens, 1, n, 0.1, return_lse=True)
+    small = fp8bs.cache_attention_weights(q, lse, cache, table, ones, lens, 1, n, 0.1)
+    out = torch.full((B, H, slots), 5.0, device="cuda")
+    print("weights, one call", flush=True)
+    fp8bs.cache_attention_weights(q, lse, cache, table, ones, lens, 1, n, 0.1, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:, :, :n], small)
+    assert all(int(torch.count_nonzero(out[b:b + 64, :, n:])) == 0 for b in range(0, B, 64))
+
+
+def test_evict_to_very_many_pages():
+    # 1024 sequences, 8 heads, a budget of 16400 tokens in pages of 16
+    B, H, D, P, budget, kv = 1024, 8, 64, 16, 16400, 40
+    width = -(-budget // P)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    k = torch.randn(B * kv, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    cache = pool(6 * B, H, D, P)
+    table, lens = torch.arange(3 * B, dtype=torch.int32, device="cuda").view(B, 3), i32_dev([kv] * B)
+    fp8bs.cache_append(k, -k, cache, table, offsets([kv] * B), lens, kv)
+    dst = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+    dst[:, :3] = 3 * B + table
+    acc = torch.rand(B, H, budget, generator=g, device="cuda")
+    print("evict, one call", flush=True)
+    kept, new, out = fp8bs.cache_evict(acc, cache, table, dst, lens, budget, budget, 5)
+    torch.cuda.synchronize()
+    assert (new == kv).all() and torch.equal(out[:, :, :kv], acc[:, :, :kv]) and (out[:, :, kv:] == 0).all()
+    assert (kept[:, :, :kv] == torch.arange(kv, dtype=torch.int32, device="cuda")).all() and (kept[:, :, kv:] == -1).all()
+    for a in (cache[1], cache[3]):
+        assert torch.equal(a[3 * B:], a[:3 * B])
+    used = (torch.arange(3 * P, device="cuda") < kv).view(3, 1, P, 1)
+    for a in (cache[0], cache[2]):
+        x = bits_of(a).view(2, B, 3, H, P, D)
+        assert torch.equal(x[1], torch.where(used, x[0], torch.zeros_like(x[0])))
