@@ -505,7 +505,10 @@ def _float_out(t, name, shape, dev, dtype=torch.float32):
     return t
 
 
-_stream_of = torch._C._cuda_getCurrentRawStream      # current HIP stream of a device, as an integer
+def _stream_of(dev):
+    """Current HIP stream of a device, as an integer (looked up on use: builds
+    of torch without GPU support, which the host-only calls serve too, lack it)."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _workspace(workspace, need, dev):

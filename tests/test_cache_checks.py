@@ -1,8 +1,10 @@
 """Checks of the cache calls and their binding that need no GPU."""
 
 import ctypes
+import importlib.util
 
 import pytest
+import torch
 
 from tests.test_cache_abi import DEVICE, F32, FAKE, I32, I64, NO_DEVICE, OK, P, SHAPE, U32, cache, fn
 
@@ -63,3 +65,14 @@ def test_work_of_one_sequence_evict(lib):
     if NO_DEVICE:
         assert call(1 << 22, heads=16) == DEVICE
         assert call(1 << 22, heads=16, batch=4096) == DEVICE
+
+
+def test_binding_imports_without_gpu_support_in_torch(lib_path, monkeypatch):
+    # host-only calls (tiles, workspace sizes) need no stream
+    from fp8_block_scaled_04_amd import fp8bs
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    spec = importlib.util.spec_from_file_location("fp8_block_scaled_04_amd.fp8bs_again", fp8bs.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    pool = (torch.zeros(4, 2, 16, 64, dtype=torch.uint8), None, None, None)
+    assert again.cache_attention_workspace_bytes(pool, torch.zeros(1, 2, dtype=torch.int32), 4, 1, 1, 5) == 0
