@@ -492,6 +492,13 @@ def _packed(t, name, heads, dim, dev):
     return ld if rows > 1 else n * dim
 
 
+def _fits(*counts):
+    """Counts that the library takes as 32-bit integers (ctypes would drop the
+    upper bits)."""
+    if max(counts) > 0x7FFFFFFF:
+        raise ValueError(f"counts must be below 2^31, got {max(counts)}")
+
+
 def _row_offsets(q_offsets, batch, dev):
     _on(q_offsets, "q_offsets", torch.int32, 1, dev)
     if q_offsets.shape[0] != batch + 1:
@@ -527,6 +534,7 @@ def cache_append(k_new, v_new, cache, table, q_offsets, kv_lens, max_new: int, p
     strided) into the last slots of their sequences; in place.  A page's
     scale grows to cover its new tokens, and its older codes are then encoded
     again."""
+    _fits(max_new)
     c, dev = _cache_args(cache, table, kv_lens)
     ld = _packed(k_new, "k_new", c.heads, c.dim, dev)
     ldv = _packed(v_new, "v_new", c.heads, c.dim, dev)
@@ -541,6 +549,7 @@ def cache_append(k_new, v_new, cache, table, q_offsets, kv_lens, max_new: int, p
 def cache_attention_workspace_bytes(cache, table, q_heads: int, rows: int, max_new: int, max_kv: int) -> int:
     """Workspace bytes of cache_attention for these sizes (0: it would not
     split the cached tokens)."""
+    _fits(q_heads, max_new, max_kv)
     pages, heads, page, dim = cache[0].shape
     c = _Cache(None, None, None, None, None, None, pages, table.shape[0], table.shape[1], heads, page, dim)
     out = ctypes.c_int64(0)
@@ -558,6 +567,7 @@ def cache_attention(q, cache, table, q_offsets, kv_lens, max_new: int, max_kv: i
     a sequence.  -> out [T][q_heads][D], or (out, lse [T][q_heads]).
     workspace: a uint8 tensor of cache_attention_workspace_bytes, allocated
     here when not given."""
+    _fits(max_new, max_kv)
     c, dev = _cache_args(cache, table, kv_lens)
     ld = _packed(q, "q", None, c.dim, dev)
     T, Hq, D = q.shape
@@ -580,6 +590,7 @@ def cache_attention(q, cache, table, q_offsets, kv_lens, max_new: int, max_kv: i
 def cache_attention_weights_workspace_bytes(cache, table, q_heads: int, max_new: int, slots: int) -> int:
     """Workspace bytes of cache_attention_weights for these sizes (0 for few
     rows)."""
+    _fits(q_heads, max_new)
     pages, heads, page, dim = cache[0].shape
     c = _Cache(None, None, None, None, None, None, pages, table.shape[0], table.shape[1], heads, page, dim)
     out = ctypes.c_int64(0)
@@ -596,6 +607,7 @@ def cache_attention_weights(q, lse, cache, table, q_offsets, kv_lens, max_new: i
     None starts every sum at 0 (slots then defaults to max_kv).  workspace: a
     uint8 tensor of cache_attention_weights_workspace_bytes, allocated here
     when not given."""
+    _fits(max_new, max_kv)
     c, dev = _cache_args(cache, table, kv_lens)
     ld = _packed(q, "q", None, c.dim, dev)
     T, Hq, _ = q.shape
@@ -627,6 +639,7 @@ def cache_evict(acc, cache, table, dst_table, kv_lens, max_kv: int, budget: int,
     [batch][width] of the same pools (no page of a source sequence).
     -> (kept int32 [batch][heads][budget]: source slots, then -1; new lengths
     int32 [batch]; the kept tokens' sums, same shape as acc, then 0)."""
+    _fits(max_kv, budget, recent)
     c, dev = _cache_args(cache, table, kv_lens)
     _need(acc, "acc", torch.float32, 3)
     slots = acc.shape[2]

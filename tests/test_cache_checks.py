@@ -76,3 +76,23 @@ def test_binding_imports_without_gpu_support_in_torch(lib_path, monkeypatch):
     spec.loader.exec_module(again)
     pool = (torch.zeros(4, 2, 16, 64, dtype=torch.uint8), None, None, None)
     assert again.cache_attention_workspace_bytes(pool, torch.zeros(1, 2, dtype=torch.int32), 4, 1, 1, 5) == 0
+
+
+def test_binding_refuses_counts_past_32_bits(lib_path):
+    # (2^32 would arrive as 0: every cached token left out)
+    from fp8_block_scaled_04_amd import fp8bs
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32)  # noqa: E731
+    codes, scales = torch.zeros(4, 2, 16, 64, dtype=torch.uint8), torch.zeros(4, 2)
+    pool = (codes, scales, codes, scales)
+    q, lse, acc = torch.zeros(1, 4, 64, dtype=torch.bfloat16), torch.zeros(1, 4), torch.zeros(1, 2, 8)
+    big = 1 << 32
+    calls = [lambda: fp8bs.cache_append(q[:, :2], q[:, :2], pool, i32(1, 2), i32(2), i32(1), big),
+             lambda: fp8bs.cache_attention_workspace_bytes(pool, i32(1, 2), 4, 1, 1, big),
+             lambda: fp8bs.cache_attention_workspace_bytes(pool, i32(1, 2), 4, 1, big + 1, 5),
+             lambda: fp8bs.cache_attention(q, pool, i32(1, 2), i32(2), i32(1), 1, big, 0.1),
+             lambda: fp8bs.cache_attention_weights_workspace_bytes(pool, i32(1, 2), 4, big + 1, 8),
+             lambda: fp8bs.cache_attention_weights(q, lse, pool, i32(1, 2), i32(2), i32(1), 1, big, 0.1),
+             lambda: fp8bs.cache_evict(acc, pool, i32(1, 2), i32(1, 2), i32(1), 8, 4, big)]
+    for call in calls:
+        with pytest.raises(ValueError, match="below 2"):
+            call()
