@@ -386,10 +386,12 @@ __global__ __launch_bounds__(kSlots) void k_weights_join(WeightArgs a, int tiles
   const Seq s = sequence(c, (int)(pair / c.heads));
   float x = 0.0f;
   if (slot < a.acc_slots) x = old_sum(a, s, pair, slot);
-  if (tile < live_tiles(s) && s.n > 0) {
+  // (no steps at all: no row sees a slot)
+  const int64_t all = tile < live_tiles(s) && s.n > 0 ? all_steps(a, s) : 0;
+  if (all > 0) {
     int64_t before = 0;
     for (int t = 0; t < tile; ++t) before += tile_steps(a, s, t).count;
-    const int64_t all = all_steps(a, s), after = before + tile_steps(a, s, tile).count;
+    const int64_t after = before + tile_steps(a, s, tile).count;
     int run = (int)(before * a.splits / all);        // its end is past `before`, or the next one's is
     while (run > 0 && run_begin(a, all, run) > before) --run;
     for (; run < a.splits && run_begin(a, all, run) < after; ++run)

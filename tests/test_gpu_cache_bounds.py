@@ -113,6 +113,25 @@ def test_weights(name):
         assert (np.abs(out_host_f64(out) - ref) <= e * ref + 1e-30).all(), name
 
 
+@pytest.mark.parametrize("max_new,G", [(64, 1), (64, 3), (70, 1)])
+def test_weights_where_no_row_sees_a_slot(max_new, G):
+    # 200 rows of 5 cached tokens: the first rows, all that max_new lets in, lie
+    # before the first slot
+    w = cache_util.make([5, 5], [200, 3], 2, G, 64, 16, seed=G)
+    d = cache_util.dev(w)
+    lse = oracle.attention(w["q"], cache_util.cache_of(w), w["table"], w["q_offsets"], w["kv_lens"], 0.1)[1].astype(np.float32)
+    acc = f32_dev(np.ones((2, 2, 8)))
+    print(f"weights of hidden rows max_new={max_new} G={G}", flush=True)
+    for n in (1, 2):
+        args = (w["table"][:n], w["q_offsets"][:n + 1], w["kv_lens"][:n], 0.1, np.ones((n, 2, 8)), 8)
+        ref = oracle.weights(w["q"], lse, cache_util.cache_of(w), *args, max_new=max_new)
+        out = fp8bs.cache_attention_weights(d["q"], f32_dev(lse), cache_dev(d), d["table"][:n], d["q_offsets"][:n + 1],
+                                            d["kv_lens"][:n], max_new, 5, 0.1, acc[:n])
+        torch.cuda.synchronize()
+        assert (ref[0] == 0).all() and (out[0] == 0).all()
+        assert (np.abs(out_host_f64(out) - ref) <= 2.0 ** -12 * ref).all()
+
+
 @pytest.mark.parametrize("P,D", [(16, 64), (64, 128)])
 @pytest.mark.parametrize("kv,new,more,max_new", [
     ([128, 100, 128], [1, 1, 3], [1, 0, 1], 3),          # the last rows have no place
