@@ -44,8 +44,9 @@ fp8bs_status cache_pointers(const fp8bs_cache& c, bool values) {
   return FP8BS_OK;
 }
 
+// A cap's reciprocal and its double stay finite.
 bool bad_scalars(float scale, float softcap) {
-  return !std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.0f;
+  return !std::isfinite(scale) || !(softcap == 0.0f || (softcap >= 0x1p-126f && softcap <= 0x1p126f));
 }
 
 }  // namespace

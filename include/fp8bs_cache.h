@@ -94,7 +94,7 @@ fp8bs_status fp8bs_cache_append(const fp8bs_cache* cache, const void* k_new, con
  *   out : BF16 or FP32 [rows][q_heads][D]
  *   lse : FP32 [rows][q_heads], or NULL
  *   workspace : fp8bs_cache_attention_workspace bytes (NULL if 0)
- * Requires q_heads % heads == 0, scale finite, softcap >= 0.  Scores and
+ * Requires q_heads % heads == 0, scale finite, softcap 0 or 2^-126 .. 2^126.  Scores and
  * softmax sums are FP32; the weights enter the product with the values as
  * BF16, in calls of few rows as two BF16 parts.
  */

@@ -6,7 +6,7 @@ import importlib.util
 import pytest
 import torch
 
-from tests.test_cache_abi import DEVICE, F32, FAKE, I32, I64, NO_DEVICE, OK, P, SHAPE, U32, cache, fn
+from tests.test_cache_abi import DEVICE, F32, FAKE, FLAGS, I32, I64, NO_DEVICE, OK, P, SHAPE, U32, cache, fn
 
 
 @pytest.fixture(scope="module")
@@ -96,3 +96,19 @@ def test_binding_refuses_counts_past_32_bits(lib_path):
     for call in calls:
         with pytest.raises(ValueError, match="below 2"):
             call()
+
+
+def test_caps_whose_reciprocal_or_double_overflows_are_refused(lib):
+    # a score of 0 times the reciprocal of a subnormal cap is NaN
+    f = fn(lib, "fp8bs_cache_attention", [P, P, I64, I32, P, I64, I32, I32, F32, F32, P, I32, P, U32, P, I64, P])
+    g = fn(lib, "fp8bs_cache_attention_weights",
+           [P, P, I64, I32, P, I64, I32, I32, F32, F32, P, P, P, I64, U32, P, I64, P])
+
+    def both(cap):
+        return (f(cache(), FAKE, 1024, 8, FAKE, 2, 1, 100, 0.1, cap, FAKE, 0, None, 0, None, 0, None),
+                g(cache(), FAKE, 1024, 8, FAKE, 2, 1, 512, 0.1, cap, FAKE, FAKE, FAKE, 512, 0, None, 0, None))
+    for cap in (1e-40, 2.0 ** -149, 2.0 ** 126.5, 3e38, float("inf"), float("nan"), -1.0):
+        assert both(cap) == (FLAGS, FLAGS), cap
+    if NO_DEVICE:
+        for cap in (0.0, -0.0, 2.0 ** -126, 30.0, 2.0 ** 126):
+            assert both(cap) == (DEVICE, DEVICE), cap
