@@ -92,13 +92,6 @@ __device__ __forceinline__ uint32_t reencode4(uint32_t w, float old, const TileS
                         div_rn(d * t.sx, t.ss, t.r));
 }
 
-// A wave-uniform value that no kernel of the launch writes, through the scalar
-// cache.
-template <typename T>
-__device__ __forceinline__ T uniform_load(const T* p) {
-  return *reinterpret_cast<const __attribute__((address_space(4))) T*>(reinterpret_cast<uintptr_t>(p));
-}
-
 // cap * tanh(x / cap), y = x / cap.  For |y| < kCapSmall by the odd series of
 // tanh, so that small scores keep FP32 relative accuracy; above by
 // 1 - 2 / (e^(2y) + 1).  tanh_ratio<TERMS>(y) is tanh(y) / y: three terms past

@@ -15,8 +15,8 @@
  *                                        rows of the current call included
  * P is 16, 32, 64 or 128 and D 64 or 128.  A token's place in its sequence is
  * its slot: slot t lies in page table[b][t / P] at row t % P.  Table entries
- * past the last cached token are never read.  Rows of a page past the last
- * cached token may hold anything.  A cached token whose table entry lies
+ * past the last cached token, and rows of a page past it, may hold anything
+ * (some are read, inside the table and the pools, and not used).  A cached token whose table entry lies
  * outside [0, pages) counts as absent (nothing is read or written for it).
  *
  * Packed rows.  The rows of all sequences are concatenated; sequence b owns
