@@ -16,8 +16,9 @@
  * P is 16, 32, 64 or 128 and D 64 or 128.  A token's place in its sequence is
  * its slot: slot t lies in page table[b][t / P] at row t % P.  Table entries
  * past the last cached token, and rows of a page past it, may hold anything
- * (some are read, inside the table and the pools, and not used).  A cached token whose table entry lies
- * outside [0, pages) counts as absent (nothing is read or written for it).
+ * (some are read, inside the table and the pools, and not used).  A cached
+ * token whose table entry lies outside [0, pages) counts as absent (nothing is
+ * read or written for it).
  *
  * Packed rows.  The rows of all sequences are concatenated; sequence b owns
  * rows [q_offsets[b], q_offsets[b + 1]) (INT32 [batch + 1], device), and they
