@@ -343,9 +343,9 @@ void attend_plan(AttendArgs& a) {
   // sequences, 16 or 20 us for one; 256 rows 111 (128) or 104 us (256); 128
   // rows of D = 64 83 (16) or 64 us (128).
   // Little work in all stays on 16-row tiles, which fill the chip sooner and
-  // round the weights to 2^-17 (the larger ones' single BF16 rounding averages
-  // out to that of the output over many rows, over a few dozen tokens it may
-  // not: 1.55 times the error of exact weights).  16 against larger, (row, head)
+  // round the weights to 2^-17 (the larger ones' single BF16 rounding for BF16
+  // outputs puts them at 1.45 times the error of exact weights, over a few dozen
+  // tokens at up to 1.67).  16 against larger, (row, head)
   // pairs / cached tokens, D = 128: 4096/128 in 6 or 13 us, 4096/1024 20 or 24,
   // 8192/256 20 or 17, 1024/32768 63 or 40; D = 64: 16384/512 11 or 20,
   // 8192/4096 37 or 44, 32768/1024 25 or 42, 65536/128 21 or 13, 1024/131072 125

@@ -59,12 +59,21 @@ __device__ __forceinline__ int v_at(int dim, int chunk) {
 // Waves per SIMD.  D = 128: two; a wave's accumulators, queries and scores take
 // 239 of 256 registers.  D = 64 is bound by the vector unit (a score costs the
 // same there, its products half): three, as workgroups of their own, whose
-// phases drift apart (513-token chunks 273 -> 213 us).
-template <int D>
-constexpr int kPerSimd = D == 64 ? 3 : 2;
+// phases drift apart (513-token chunks 273 -> 213 us), though the 168 registers
+// that leaves spill 35 (21 without a cap).  Second parts of the weights do not
+// fit beside that: two.
+template <int D, bool TWO>
+constexpr int kPerSimd = D == 64 && !TWO ? 3 : 2;
 
-template <int D, bool CAP, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(kPerSimd<D>, kPerSimd<D>)))
+// A weight meets the codes rounded to BF16 once: 2^-9 of it, about what the
+// rounding of a BF16 output takes again.  TWO (FP32 outputs): as two BF16 parts,
+// the second being what the first leaves, so that 2^-18 of it is lost; a step's
+// outputs are then added before the scores of the next one.  The second products
+// cost: prompts of up to 6000 tokens 603 us instead of 450, 25-token rows of 32
+// sequences behind 4096 (D = 128, whose 128-row form spills 38 registers) 162
+// instead of 86, the 513-token chunks (D = 64) 244 instead of 190.
+template <int D, bool CAP, int WAVES, bool TWO>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(kPerSimd<D, TWO>, kPerSimd<D, TWO>)))
 void k_attend_tiles(AttendArgs a, int row_tiles) {
   const CacheArgs& c = a.c;
   constexpr int T = 64 * WAVES, BM = 32 * WAVES;
@@ -223,7 +232,7 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
 
   constexpr int NS = D / 32;                         // products of a 16-token group, for scores and for outputs
   v16f o[DT], sc[2];                                 // outputs; scores: sc[u / 2][8 (u & 1) + i] is of group u
-  v8bf pf[4];                                        // weights of group u, times the value scale
+  v8bf pf[4], pl[4];                                 // weights of group u, times the value scale; (TWO) the second parts
 #pragma unroll
   for (int d = 0; d < DT; ++d) o[d] = v16f{};
   float m = -INFINITY, l = 0.0f;
@@ -242,12 +251,13 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
 #pragma unroll
     for (int j = 0; j < 4 * NS; ++j) {
       o[j % NS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[j % kAhead], pf[j / NS], o[j % NS], 0, 0, 0);
+      if (TWO) o[j % NS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[j % kAhead], pl[j / NS], o[j % NS], 0, 0, 0);
       if (j + kAhead < 4 * NS) ring[j % kAhead] = value(buf, j + kAhead);
     }
   };
 
-  // Matrix phase: the scores of step t, then (not FIRST) the outputs of step
-  // t - 1, as one stream of products.  The sum so far is rescaled beside the
+  // Matrix phase: the scores of step t, then (not FIRST, which TWO always is) the
+  // outputs of step t - 1, as one stream of products.  The sum so far is rescaled beside the
   // score products, every step: the vector unit is idle there, and no branch
   // surrounds the accumulators.  g0, g1, g2: pages of steps t, t + 1, t + 2.
   auto matrix = [&](auto first, int t, int it, int g0, int g1, int g2) {
@@ -365,7 +375,9 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
           else y = __builtin_fmaf(x, f[u], -to);
           const float p = __builtin_amdgcn_exp2f(y);
           sum += p;
-          pf[u][e] = (__bf16)(kGeneral ? p * vs : p);
+          const float w = kGeneral ? p * vs : p;
+          pf[u][e] = (__bf16)w;
+          if (TWO) pl[u][e] = (__bf16)(w - (float)pf[u][e]);
         }
         l = kGeneral ? l + sum : __builtin_fmaf(sum, vs, l);
         asm volatile("" : "+v"(l));                  // the sum stays here: sunk below, it would hold every weight
@@ -395,12 +407,13 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
       if (group == 1) __syncthreads();
       softmax(t, g0, sl);
       if (group == 0) __syncthreads();
+      if (TWO) add_outputs((it - 1) & 1);
       g0 = g1;
       g1 = g2;
       g2 = check(raw, t + 3 * kTok);
       sl = scales_of(g0);
       raw = lookup(t + 4 * kTok);
-      matrix(Int<0>{}, t + kTok, it, g0, g1, g2);
+      matrix(Int<TWO>{}, t + kTok, it, g0, g1, g2);
     }
     if (group == 1) __syncthreads();
     softmax(t, g0, sl);
@@ -435,16 +448,22 @@ void k_attend_tiles(AttendArgs a, int row_tiles) {
   if (a.lse && half == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + __builtin_log2f(l)) * kLn2;
 }
 
-template <int D, bool CAP>
+template <int D, bool CAP, bool TWO>
 void launch(const AttendArgs& a, int row_tiles, hipStream_t stream) {
   const dim3 grid((unsigned)((int64_t)a.c.batch * a.c.heads * row_tiles * a.splits));
   if constexpr (D == 128) {
     if (a.tile_rows == 256) {
-      k_attend_tiles<D, CAP, 8><<<grid, 512, 0, stream>>>(a, row_tiles);
+      k_attend_tiles<D, CAP, 8, TWO><<<grid, 512, 0, stream>>>(a, row_tiles);
       return;
     }
   }
-  k_attend_tiles<D, CAP, 4><<<grid, 256, 0, stream>>>(a, row_tiles);
+  k_attend_tiles<D, CAP, 4, TWO><<<grid, 256, 0, stream>>>(a, row_tiles);
+}
+
+template <int D, bool CAP>
+void launch(const AttendArgs& a, int row_tiles, hipStream_t stream) {
+  if (a.out_f32) launch<D, CAP, true>(a, row_tiles, stream);
+  else launch<D, CAP, false>(a, row_tiles, stream);
 }
 
 }  // namespace

@@ -564,7 +564,9 @@ def cache_attention(q, cache, table, q_offsets, kv_lens, max_new: int, max_kv: i
     n sees slots 0 .. kv_len - n + i (full=True: all of them); softcap > 0
     caps the scores by softcap * tanh(x / softcap).  Rows that see nothing
     are 0 (lse -inf).  max_new and max_kv bound the rows and cached tokens of
-    a sequence.  -> out [T][q_heads][D], or (out, lse [T][q_heads]).
+    a sequence.  -> out [T][q_heads][D], or (out, lse [T][q_heads]).  FP32
+    outputs take the softmax weights as two BF16 parts; BF16 outputs, except in
+    calls of few rows, as one.
     workspace: a uint8 tensor of cache_attention_workspace_bytes, allocated
     here when not given."""
     _fits(max_new, max_kv)

@@ -95,9 +95,14 @@ fp8bs_status fp8bs_cache_append(const fp8bs_cache* cache, const void* k_new, con
  *   out : BF16 or FP32 [rows][q_heads][D]
  *   lse : FP32 [rows][q_heads], or NULL
  *   workspace : fp8bs_cache_attention_workspace bytes (NULL if 0)
- * Requires q_heads % heads == 0, scale finite, softcap 0 or 2^-126 .. 2^126.  Scores and
- * softmax sums are FP32; the weights enter the product with the values as
- * BF16, in calls of few rows as two BF16 parts.
+ * Requires q_heads % heads == 0, scale finite, softcap 0 or 2^-126 .. 2^126.
+ * Scores and softmax sums are FP32.  The weights enter the product with the
+ * values as two BF16 parts (2^-17 of a weight is lost) where out is FP32, and in
+ * calls of few rows: by max_new and the call's sizes, so that a row's sequence
+ * alone does not decide it.  Elsewhere they are rounded to BF16 once (2^-9),
+ * about the size of the rounding of a BF16 out.  Sums of weight * value are FP32
+ * before they are divided by the sum of the weights: 2^8 times the values'
+ * sizes, added up over a row, has to stay below 2^128.
  */
 fp8bs_status fp8bs_cache_attention(const fp8bs_cache* cache, const void* q, int64_t ld_q, int32_t q_heads,
                                    const int32_t* q_offsets, int64_t rows, int32_t max_new, int32_t max_kv,

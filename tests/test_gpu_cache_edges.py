@@ -5,9 +5,10 @@ import pytest
 import torch
 
 from fp8_block_scaled_04_amd import fp8bs
+from oracle import cache as oracle
 from tests import cache_util
-from tests.gpu_util import f32_dev, i32_dev, require_gpu
-from tests.test_gpu_cache import cache_dev
+from tests.gpu_util import f32_dev, i32_dev, out_host_f64, require_gpu
+from tests.test_gpu_cache import BOUND, abs_values, cache_dev, score_error
 
 pytestmark = pytest.mark.gpu
 
@@ -165,3 +166,35 @@ def test_evict_to_very_many_pages():
     for a in (cache[0], cache[2]):
         x = bits_of(a).view(2, B, 3, H, P, D)
         assert torch.equal(x[1], torch.where(used, x[0], torch.zeros_like(x[0])))
+
+
+# FP32 outputs: the weights meet the codes as two BF16 parts on every kernel.  A
+# part is rounded to nearest, so 2^-18 of a weight is lost (2^-17 taken, doubled
+# for the sum it is divided by); scores as in tests/test_gpu_cache.py.
+FP32_SHAPES = [  # cached tokens, rows, heads, group, D, P, max_new, max_kv
+    ([30] * 12, [30] * 12, 2, 8, 128, 32, 30, BOUND),                          # 256-row tiles
+    ([30] * 12, [30] * 12, 2, 4, 128, 32, 30, BOUND),                          # 128-row tiles
+    ([30] * 12, [30] * 12, 2, 8, 64, 16, 30, BOUND),                           # 128-row tiles of D = 64
+    ([700, 513, 260, 129], [150, 64, 33, 129], 1, 16, 128, 64, 150, 1400),     # splits
+    ([700, 513, 260, 129], [150, 64, 33, 129], 1, 16, 64, 64, 150, 6000),
+    ([300, 128, 129, 90] * 10, [7] * 40, 1, 16, 128, 16, 7, 300),
+    ([250, 200], [250, 200], 2, 40, 64, 64, 250, 250),
+    ([1, 15, 40], [1, 1, 2], 2, 3, 128, 16, 2, 40),                            # 16-row tiles
+]
+
+
+@pytest.mark.parametrize("kv,new,H,G,D,P,max_new,max_kv", FP32_SHAPES)
+def test_fp32_outputs_keep_two_part_weights(kv, new, H, G, D, P, max_new, max_kv):
+    w = cache_util.make(kv, new, H, G, D, P, seed=H + G + D)
+    d = cache_util.dev(w)
+    for cap, full in ((0.0, False), (3.0, False), (0.0, True)):
+        print(f"FP32 outputs H={H} G={G} D={D} P={P} cap={cap} full={full}", flush=True)
+        out = fp8bs.cache_attention(d["q"], cache_dev(d), d["table"], d["q_offsets"], d["kv_lens"], max_new, max_kv,
+                                    D ** -0.5, softcap=cap, full=full, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        args = (w["table"], w["q_offsets"], w["kv_lens"], D ** -0.5, cap, full)
+        ref, _ = oracle.attention(w["q"], cache_util.cache_of(w), *args)
+        size, _ = oracle.attention(w["q"], abs_values(w), *args)
+        tol = (2 * score_error(w, D ** -0.5, cap) + 2.0 ** -16) * size + 1e-30
+        bad = np.abs(out_host_f64(out) - ref) > tol
+        assert not bad.any(), f"{bad.sum()} of {bad.size}, worst {np.max(np.abs(out_host_f64(out) - ref) / tol):.3g}"
