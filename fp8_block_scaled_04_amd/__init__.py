@@ -18,8 +18,8 @@ _PUBLIC = (
     "quantize_1x128", "quantize_transpose_128x1", "quantize_128x128", "quantize_dual",
     "transpose_128x128", "gemm", "gemm_splitk", "gemm_splitk_noalloc", "splitk_workspace_bytes",
     "gemm_fused_quantize", "gemm_wgrad", "grouped_gemm_contiguous", "grouped_gemm_masked",
-    "cache_append", "cache_attention", "cache_attention_workspace_bytes", "cache_attention_weights",
-    "cache_attention_weights_workspace_bytes", "cache_evict",
+    "cache_append", "cache_attention", "cache_attention_tile", "cache_attention_workspace_bytes",
+    "cache_attention_weights", "cache_attention_weights_workspace_bytes", "cache_evict",
     "cast_to_e4m3", "gemm_tile", "stream_reference", "abi_version", "Fp8bsError", "library",
 )
 

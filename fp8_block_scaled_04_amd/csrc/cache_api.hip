@@ -49,6 +49,19 @@ bool bad_scalars(float scale, float softcap) {
   return !std::isfinite(scale) || !(softcap == 0.0f || (softcap >= 0x1p-126f && softcap <= 0x1p126f));
 }
 
+// The plan of an attention call from its sizes; false for sizes it refuses.
+bool attention_plan(const fp8bs_cache& c, int32_t q_heads, int64_t rows, int32_t max_new, int32_t max_kv,
+                    fp8bs::AttendArgs& a) {
+  if (!sizes_fit(c, rows, max_new, max_kv) || q_heads <= 0 ||
+      !query_sizes_fit(c, (int64_t)q_heads * c.dim, q_heads, max_new))
+    return false;
+  a.c = args(c, nullptr, rows, max_new, max_kv);
+  a.q_heads = q_heads;
+  a.group = q_heads / c.heads;
+  attend_plan(a);
+  return attend_items(a) <= fp8bs::kMaxItems;
+}
+
 }  // namespace
 
 extern "C" {
@@ -103,18 +116,17 @@ fp8bs_status fp8bs_cache_attention(const fp8bs_cache* cache, const void* q, int6
 fp8bs_status fp8bs_cache_attention_workspace(const fp8bs_cache* cache, int32_t q_heads, int64_t rows,
                                              int32_t max_new, int32_t max_kv, int64_t* bytes) {
   if (!cache) return FP8BS_ERR_NULL;
-  const fp8bs_cache& c = *cache;
-  if (!sizes_fit(c, rows, max_new, max_kv) || q_heads <= 0 ||
-      !query_sizes_fit(c, (int64_t)q_heads * c.dim, q_heads, max_new))
-    return FP8BS_ERR_SHAPE;
-  if (!bytes) return FP8BS_ERR_NULL;
   fp8bs::AttendArgs a{};
-  a.c = args(c, nullptr, rows, max_new, max_kv);
-  a.q_heads = q_heads;
-  a.group = q_heads / c.heads;
-  attend_plan(a);
+  if (!attention_plan(*cache, q_heads, rows, max_new, max_kv, a)) return FP8BS_ERR_SHAPE;
+  if (!bytes) return FP8BS_ERR_NULL;
   *bytes = attend_workspace_bytes(a);
   return FP8BS_OK;
+}
+
+int32_t fp8bs_cache_attention_tile(const fp8bs_cache* cache, int32_t q_heads, int64_t rows, int32_t max_new,
+                                   int32_t max_kv) {
+  fp8bs::AttendArgs a{};
+  return cache && attention_plan(*cache, q_heads, rows, max_new, max_kv, a) ? a.tile_rows : 0;
 }
 
 fp8bs_status fp8bs_cache_attention_weights(const fp8bs_cache* cache, const void* q, int64_t ld_q, int32_t q_heads,

@@ -70,6 +70,9 @@ _cappend = _sig("fp8bs_cache_append", [_CP, _P, _P, _I64, _P, _I64, _I32, _U32, 
 _cattn = _sig("fp8bs_cache_attention",
               [_CP, _P, _I64, _I32, _P, _I64, _I32, _I32, _F32, _F32, _P, _I32, _P, _U32, _P, _I64, _P])
 _cattn_ws = _sig("fp8bs_cache_attention_workspace", [_CP, _I32, _I64, _I32, _I32, _P])
+_cattn_tile = _lib.fp8bs_cache_attention_tile
+_cattn_tile.argtypes = [_CP, _I32, _I64, _I32, _I32]
+_cattn_tile.restype = _I32
 _cweights = _sig("fp8bs_cache_attention_weights",
                  [_CP, _P, _I64, _I32, _P, _I64, _I32, _I32, _F32, _F32, _P, _P, _P, _I64, _U32, _P, _I64, _P])
 _cweights_ws = _sig("fp8bs_cache_attention_weights_workspace", [_CP, _I32, _I32, _I64, _P])
@@ -555,6 +558,18 @@ def cache_attention_workspace_bytes(cache, table, q_heads: int, rows: int, max_n
     out = ctypes.c_int64(0)
     _check(_cattn_ws(c, q_heads, rows, max_new, max_kv, ctypes.byref(out)), "cache_attention_workspace")
     return int(out.value)
+
+
+def cache_attention_tile(cache, table, q_heads: int, rows: int, max_new: int, max_kv: int) -> int:
+    """Rows per workgroup of the kernel that cache_attention would run on for
+    these sizes: 16 (few rows), 128 or 256; host-side, no device work."""
+    _fits(q_heads, max_new, max_kv)
+    pages, heads, page, dim = cache[0].shape
+    c = _Cache(None, None, None, None, None, None, pages, table.shape[0], table.shape[1], heads, page, dim)
+    tile = _cattn_tile(c, q_heads, rows, max_new, max_kv)
+    if tile == 0:
+        raise ValueError("cache_attention refuses these sizes")
+    return tile
 
 
 def cache_attention(q, cache, table, q_offsets, kv_lens, max_new: int, max_kv: int, scale: float, softcap: float = 0.0,

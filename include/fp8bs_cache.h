@@ -115,6 +115,13 @@ fp8bs_status fp8bs_cache_attention(const fp8bs_cache* cache, const void* q, int6
 fp8bs_status fp8bs_cache_attention_workspace(const fp8bs_cache* cache, int32_t q_heads, int64_t rows,
                                              int32_t max_new, int32_t max_kv, int64_t* bytes);
 
+/* Rows per workgroup of the kernel that a fp8bs_cache_attention call of these
+ * sizes would run on: 16 (few rows), 128 or 256; 0 for sizes that the call
+ * refuses.  Host-side query for tests and tuning; reads only the sizes of
+ * *cache. */
+int32_t fp8bs_cache_attention_tile(const fp8bs_cache* cache, int32_t q_heads, int64_t rows, int32_t max_new,
+                                   int32_t max_kv);
+
 /*
  * The attention weight each cached token received from this call's rows,
  * added to a running sum:

@@ -112,3 +112,26 @@ def test_caps_whose_reciprocal_or_double_overflows_are_refused(lib):
     if NO_DEVICE:
         for cap in (0.0, -0.0, 2.0 ** -126, 30.0, 2.0 ** 126):
             assert both(cap) == (DEVICE, DEVICE), cap
+
+
+def test_attention_tile(lib):
+    f = lib.fp8bs_cache_attention_tile
+    f.argtypes, f.restype = [P, I32, I64, I32, I32], I32
+
+    def tile(q_heads, rows, new, kv, **kw):
+        return f(cache(**kw), q_heads, rows, new, kv)
+    assert f(None, 8, 1, 1, 100) == 0
+    assert tile(6, 1, 1, 100) == tile(0, 1, 1, 100) == tile(8, -1, 1, 100) == tile(8, 1, 1, -1) == tile(8, 1, 1, 1, page=48) == 0
+    # single tokens; few (row, head) pairs; few rows of a sequence
+    assert tile(32, 2, 1, 131072) == tile(32, 128, 64, 128) == tile(32, 40000, 8, 131072, heads=8) == 16
+    assert tile(32, 8000, 8, 131072, dim=64) == tile(8, 4096, 4096, 1024, dim=64) == 16
+    # (eight query heads per key head: 64, 72, 128 and 136 rows)
+    assert tile(32, 8000, 8, 4096, dim=64) == 16 and tile(32, 8000, 9, 4096, dim=64) == 128
+    assert tile(32, 8000, 8, 4096) == 16 and tile(32, 8000, 8, 4096, batch=16) == 128
+    assert tile(32, 8000, 16, 4096) == 128 and tile(32, 8000, 17, 4096) == 256
+    assert tile(32, 8000, 4000, 4096) == 256
+    from fp8_block_scaled_04_amd import fp8bs
+    pool, table = (torch.zeros(4, 8, 16, 128, dtype=torch.uint8),), torch.zeros(2, 6000, dtype=torch.int32)
+    assert fp8bs.cache_attention_tile(pool, table, 32, 8000, 4000, 4096) == 256
+    with pytest.raises(ValueError):
+        fp8bs.cache_attention_tile(pool, table, 30, 8000, 4000, 4096)
