@@ -15,6 +15,7 @@ using fp8bs::check_device;
 using fp8bs::launched;
 
 constexpr int64_t kMaxCount = int64_t(1) << 30;      // slots, rows: 32-bit indexes in the kernels
+constexpr int64_t kMaxPairs = int64_t(1) << 40;      // (row, query head) pairs: bytes of 64 splits stay in 64 bits
 
 bool sizes_fit(const fp8bs_cache& c, int64_t rows, int64_t max_new, int64_t max_kv) {
   if (c.batch < 0 || c.heads <= 0 || c.pages <= 0 || c.table_width <= 0) return false;
@@ -24,9 +25,9 @@ bool sizes_fit(const fp8bs_cache& c, int64_t rows, int64_t max_new, int64_t max_
   return rows >= 0 && rows <= kMaxCount && max_new >= 0 && max_new <= kMaxCount && max_kv >= 0 && max_kv <= kMaxCount;
 }
 
-bool query_sizes_fit(const fp8bs_cache& c, int64_t ld, int32_t q_heads, int64_t max_new) {
+bool query_sizes_fit(const fp8bs_cache& c, int64_t ld, int32_t q_heads, int64_t rows, int64_t max_new) {
   return q_heads > 0 && q_heads % c.heads == 0 && ld >= (int64_t)q_heads * c.dim && ld % 8 == 0 &&
-         max_new * q_heads <= kMaxCount;
+         max_new * q_heads <= kMaxCount && rows * q_heads <= kMaxPairs;
 }
 
 CacheArgs args(const fp8bs_cache& c, const int32_t* q_offsets, int64_t rows, int32_t max_new, int32_t max_kv) {
@@ -53,7 +54,7 @@ bool bad_scalars(float scale, float softcap) {
 bool attention_plan(const fp8bs_cache& c, int32_t q_heads, int64_t rows, int32_t max_new, int32_t max_kv,
                     fp8bs::AttendArgs& a) {
   if (!sizes_fit(c, rows, max_new, max_kv) || q_heads <= 0 ||
-      !query_sizes_fit(c, (int64_t)q_heads * c.dim, q_heads, max_new))
+      !query_sizes_fit(c, (int64_t)q_heads * c.dim, q_heads, rows, max_new))
     return false;
   a.c = args(c, nullptr, rows, max_new, max_kv);
   a.q_heads = q_heads;
@@ -90,7 +91,7 @@ fp8bs_status fp8bs_cache_attention(const fp8bs_cache* cache, const void* q, int6
                                    uint32_t flags, void* workspace, int64_t workspace_bytes, fp8bs_stream_t stream) {
   if (!cache) return FP8BS_ERR_NULL;
   const fp8bs_cache& c = *cache;
-  if (!sizes_fit(c, rows, max_new, max_kv) || !query_sizes_fit(c, ld_q, q_heads, max_new)) return FP8BS_ERR_SHAPE;
+  if (!sizes_fit(c, rows, max_new, max_kv) || !query_sizes_fit(c, ld_q, q_heads, rows, max_new)) return FP8BS_ERR_SHAPE;
   fp8bs::AttendArgs a{args(c, q_offsets, rows, max_new, max_kv), q, ld_q, q_heads, q_heads / c.heads, scale, softcap,
                       out, lse, out_dtype == FP8BS_OUT_FP32, (flags & FP8BS_MASK_FULL) != 0, 16, 0, 1, nullptr,
                       nullptr};
@@ -136,7 +137,7 @@ fp8bs_status fp8bs_cache_attention_weights(const fp8bs_cache* cache, const void*
                                            int64_t workspace_bytes, fp8bs_stream_t stream) {
   if (!cache) return FP8BS_ERR_NULL;
   const fp8bs_cache& c = *cache;
-  if (!sizes_fit(c, rows, max_new, max_kv) || !query_sizes_fit(c, ld_q, q_heads, max_new)) return FP8BS_ERR_SHAPE;
+  if (!sizes_fit(c, rows, max_new, max_kv) || !query_sizes_fit(c, ld_q, q_heads, rows, max_new)) return FP8BS_ERR_SHAPE;
   if (acc_slots < max_kv || acc_slots > kMaxCount) return FP8BS_ERR_SHAPE;
   fp8bs::WeightArgs a{args(c, q_offsets, rows, max_new, max_kv), q, ld_q, q_heads, q_heads / c.heads, scale, softcap,
                       lse, acc_in, acc_out, acc_slots, (flags & FP8BS_MASK_FULL) != 0, 0, nullptr};
@@ -161,7 +162,7 @@ fp8bs_status fp8bs_cache_attention_weights_workspace(const fp8bs_cache* cache, i
   if (!cache) return FP8BS_ERR_NULL;
   const fp8bs_cache& c = *cache;
   if (!sizes_fit(c, 0, max_new, 0) || q_heads <= 0 || acc_slots < 0 || acc_slots > kMaxCount ||
-      !query_sizes_fit(c, (int64_t)q_heads * c.dim, q_heads, max_new))
+      !query_sizes_fit(c, (int64_t)q_heads * c.dim, q_heads, 0, max_new))
     return FP8BS_ERR_SHAPE;
   if (!bytes) return FP8BS_ERR_NULL;
   fp8bs::WeightArgs a{};

@@ -30,11 +30,12 @@
  *
  * Checks.  Sizes (FP8BS_ERR_SHAPE): batch, rows, max_new, max_kv >= 0; pages,
  * table_width, heads >= 1; rows, table_width * P and max_new * q_heads at most
- * 2^30, and no more work per sequence than one launch holds (2^32 work-items:
- * of the smallest pages 2^27 / heads new tokens appended or kept, 2^32 / heads
- * slots of sums); P and D as above; the rules of each call.  Flags, dtypes and
- * scalars (FP8BS_ERR_FLAGS).  Alignment: 16 bytes for codes, BF16 data, out and
- * workspace, 4 for scales, sums, lse and the INT32 arrays.
+ * 2^30, rows * q_heads at most 2^40, and no more work per sequence than one
+ * launch holds (2^32 work-items: of the smallest pages 2^27 / heads new tokens
+ * appended or kept, 2^32 / heads slots of sums); P and D as above; the rules of
+ * each call.  Flags, dtypes and scalars (FP8BS_ERR_FLAGS).  Alignment: 16 bytes
+ * for codes, BF16 data, out and workspace, 4 for scales, sums, lse and the INT32
+ * arrays.
  */
 #ifndef FP8BS_CACHE_H
 #define FP8BS_CACHE_H

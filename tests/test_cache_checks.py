@@ -135,3 +135,19 @@ def test_attention_tile(lib):
     assert fp8bs.cache_attention_tile(pool, table, 32, 8000, 4000, 4096) == 256
     with pytest.raises(ValueError):
         fp8bs.cache_attention_tile(pool, table, 30, 8000, 4000, 4096)
+
+
+def test_attention_workspace_bytes_do_not_overflow(lib):
+    # 64 splits of 2^50 (row, query head) pairs: 2^65 bytes
+    ws = fn(lib, "fp8bs_cache_attention_workspace", [P, I32, I64, I32, I32, P])
+    f = fn(lib, "fp8bs_cache_attention", [P, P, I64, I32, P, I64, I32, I32, F32, F32, P, I32, P, U32, P, I64, P])
+    n = I64(-1)
+    for lg in range(8, 31):
+        status = ws(cache(batch=1, heads=1), 1 << lg, 1 << 30, 1, 1 << 30, ctypes.byref(n))
+        if lg <= 10:
+            one = (1 << 30 + lg) * 130 * 4
+            assert status == OK and n.value % one == 0 and 1 < n.value // one <= 64
+        else:
+            assert status == SHAPE
+            assert f(cache(batch=1, heads=1), FAKE, 128 << lg, 1 << lg, FAKE, 1 << 30, 1, 1 << 30, 0.1, 0.0, FAKE, 0, None,
+                     0, FAKE, 1 << 62, None) == SHAPE
