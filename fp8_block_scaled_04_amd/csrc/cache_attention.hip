@@ -23,7 +23,7 @@ namespace fp8bs {
 namespace {
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves, kStep = 32;
-constexpr int kMaxSplits = 64;
+constexpr int kMaxSplits = 64;                       // (with fewer than 12 pairs the chip is then not full)
 
 template <int D, bool CAP>
 __global__ __launch_bounds__(kThreads) void k_attend_rows(AttendArgs a, int row_tiles) {

@@ -17,11 +17,13 @@
 // vector slots are free: keys of step t + 1 and values of step t are converted
 // and written there, the codes of the next ones requested.
 //
-// Two causal prompts of up to 6000 tokens (8 heads x 4, D = 128) take 450 us, 937
-// TFLOP/s (a BF16 library product of 8192^3: 1207).  The matrix core is busy
-// 41 % of the time and the vector unit 60 %; either alone would need about 180
-// and 270 us.  D = 64 with capped scores (four 513-token chunks behind up to
-// 9000) takes 192 us, the vector unit busy 60 %.
+// Two causal prompts of up to 6000 tokens (8 heads x 4, D = 128) take 460 us, 917
+// TFLOP/s (450 to 473 us over several cards; a BF16 library product of 8192^3:
+// 1207).  The matrix core is busy 41 % of the time and the vector unit 60 %:
+// either alone would need about 180 and 270 us, so they hardly overlap in effect.
+// D = 64 with capped scores (four 513-token chunks behind up to 9000) takes 190
+// us: the vector unit is busy 60 % and waves wait 38 % of the time, beside 35
+// spilled registers.
 #include "cache_device.h"
 
 namespace fp8bs {

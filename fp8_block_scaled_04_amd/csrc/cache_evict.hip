@@ -11,9 +11,10 @@
 // then, and the copies take their counts from the kept slots, so both may be one
 // array.
 //
-// The move is HBM bound: 16 sequences cut to 4096 tokens (8 heads of 128) in 59
-// us, 262 MB at 4.4 TB/s; the search before it takes 18 us of latency (its reads
-// 2, each counted digit 3, ranks 4, what it writes 6), 7.5 us for 3 short ones.
+// The move is HBM bound: 16 sequences cut to 4096 tokens (8 heads of 128) in 60
+// us, 262 MB at 4.4 TB/s (59 with counts from the lengths); the search before it
+// takes 17.5 us of latency (its reads 2, each counted digit 3, ranks 4, what it
+// writes 6), 7.5 us for 3 short ones.
 #include "cache_device.h"
 
 namespace fp8bs {

@@ -18,7 +18,14 @@
 // round of loads, whose latency the table entries and old sums no longer add
 // to (56 us before).  k_weights_tiles takes the matrix core 2 D flops and the
 // vector unit a multiply-add, an exponential and an addition per pair: 67
-// GFLOP of a 3500-token prompt in 96 us with the join, 700 TFLOP/s.
+// GFLOP of a 3500-token prompt in 96 us with the join, 700 TFLOP/s; its capped
+// form at D = 128 (168 us) spills 18 registers.
+//
+// Everything is FP32.  k_weights_tiles takes lse to base 2 once per row and keeps
+// one running sum per slot over a run's rows, where an exact lse - x and a sum in
+// parts would cost the loop another operation or register per score: sums of a
+// 3500-token prompt are 2.0e-7 from exact, those of separate FP32 torch
+// operations 6.4e-8.
 #include "cache_device.h"
 
 namespace fp8bs {
