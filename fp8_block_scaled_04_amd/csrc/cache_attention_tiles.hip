@@ -71,9 +71,10 @@ constexpr int kPerSimd = D == 64 && !TWO ? 3 : 2;
 // rounding of a BF16 output takes again.  TWO (FP32 outputs): as two BF16 parts,
 // the second being what the first leaves, so that 2^-18 of it is lost; a step's
 // outputs are then added before the scores of the next one.  The second products
-// cost: prompts of up to 6000 tokens 603 us instead of 450, 25-token rows of 32
-// sequences behind 4096 (D = 128, whose 128-row form spills 38 registers) 162
-// instead of 86, the 513-token chunks (D = 64) 244 instead of 190.
+// cost: prompts of up to 6000 tokens 603 us instead of 450, 25 tokens of each of 32
+// sequences behind 4096 (D = 128, 128 rows) 162 instead of 86 (168 with one wave
+// per SIMD and without the 38 spilled registers), the 513-token chunks (D = 64)
+// 244 instead of 190.
 template <int D, bool CAP, int WAVES, bool TWO>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(kPerSimd<D, TWO>, kPerSimd<D, TWO>)))
 void k_attend_tiles(AttendArgs a, int row_tiles) {
