@@ -1,0 +1,245 @@
+// Residual addition, RMS norm and 1x128 quantization, and the norm's gradients
+// (include/fp8bs_layer.h, fp8bs_rms_norm_quantize and fp8bs_rms_norm_backward).
+//
+// One workgroup per row at a time, the row in registers: sixteen lanes hold one
+// 1x128 tile, eight values each, so the row's sum needs one pass through LDS and
+// a tile's largest value four DPP steps.  HBM-bound.
+#include <algorithm>
+
+#include "layer.h"
+#include "quant_common.h"
+
+namespace fp8bs {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// The eight values of piece p (values 8 p .. 8 p + 7) of a BF16 row, still packed.
+__device__ __forceinline__ u32x4 piece(const void* row, int p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row) + p);
+}
+__device__ __forceinline__ void put_piece(void* row, int p, u32x4 v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(row) + p);
+}
+__device__ __forceinline__ void unpack8(float (&f)[8], u32x4 v) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[2 * e] = bf16_lo(v[e]), f[2 * e + 1] = bf16_hi(v[e]);
+}
+__device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
+  return u32x4{pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7])};
+}
+// Norm weights of a piece, BF16 or FP32.
+__device__ __forceinline__ void weight8(float (&f)[8], const void* weight, bool f32, int p) {
+  if (f32) {
+    const float4* w = static_cast<const float4*>(weight) + 2 * p;
+    const float4 a = w[0], b = w[1];
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  } else {
+    unpack8(f, static_cast<const u32x4*>(weight)[p]);
+  }
+}
+
+// Sum over the workgroup, the same order on every lane and call.  `red` has 16
+// floats of its own for each of two calls in a row: a wave may still read the
+// last call's while another writes this one's.
+__device__ __forceinline__ float group_sum(float v, float* red) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+  const int waves = blockDim.x / 64;
+  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = v;
+  __syncthreads();
+  float t = 0.0f;
+  for (int w = 0; w < waves; ++w) t += red[w];
+  return t;
+}
+
+// V: pieces per lane.
+template <int V, bool POW2>
+__global__ __launch_bounds__(1024) void k_rms_norm(NormArgs a) {
+  __shared__ float red[2][16];
+  const int pieces = a.K / 8, threads = blockDim.x, tid = threadIdx.x;
+  float w[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int p = v * threads + tid;
+    if (p < pieces) weight8(w[v], a.weight, a.weight_f32, p);
+  }
+  int turn = 0;
+  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
+    const int64_t at = m * a.K;
+    const uint16_t* xr = static_cast<const uint16_t*>(a.x) + at;
+    const uint16_t* rr = static_cast<const uint16_t*>(a.residual) + at;
+    u32x4 x[V], r[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = v * threads + tid;
+      x[v] = r[v] = u32x4{0u, 0u, 0u, 0u};
+      if (p < pieces) {
+        x[v] = piece(xr, p);
+        if (a.residual) r[v] = piece(rr, p);
+      }
+    }
+    float h[V][8], sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      unpack8(h[v], x[v]);
+      if (a.residual) {
+        // the stored sum is BF16, and the norm is that of the stored sum (what
+        // the backward pass and the next layer see)
+        float f[8];
+        unpack8(f, r[v]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] += h[v][e];
+        const u32x4 b = pack8(f);
+        unpack8(h[v], b);
+        const int p = v * threads + tid;
+        if (p < pieces) put_piece(static_cast<uint16_t*>(a.h) + at, p, b);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(h[v][e], h[v][e], sum);
+    }
+    const float rstd = 1.0f / sqrtf(group_sum(sum, red[turn]) / (float)a.K + a.eps);
+    if (a.rstd && tid == 0) a.rstd[m] = rstd;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = v * threads + tid;
+      if (p >= pieces) break;                        // (all sixteen lanes of a tile or none)
+      float amax = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        h[v][e] = h[v][e] * rstd * w[v][e];
+        amax = fmaxf(amax, __builtin_fabsf(h[v][e]));
+      }
+      if (a.y) put_piece(static_cast<uint16_t*>(a.y) + at, p, pack8(h[v]));
+      const TileScale t = tile_scale<POW2>(row16_max(amax));
+      if (tid % 16 == 0) a.s[(int64_t)(p / 16) * a.M + m] = t.s;
+      float c[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] = quot<POW2>(h[v][e] * t.sx, t);
+      // (ordinary stores: the product that reads the codes comes next)
+      *reinterpret_cast<uint2*>(a.q + at + (int64_t)p * 8) =
+          make_uint2(pack4_e4m3(c[0], c[1], c[2], c[3]), pack4_e4m3(c[4], c[5], c[6], c[7]));
+    }
+  }
+}
+
+// Row group g takes rows g, g + groups, ...; its sums for dweight stay in
+// registers and leave as one partial row.
+template <int V>
+__global__ __launch_bounds__(1024) void k_rms_norm_back(NormBackArgs a) {
+  __shared__ float red[2][16];
+  const int pieces = a.K / 8, threads = blockDim.x, tid = threadIdx.x;
+  float w[V][8], dw[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int p = v * threads + tid;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[v][e] = dw[v][e] = 0.0f;
+    if (p < pieces) weight8(w[v], a.weight, a.weight_f32, p);
+  }
+  int turn = 0;
+  for (int64_t m = blockIdx.x; m < a.M; m += a.groups, turn ^= 1) {
+    const int64_t at = m * a.K;
+    u32x4 dyp[V], hp[V], dhp[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = v * threads + tid;
+      dyp[v] = hp[v] = dhp[v] = u32x4{0u, 0u, 0u, 0u};
+      if (p < pieces) {
+        dyp[v] = piece(static_cast<const uint16_t*>(a.dy) + at, p);
+        hp[v] = piece(static_cast<const uint16_t*>(a.h) + at, p);
+        if (a.dh) dhp[v] = piece(static_cast<const uint16_t*>(a.dh) + at, p);
+      }
+    }
+    const float rstd = a.rstd[m];
+    float g[V][8], n[V][8], dot = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      unpack8(g[v], dyp[v]);
+      unpack8(n[v], hp[v]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        n[v][e] *= rstd;
+        dw[v][e] = __builtin_fmaf(g[v][e], n[v][e], dw[v][e]);
+        g[v][e] *= w[v][e];
+        dot = __builtin_fmaf(g[v][e], n[v][e], dot);
+      }
+    }
+    const float mean = group_sum(dot, red[turn]) / (float)a.K;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = v * threads + tid;
+      if (p >= pieces) break;
+      float d[8];
+      unpack8(d, dhp[v]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] = __builtin_fmaf(rstd, __builtin_fmaf(-n[v][e], mean, g[v][e]), d[e]);
+      put_piece(static_cast<uint16_t*>(a.dx) + at, p, pack8(d));
+    }
+  }
+  float* part = a.part + (int64_t)blockIdx.x * a.K;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int p = v * threads + tid;
+    if (p >= pieces) break;
+    reinterpret_cast<float4*>(part)[2 * p] = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
+    reinterpret_cast<float4*>(part)[2 * p + 1] = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+  }
+}
+
+// dweight = the groups' partial rows added up; 16 lanes of four columns, 16
+// runs of groups.
+__global__ __launch_bounds__(256) void k_rms_norm_dweight(const float* part, int groups, int K, float* dweight,
+                                                          bool accumulate) {
+  __shared__ float4 red[16][16];
+  const int c = threadIdx.x % 16, r = threadIdx.x / 16;
+  const int col = (blockIdx.x * 16 + c) * 4;         // (K is a multiple of 64)
+  float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int g = r; g < groups; g += 16) {
+    const float4 p = *reinterpret_cast<const float4*>(part + (int64_t)g * K + col);
+    t.x += p.x, t.y += p.y, t.z += p.z, t.w += p.w;
+  }
+  red[r][c] = t;
+  __syncthreads();
+  if (r) return;
+  for (int i = 1; i < 16; ++i) t.x += red[i][c].x, t.y += red[i][c].y, t.z += red[i][c].z, t.w += red[i][c].w;
+  float4* out = reinterpret_cast<float4*>(dweight + col);
+  if (accumulate) t.x += out->x, t.y += out->y, t.z += out->z, t.w += out->w;
+  *out = t;
+}
+
+// Pieces per lane, and the lanes, that hold a row.
+struct Shape {
+  int v, threads;
+};
+Shape shape_of(int K) {
+  const int lanes = K / 8;
+  const int v = lanes <= 256 ? 1 : 2;
+  return {v, (lanes + 64 * v - 1) / (64 * v) * 64};
+}
+
+}  // namespace
+
+int32_t norm_back_groups(int64_t M, int64_t) { return (int32_t)std::min<int64_t>(M, 512); }
+
+hipError_t launch_rms_norm(const NormArgs& a, bool pow2, hipStream_t stream) {
+  const Shape s = shape_of(a.K);
+  const unsigned grid = (unsigned)std::min<int64_t>(a.M, 1 << 20);
+  const auto k = pow2 ? (s.v == 1 ? k_rms_norm<1, true> : k_rms_norm<2, true>)
+                      : (s.v == 1 ? k_rms_norm<1, false> : k_rms_norm<2, false>);
+  k<<<grid, s.threads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_rms_norm_back(const NormBackArgs& a, hipStream_t stream) {
+  if (a.groups) {
+    const Shape s = shape_of(a.K);
+    const auto k = s.v == 1 ? k_rms_norm_back<1> : k_rms_norm_back<2>;
+    k<<<a.groups, s.threads, 0, stream>>>(a);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  k_rms_norm_dweight<<<a.K / 64, 256, 0, stream>>>(a.part, a.groups, a.K, a.dweight, a.accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace fp8bs

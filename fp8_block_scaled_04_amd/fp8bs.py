@@ -77,6 +77,15 @@ _cweights = _sig("fp8bs_cache_attention_weights",
                  [_CP, _P, _I64, _I32, _P, _I64, _I32, _I32, _F32, _F32, _P, _P, _P, _I64, _U32, _P, _I64, _P])
 _cweights_ws = _sig("fp8bs_cache_attention_weights_workspace", [_CP, _I32, _I32, _I64, _P])
 _cevict = _sig("fp8bs_cache_evict", [_CP, _P, _I64, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P])
+_norm = _sig("fp8bs_rms_norm_quantize", [_P, _P, _P, _I32, _F32, _I64, _I64, _P, _P, _P, _P, _P, _U32, _P])
+_norm_back = _sig("fp8bs_rms_norm_backward",
+                  [_P, _P, _P, _P, _I32, _P, _I64, _I64, _P, _P, _I32, _P, _I64, _P])
+_norm_back_ws = _sig("fp8bs_rms_norm_backward_workspace", [_I64, _I64, _P])
+_route = _sig("fp8bs_moe_route", [_P, _I32, _I64, _I32, _I32, _P, _P, _U32, _P])
+_route_back = _sig("fp8bs_moe_route_backward", [_P, _I32, _P, _P, _I64, _I32, _I32, _P, _U32, _P])
+_experts = _sig("fp8bs_moe_experts",
+                [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _P, _I64, _P])
+_experts_ws = _sig("fp8bs_moe_experts_workspace", [_I64, _I64, _I64, _I32, _I32, _P])
 _lib.fp8bs_status_str.argtypes = [ctypes.c_int]
 _lib.fp8bs_status_str.restype = ctypes.c_char_p
 _lib.fp8bs_abi_version.argtypes = []
@@ -84,6 +93,7 @@ _lib.fp8bs_abi_version.restype = ctypes.c_int32
 
 SCALE_POW2 = 1
 MASK_FULL = 2
+ROUTE_RENORM = 4
 OUT_BF16, OUT_FP32 = 0, 1
 
 
@@ -528,7 +538,7 @@ def _workspace(workspace, need, dev):
             return None, None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != dev:
-        raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
+        raise ValueError("workspace must be a contiguous uint8 tensor on the operands' device")
     return workspace, workspace.data_ptr(), workspace.numel()
 
 
@@ -670,6 +680,198 @@ def cache_evict(acc, cache, table, dst_table, kv_lens, max_kv: int, budget: int,
     _check(_cevict(c, acc.data_ptr(), slots, dst_table.data_ptr(), dst_table.shape[1], max_kv, budget, recent,
                    kept.data_ptr(), lens.data_ptr(), acc_out.data_ptr(), _stream_of(dev)), "cache_evict")
     return kept, lens, acc_out
+
+
+# ---- norm, router and experts (include/fp8bs_layer.h) ----
+
+
+def _launch(dev, f, where, *args):
+    """f(*args, stream) on GPU `dev` and its current stream."""
+    if torch.cuda.current_device() == dev:
+        status = f(*args, _stream_of(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, _stream_of(dev))
+    if status:
+        raise Fp8bsError(status, where)
+
+
+def _device_of(t, name):
+    """GPU of the tensor that a call goes by."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return dev
+
+
+def _shaped(t, name, dtype, shape, dev):
+    """A dense tensor of this type and shape on GPU `dev`."""
+    _on(t, name, dtype, len(shape), dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _type_code(t, name):
+    if t.dtype is torch.bfloat16:
+        return 0
+    if t.dtype is torch.float32:
+        return 1
+    raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+
+
+def rms_norm_quantize(x, weight, eps: float = 1e-6, residual=None, pow2: bool = False, return_y: bool = False, h=None):
+    """Adds the residual, takes the RMS norm and quantizes it 1x128: h = x +
+    residual in BF16, rstd = 1 / sqrt(mean(h^2) + eps), y = h rstd weight.
+    x, residual: BF16 [M][K]; weight: BF16 or FP32 [K].
+    -> (q [M][K] E4M3, s [K/128][M], h, rstd [M]), with y (BF16) as a fifth
+    where return_y is set.  Without a residual h is x itself.  h: the tensor
+    that takes the sum; may be x or residual (in place)."""
+    dev = _device_of(x, "x")
+    _on(x, "x", torch.bfloat16, 2, dev)
+    M, K = x.shape
+    code = _type_code(weight, "weight")
+    _shaped(weight, "weight", weight.dtype, (K,), dev)
+    if residual is not None:
+        _shaped(residual, "residual", torch.bfloat16, x.shape, dev)
+        if h is None:
+            h = torch.empty_like(x)
+        else:
+            _shaped(h, "h", torch.bfloat16, x.shape, dev)
+    elif h is not None:
+        raise ValueError("h is the sum with a residual: give one")
+    q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
+    s = torch.empty((K // 128, M), dtype=torch.float32, device=x.device)
+    rstd = torch.empty((M,), dtype=torch.float32, device=x.device)
+    y = torch.empty_like(x) if return_y else None
+    _launch(dev, _norm, "rms_norm_quantize", x.data_ptr(), residual.data_ptr() if residual is not None else None,
+            weight.data_ptr(), code, eps, M, K, h.data_ptr() if h is not None else None,
+            y.data_ptr() if return_y else None, q.data_ptr(), s.data_ptr(), rstd.data_ptr(), SCALE_POW2 if pow2 else 0)
+    h = x if h is None else h
+    return (q, s, h, rstd, y) if return_y else (q, s, h, rstd)
+
+
+def rms_norm_backward_workspace_bytes(M: int, K: int) -> int:
+    """Workspace bytes of rms_norm_backward for [M][K]."""
+    out = ctypes.c_int64(0)
+    _check(_norm_back_ws(M, K, ctypes.byref(out)), "rms_norm_backward_workspace")
+    return int(out.value)
+
+
+def rms_norm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, accumulate: bool = False, workspace=None):
+    """Gradients of the norm: dy [M][K] of y (the quantization passed through),
+    h and rstd of rms_norm_quantize, dh what reaches h by other ways.
+    -> (dx BF16 [M][K], of x and of the residual alike; dweight FP32 [K]).
+    dx: the tensor that takes it; may be dy or dh (in place).  accumulate=True
+    adds to dweight.  workspace: a uint8 tensor of
+    rms_norm_backward_workspace_bytes, allocated here when not given."""
+    dev = _device_of(h, "h")
+    _on(h, "h", torch.bfloat16, 2, dev)
+    M, K = h.shape
+    _shaped(dy, "dy", torch.bfloat16, h.shape, dev)
+    _shaped(rstd, "rstd", torch.float32, (M,), dev)
+    code = _type_code(weight, "weight")
+    _shaped(weight, "weight", weight.dtype, (K,), dev)
+    if dh is not None:
+        _shaped(dh, "dh", torch.bfloat16, h.shape, dev)
+    if dx is None:
+        dx = torch.empty_like(h)
+    else:
+        _shaped(dx, "dx", torch.bfloat16, h.shape, dev)
+    if dweight is None:
+        if accumulate:
+            raise ValueError("accumulate needs an existing dweight")
+        dweight = torch.empty((K,), dtype=torch.float32, device=h.device)
+    else:
+        _shaped(dweight, "dweight", torch.float32, (K,), dev)
+    workspace, ws, ws_bytes = _workspace(workspace, rms_norm_backward_workspace_bytes(M, K), dev)
+    _launch(dev, _norm_back, "rms_norm_backward", dy.data_ptr(), h.data_ptr(), rstd.data_ptr(), weight.data_ptr(), code,
+            dh.data_ptr() if dh is not None else None, M, K, dx.data_ptr(), dweight.data_ptr(), 1 if accumulate else 0,
+            ws, ws_bytes)
+    return dx, dweight
+
+
+def moe_route(logits, topk: int, renormalize: bool = True):
+    """The topk experts of each token by logits [T][E] (BF16 or FP32), largest
+    first (ties: the lowest index), and their softmax weights: over the chosen
+    ones (renormalize) or over all.  An expert of logit -inf or NaN is never
+    chosen; places without one get id -1 and weight 0.
+    -> (ids int32 [T][topk], weights FP32 [T][topk])"""
+    dev = _device_of(logits, "logits")
+    code = _type_code(logits, "logits")
+    _on(logits, "logits", logits.dtype, 2, dev)
+    T, E = logits.shape
+    _fits(E, topk)
+    if topk < 1 or topk > E:
+        raise ValueError(f"topk must be 1 .. {E}, got {topk}")
+    ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
+    _launch(dev, _route, "moe_route", logits.data_ptr(), code, T, E, topk, ids.data_ptr(), weights.data_ptr(),
+            ROUTE_RENORM if renormalize else 0)
+    return ids, weights
+
+
+def moe_route_backward(logits, ids, dweights, renormalize: bool = True):
+    """Gradient of moe_route's weights: dweights FP32 [T][topk] -> dlogits
+    [T][E] of the logits' type, the choice (ids) held fixed."""
+    dev = _device_of(logits, "logits")
+    code = _type_code(logits, "logits")
+    _on(logits, "logits", logits.dtype, 2, dev)
+    T, E = logits.shape
+    _on(ids, "ids", torch.int32, 2, dev)
+    if ids.shape[0] != T:
+        raise ValueError(f"ids must have {T} rows, got {ids.shape[0]}")
+    _fits(E, ids.shape[1])
+    _shaped(dweights, "dweights", torch.float32, ids.shape, dev)
+    out = torch.empty_like(logits)
+    _launch(dev, _route_back, "moe_route_backward", logits.data_ptr(), code, ids.data_ptr(), dweights.data_ptr(), T, E,
+            ids.shape[1], out.data_ptr(), ROUTE_RENORM if renormalize else 0)
+    return out
+
+
+def moe_experts_workspace_bytes(T: int, H: int, I: int, E: int, topk: int) -> int:
+    """Workspace bytes of moe_experts for T tokens of width H, E experts of
+    inner width I."""
+    _fits(E, topk)
+    out = ctypes.c_int64(0)
+    _check(_experts_ws(T, H, I, E, topk, ctypes.byref(out)), "moe_experts_workspace")
+    return int(out.value)
+
+
+def moe_experts(x, sx, ids, weights, w13, s13, w2, s2, out_dtype=torch.bfloat16, out=None, workspace=None):
+    """The experts of a few tokens (at most 128): x E4M3 [T][H] with 1x128
+    scales sx [H/128][T]; ids int32 and weights FP32 [T][topk]; w13 E4M3
+    [E][2 I][H] (gate rows, then up rows) and w2 [E][H][I] with 128x128 block
+    scales s13 [E][2 I/128][H/128], s2 [E][H/128][I/128].
+    -> [T][H], the sum over a token's experts of
+    weight * w2 (silu(gate x) * (up x)).  Ids outside [0, E) are left out;
+    tokens without an expert get 0.  workspace: a uint8 tensor of
+    moe_experts_workspace_bytes, allocated here when not given."""
+    _codes(x, "x"); _codes(w13, "w13"); _codes(w2, "w2")
+    dev = _device_of(x, "x")
+    _on(x, "x", x.dtype, 2, dev)
+    _on(w13, "w13", w13.dtype, 3, dev)
+    _on(ids, "ids", torch.int32, 2, dev)
+    T, H = x.shape
+    E, I = w13.shape[0], w13.shape[1] // 2
+    topk = ids.shape[1]
+    if w13.shape[2] != H or w13.shape[1] != 2 * I or H % 128 or I % 128:
+        raise ValueError(f"w13 must be [E][2 I][{H}], the widths multiples of 128, got {tuple(w13.shape)}")
+    _shaped(sx, "sx", torch.float32, (H // 128, T), dev)
+    _shaped(ids, "ids", torch.int32, (T, topk), dev)
+    _shaped(weights, "weights", torch.float32, (T, topk), dev)
+    _shaped(s13, "s13", torch.float32, (E, 2 * I // 128, H // 128), dev)
+    _shaped(w2, "w2", w2.dtype, (E, H, I), dev)
+    _shaped(s2, "s2", torch.float32, (E, H // 128, I // 128), dev)
+    code = _out_code(out_dtype)
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype, device=x.device)
+    else:
+        _shaped(out, "out", out_dtype, (T, H), dev)
+    workspace, ws, ws_bytes = _workspace(workspace, moe_experts_workspace_bytes(T, H, I, E, topk), dev)
+    _launch(dev, _experts, "moe_experts", x.data_ptr(), sx.data_ptr(), ids.data_ptr(), weights.data_ptr(),
+            w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), out.data_ptr(), T, H, I, E, topk, code, ws,
+            ws_bytes)
+    return out
 
 
 GEMM_LAYOUTS = {"dense": 0, "contiguous": 1, "masked": 2, "wgrad": 3, "fused_quantize": 4}

@@ -1,0 +1,153 @@
+"""Argument checks of the norm, router and expert calls (include/fp8bs_layer.h)
+and of their binding, without a GPU: the documented status comes back before the
+HIP runtime is touched."""
+
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "fp8bs_layer.h")
+OK, NULL, SHAPE, ALIGN, FLAGS, DEVICE, LAUNCH = range(7)
+P = ctypes.c_void_p
+I64, I32, U32, F32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_float
+FAKE, MIS, ODD = 0x10000, 0x10008, 0x10002
+NO_DEVICE = torch.cuda.device_count() == 0
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module")
+def lib(lib_path):
+    return ctypes.CDLL(lib_path)
+
+
+def caller(lib, name, args, good):
+    """f(**changes): the call with good arguments but for the changes; a stream
+    of NULL at the end."""
+    f = getattr(lib, name)
+    f.argtypes, f.restype = args, ctypes.c_int
+
+    def call(**kw):
+        assert not set(kw) - set(good)
+        return f(*[kw.get(k, v) for k, v in good.items()])
+    return call
+
+
+def test_every_declared_symbol_is_exported(lib):
+    names = sorted(set(re.findall(r"^fp8bs_status (fp8bs_\w+)\s*\(", open(HEADER).read(), re.M)))
+    assert len(names) == 7, names
+    for n in names:
+        assert hasattr(lib, n), n
+
+
+def test_norm(lib):
+    call = caller(lib, "fp8bs_rms_norm_quantize", [P, P, P, I32, F32, I64, I64, P, P, P, P, P, U32, P],
+                  dict(x=FAKE, r=FAKE, w=FAKE, wt=0, eps=1e-6, M=3, K=256, h=FAKE, y=FAKE, q=FAKE, s=FAKE, rstd=FAKE,
+                       flags=0, stream=None))
+    for bad in (dict(M=-1), dict(M=1 << 31), dict(K=0), dict(K=-128), dict(K=192), dict(K=16384 + 128)):
+        assert call(**bad) == SHAPE, bad
+    for bad in (dict(flags=2), dict(flags=4), dict(wt=2), dict(wt=-1), dict(eps=0.0), dict(eps=-1e-6), dict(eps=INF),
+                dict(eps=NAN), dict(eps=1e-39)):
+        assert call(**bad) == FLAGS, bad
+    assert call(M=0, x=None, q=None, w=None, s=None) == OK
+    for bad in (dict(x=None), dict(w=None), dict(q=None), dict(s=None), dict(r=None), dict(h=None)):
+        assert call(**bad) == NULL, bad
+    for bad in (dict(x=MIS), dict(r=MIS), dict(w=MIS), dict(h=MIS), dict(y=MIS), dict(q=MIS), dict(s=MIS), dict(rstd=ODD)):
+        assert call(**bad) == ALIGN, bad
+    if NO_DEVICE:
+        assert call() == DEVICE and call(r=None, h=None, y=None, rstd=None, wt=1, flags=1, K=16384) == DEVICE
+
+
+def test_norm_backward(lib):
+    ws = getattr(lib, "fp8bs_rms_norm_backward_workspace")
+    ws.argtypes, ws.restype = [I64, I64, P], ctypes.c_int
+    n = I64(-1)
+    assert ws(0, 256, ctypes.byref(n)) == OK and n.value == 0
+    assert ws(1 << 30, 256, ctypes.byref(n)) == OK and 0 < n.value <= 1024 * 256 * 4
+    assert ws(3, 256, None) == NULL and ws(3, 200, ctypes.byref(n)) == SHAPE and ws(-1, 256, ctypes.byref(n)) == SHAPE
+    assert ws(3, 256, ctypes.byref(n)) == OK
+    call = caller(lib, "fp8bs_rms_norm_backward", [P, P, P, P, I32, P, I64, I64, P, P, I32, P, I64, P],
+                  dict(dy=FAKE, h=FAKE, rstd=FAKE, w=FAKE, wt=1, dh=FAKE, M=3, K=256, dx=FAKE, dw=FAKE, acc=0, ws=FAKE,
+                       n=n.value, stream=None))
+    for bad in (dict(M=-1), dict(K=0), dict(K=130), dict(n=n.value - 1), dict(n=-1)):
+        assert call(**bad) == SHAPE, bad
+    for bad in (dict(wt=2), dict(acc=2), dict(acc=-1)):
+        assert call(**bad) == FLAGS, bad
+    assert call(M=0, n=0, acc=1, dw=None, ws=None, dy=None) == OK      # nothing to add
+    for bad in (dict(dy=None), dict(h=None), dict(rstd=None), dict(w=None), dict(dx=None), dict(dw=None), dict(ws=None),
+                dict(M=0, dw=None)):
+        assert call(**bad) == NULL, bad
+    for bad in (dict(dy=MIS), dict(h=MIS), dict(w=MIS), dict(dh=MIS), dict(dx=MIS), dict(dw=MIS), dict(ws=MIS),
+                dict(rstd=ODD)):
+        assert call(**bad) == ALIGN, bad
+    if NO_DEVICE:
+        assert call() == DEVICE and call(dh=None, acc=1) == DEVICE and call(M=0, n=0, ws=None, dy=None) == DEVICE
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_route(lib, back):
+    if back:
+        call = caller(lib, "fp8bs_moe_route_backward", [P, I32, P, P, I64, I32, I32, P, U32, P],
+                      dict(x=FAKE, type=1, ids=FAKE, w=FAKE, T=3, E=8, k=2, out=FAKE, flags=4, stream=None))
+    else:
+        call = caller(lib, "fp8bs_moe_route", [P, I32, I64, I32, I32, P, P, U32, P],
+                      dict(x=FAKE, type=1, T=3, E=8, k=2, ids=FAKE, w=FAKE, flags=4, stream=None))
+    for bad in (dict(T=-1), dict(T=1 << 31), dict(E=0), dict(E=1025), dict(k=0), dict(k=9), dict(E=100, k=65), dict(k=-1)):
+        assert call(**bad) == SHAPE, bad
+    for bad in (dict(flags=1), dict(flags=2), dict(type=2)):
+        assert call(**bad) == FLAGS, bad
+    assert call(T=0, x=None, ids=None) == OK
+    for bad in (dict(x=None), dict(ids=None), dict(w=None)) + ((dict(out=None),) if back else ()):
+        assert call(**bad) == NULL, bad
+    for bad in (dict(x=MIS), dict(ids=ODD), dict(w=ODD)) + ((dict(out=MIS),) if back else ()):
+        assert call(**bad) == ALIGN, bad
+    if NO_DEVICE:
+        assert call() == DEVICE and call(type=0, flags=0, E=1024, k=64) == DEVICE
+
+
+def test_experts(lib):
+    ws = getattr(lib, "fp8bs_moe_experts_workspace")
+    ws.argtypes, ws.restype = [I64, I64, I64, I32, I32, P], ctypes.c_int
+    n = I64(-1)
+    assert ws(0, 256, 128, 4, 2, ctypes.byref(n)) == OK and n.value == 0
+    assert ws(3, 256, 128, 4, 2, None) == NULL and ws(129, 256, 128, 4, 2, ctypes.byref(n)) == SHAPE
+    assert ws(128, 65536, 8192, 1024, 16, ctypes.byref(n)) == OK and n.value > 0
+    assert ws(3, 256, 128, 4, 2, ctypes.byref(n)) == OK and n.value >= 3 * 2 * 128 * 4
+    call = caller(lib, "fp8bs_moe_experts", [P, P, P, P, P, P, P, P, P, I64, I64, I64, I32, I32, I32, P, I64, P],
+                  dict(x=FAKE, sx=FAKE, ids=FAKE, w=FAKE, w13=FAKE, s13=FAKE, w2=FAKE, s2=FAKE, out=FAKE, T=3, H=256,
+                       I=128, E=4, k=2, dt=0, ws=FAKE, n=n.value, stream=None))
+    for bad in (dict(T=-1), dict(T=129), dict(H=0), dict(H=64), dict(H=65536 + 128), dict(I=0), dict(I=192), dict(E=0),
+                dict(E=1025), dict(k=0), dict(k=17), dict(H=65536, I=16384), dict(n=n.value - 1), dict(n=0)):
+        assert call(**bad) == SHAPE, bad
+    assert call(dt=2) == FLAGS and call(dt=-1) == FLAGS
+    assert call(T=0, n=0, x=None, ws=None) == OK
+    for bad in ("x", "sx", "ids", "w", "w13", "s13", "w2", "s2", "out", "ws"):
+        assert call(**{bad: None}) == NULL, bad
+    for bad in ("x", "w13", "w2", "out", "ws"):
+        assert call(**{bad: MIS}) == ALIGN, bad
+    for bad in ("sx", "ids", "w", "s13", "s2"):
+        assert call(**{bad: ODD}) == ALIGN, bad
+    if NO_DEVICE:
+        assert call() == DEVICE and call(dt=1, sx=0x10004, k=16, n=1 << 30) == DEVICE    # (topk may pass E)
+
+
+def test_binding_refuses_cpu_tensors_and_large_counts(lib_path):
+    from fp8_block_scaled_04_amd import fp8bs as fb
+    b, f = torch.zeros(2, 128, dtype=torch.bfloat16), torch.zeros(2, 128)
+    q, i = torch.zeros(2, 128, dtype=torch.uint8), torch.zeros(2, 1, dtype=torch.int32)
+    w = torch.zeros(1, 256, 128, dtype=torch.uint8)
+    for call in (lambda: fb.rms_norm_quantize(b, b[0]), lambda: fb.rms_norm_backward(b, b, f[:, 0], b[0]),
+                 lambda: fb.moe_route(f, 2), lambda: fb.moe_route_backward(f, i, f[:, :1]),
+                 lambda: fb.moe_experts(q, f, i, f, w, f, w, f)):
+        with pytest.raises(ValueError, match="GPU tensor"):
+            call()
+    with pytest.raises(ValueError, match="below 2"):
+        fb.moe_experts_workspace_bytes(1, 128, 128, (1 << 32) + 4, 1)
+    with pytest.raises(fb.Fp8bsError):
+        fb.moe_experts_workspace_bytes(129, 128, 128, 4, 1)
+    with pytest.raises(fb.Fp8bsError):
+        fb.rms_norm_backward_workspace_bytes(4, 100)
+    assert fb.moe_experts_workspace_bytes(1, 128, 128, 4, 1) > 0
