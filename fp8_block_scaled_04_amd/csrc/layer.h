@@ -67,17 +67,16 @@ struct ExpertArgs {
   bool out_f32;
   int32_t T, H, I, E, topk;
   int32_t slots;             // min(E, T topk): as many experts may have tokens
-  int32_t splits;            // runs of slots that the second product is split over
   // workspace
   uint16_t* hi;              // [T topk][I] BF16, weighted activations
   uint16_t* lo;              // what hi leaves
   Slot* slot;                // [slots]
-  int32_t* token;            // [T topk] token of each row
-  float* part;               // [splits][T][H] where splits > 1
+  int32_t* place;            // [T topk] of each row, the place of the call it is for
+  float* part;               // [T topk][H] second product, by place
 };
 
 int32_t norm_back_groups(int64_t M, int64_t K);
-// Sets slots and splits from the sizes; the workspace and its layout.
+// Sets slots from the sizes; the workspace's size and, from `base`, its layout.
 void experts_plan(ExpertArgs& a);
 int64_t experts_workspace(ExpertArgs& a, void* base);
 

@@ -2,8 +2,8 @@
 //
 //   k_moe_up    per expert, g and u = w13 x, then the weighted activations
 //               weight g / (1 + exp(-g)) u, as two BF16 parts
-//   k_moe_down  w2 times them, summed over the experts of a token
-//   k_moe_join  adds the runs that k_moe_down was split over, if any
+//   k_moe_down  w2 times them
+//   k_moe_join  the sums of each token's rows
 //
 // Bound by HBM: every expert that has a token is read once, 3 H I codes for at
 // most a few dozen rows of products.  So weights go from memory straight to the
@@ -30,7 +30,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kMaxTokens = 128;
-constexpr int kMaxPlaces = kMaxTokens * 16;
 constexpr int kMaxChunks = 65536 / 128;
 
 // A buffer of `bytes` (below 2^31) from `base`: reads past them give 0 without
@@ -58,7 +57,7 @@ __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane
 
 // The rows of one slot, found by every workgroup of it.
 struct Rows {
-  int token[kMaxTokens];
+  int token[kMaxTokens], place[kMaxTokens];
   float weight[kMaxTokens];
 };
 
@@ -100,6 +99,7 @@ __device__ __forceinline__ Slot find_rows(const ExpertArgs& a, int slot, Rows& r
   if (hit < places) {
     const int r = before + __builtin_popcountll(mask & ((1ull << (tid % 64)) - 1));
     rows.token[r] = tid;
+    rows.place[r] = hit;
     rows.weight[r] = w;
   }
   if ((uint32_t)e >= (uint32_t)a.E || (a.slots < a.E && lowest != slot)) s.n = 0;
@@ -107,40 +107,70 @@ __device__ __forceinline__ Slot find_rows(const ExpertArgs& a, int slot, Rows& r
   return s;
 }
 
-// MF: 16-row fragments of this pass.  The waves take the 128-wide chunks of H in
-// turn; U chunks are in flight.
-template <int MF, int U>
+// Column c of the activations is kept at place_of(c) of its row: the 16 codes
+// that a lane of k_moe_down loads at once belong to two products, so the halves
+// of 16 columns lie 32 apart, and the rows' 64-byte pieces of a product are whole.
+__device__ __forceinline__ int place_of(int c) {
+  return (c & ~63) + ((c >> 3) & 1) * 32 + ((c >> 4) & 3) * 8 + (c & 7);
+}
+
+// Adds up the waves' accumulators of MF x NC fragments and hands each sum to
+// f(row, column, gate or only value, up), columns 16 per fragment.  `red` holds
+// kWaves * MF * NC * 256 floats.
+template <int MF, int NC>
+__device__ __forceinline__ void leave(const v4f (&acc)[MF][NC], float* red) {
+  v4f* mine = reinterpret_cast<v4f*>(red) + wave_id() * MF * NC * 64 + threadIdx.x % 64;
+#pragma unroll
+  for (int f = 0; f < MF; ++f)
+#pragma unroll
+    for (int n = 0; n < NC; ++n) mine[(f * NC + n) * 64] = acc[f][n];
+  __syncthreads();
+}
+// Row m, column c of fragment (f, n): lane (c / 4) 16 + m has c % 4.
+template <int MF, int NC>
+__device__ __forceinline__ float total(const float* red, int f, int n, int m, int c) {
+  float t = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) t += red[((w * MF + f) * NC + n) * 256 + ((c / 4) * 16 + m) * 4 + c % 4];
+  return t;
+}
+
+// MF: 16-row fragments of this pass; NG: 16-column fragments of gate and of up.
+// The waves take the 128-wide chunks of H in turn; U chunks are in flight.
+template <int MF, int NG, int U>
 __device__ __forceinline__ void up_rows(const ExpertArgs& a, const Slot& s, int row0, int col0, const Rows& rows,
                                         const float* scale_g, const float* scale_u, float* red) {
+  constexpr int NC = 2 * NG;
   const int lane = threadIdx.x % 64, wave = wave_id(), fr = lane % 16, fg = lane / 16;
   const int chunks = a.H / 128;
-  const int64_t stride = a.H, panel = 2 * (int64_t)a.I * a.H;
+  const int64_t panel = 2 * (int64_t)a.I * a.H;
   const auto wb = buffer(a.w13 + (int64_t)s.expert * panel, panel);
   const auto xb = buffer(a.x, (int64_t)a.T * a.H);
   const auto sb = buffer(a.sx, (int64_t)a.T * chunks * 4);
-  const uint32_t gate = (uint32_t)((col0 + fr) * stride + fg * 16);
-  const uint32_t up = gate + (uint32_t)(a.I * stride);
-  uint32_t xrow[MF], srow[MF];
+  uint32_t wrow[NC], xrow[MF], srow[MF];
+#pragma unroll
+  for (int n = 0; n < NC; ++n) wrow[n] = (uint32_t)(((n / NG) * a.I + col0 + (n % NG) * 16 + fr) * (int64_t)a.H + fg * 16);
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
     const int r = row0 + f * 16 + fr;
     const bool there = r < s.n;
     const int t = there ? rows.token[r] : 0;
-    xrow[f] = there ? (uint32_t)(t * stride + fg * 16) : kNoRow;
+    xrow[f] = there ? (uint32_t)(t * a.H + fg * 16) : kNoRow;
     srow[f] = there ? (uint32_t)t * 4 : kNoRow;
   }
 
   struct Chunk {
-    u32x4 g0, g1, u0, u1, x0[MF], x1[MF];
+    u32x4 w0[NC], w1[NC], x0[MF], x1[MF];
     float sx[MF];
   } c[U];
   auto fetch = [&](Chunk& k, int kb) {
     const uint32_t at = kb < chunks ? (uint32_t)kb * 128 : kNoChunk;
     const uint32_t sat = kb < chunks ? (uint32_t)(kb * a.T * 4) : kNoChunk;
-    k.g0 = load16(wb, gate + at);
-    k.g1 = load16(wb, gate + at + 64);
-    k.u0 = load16(wb, up + at);
-    k.u1 = load16(wb, up + at + 64);
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      k.w0[n] = load16(wb, wrow[n] + at);
+      k.w1[n] = load16(wb, wrow[n] + at + 64);
+    }
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
       k.x0[f] = load16(xb, xrow[f] + at);
@@ -148,9 +178,11 @@ __device__ __forceinline__ void up_rows(const ExpertArgs& a, const Slot& s, int 
       k.sx[f] = load4(sb, srow[f] + sat);
     }
   };
-  v4f ag[MF], au[MF];
+  v4f acc[MF][NC];
 #pragma unroll
-  for (int f = 0; f < MF; ++f) ag[f] = au[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int f = 0; f < MF; ++f)
+#pragma unroll
+    for (int n = 0; n < NC; ++n) acc[f][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < U; ++i) fetch(c[i], wave + i * kWaves);
   const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
@@ -159,45 +191,35 @@ __device__ __forceinline__ void up_rows(const ExpertArgs& a, const Slot& s, int 
     for (int i = 0; i < U; ++i) {
       const int kb = k0 + i * kWaves;
       const float sg = scale_g[min(kb, chunks - 1)], su = scale_u[min(kb, chunks - 1)];
-      const v8i g = join(c[i].g0, c[i].g1), u = join(c[i].u0, c[i].u1);
+      v8i x[MF];
 #pragma unroll
-      for (int f = 0; f < MF; ++f) {
-        const v8i x = join(c[i].x0[f], c[i].x1[f]);
-        const v4f pg = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(g, x, zero, 0, 0, 0, 0, 0, 0);
-        const v4f pu = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(u, x, zero, 0, 0, 0, 0, 0, 0);
-        const float wg = c[i].sx[f] * sg, wu = c[i].sx[f] * su;
+      for (int f = 0; f < MF; ++f) x[f] = join(c[i].x0[f], c[i].x1[f]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          ag[f][e] = __builtin_fmaf(pg[e], wg, ag[f][e]);
-          au[f][e] = __builtin_fmaf(pu[e], wu, au[f][e]);
+      for (int n = 0; n < NC; ++n) {
+        const v8i w = join(c[i].w0[n], c[i].w1[n]);
+#pragma unroll
+        for (int f = 0; f < MF; ++f) {
+          const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x[f], zero, 0, 0, 0, 0, 0, 0);
+          const float by = c[i].sx[f] * (n < NG ? sg : su);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[f][n][e] = __builtin_fmaf(p[e], by, acc[f][n][e]);
         }
       }
       fetch(c[i], kb + U * kWaves);
     }
   }
-  // the waves' sums, [wave][fragment][gate, up][lane][4]
-  v4f* mine = reinterpret_cast<v4f*>(red) + (wave * MF * 2) * 64 + lane;
+  leave(acc, red);
+  const int m = threadIdx.x / 16, col = threadIdx.x % 16;
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
-    mine[(f * 2) * 64] = ag[f];
-    mine[(f * 2 + 1) * 64] = au[f];
-  }
-  __syncthreads();
-  // thread -> row m, column n of a fragment: lane (n / 4) 16 + m has n % 4
-  const int m = threadIdx.x / 16, n = threadIdx.x % 16, from = ((n / 4) * 16 + m) * 4 + n % 4;
-#pragma unroll
-  for (int f = 0; f < MF; ++f) {
-    float g = 0.0f, u = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      g += red[((w * MF + f) * 2) * 256 + from];
-      u += red[((w * MF + f) * 2 + 1) * 256 + from];
-    }
     const int r = row0 + f * 16 + m;
-    if (r < s.n) {
+    if (r >= s.n) continue;
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      const float g = total<MF, NC>(red, f, n, m, col), u = total<MF, NC>(red, f, NG + n, m, col);
       const float v = rows.weight[r] * (g / (1.0f + expf(-g))) * u;
       const __bf16 hi = (__bf16)v, lo = (__bf16)(v - (float)hi);
-      const int64_t at = (int64_t)(s.base + r) * a.I + col0 + n;
+      const int64_t at = (int64_t)(s.base + r) * a.I + place_of(col0 + n * 16 + col);
       a.hi[at] = __builtin_bit_cast(uint16_t, hi);
       a.lo[at] = __builtin_bit_cast(uint16_t, lo);
     }
@@ -205,17 +227,17 @@ __device__ __forceinline__ void up_rows(const ExpertArgs& a, const Slot& s, int 
   __syncthreads();
 }
 
-// One workgroup per slot and 16 columns of I.
-template <int MAXF>
+// One workgroup per slot and 16 NG columns of I.
+template <int MAXF, int NG>
 __global__ __launch_bounds__(kThreads) void k_moe_up(ExpertArgs a) {
   __shared__ Rows rows;
   __shared__ float scale_g[kMaxChunks], scale_u[kMaxChunks];
-  __shared__ __align__(16) float red[kWaves * MAXF * 2 * 256];
-  const int tiles = a.I / 16, slot = blockIdx.x / tiles, col0 = (blockIdx.x % tiles) * 16;
+  __shared__ __align__(16) float red[kWaves * MAXF * 2 * NG * 256];
+  const int tiles = a.I / (16 * NG), slot = blockIdx.x / tiles, col0 = (blockIdx.x % tiles) * 16 * NG;
   const Slot s = find_rows(a, slot, rows);
   if (blockIdx.x % tiles == 0) {                     // what k_moe_down needs to know
     if (threadIdx.x == 0) a.slot[slot] = s;
-    for (int r = threadIdx.x; r < s.n; r += kThreads) a.token[s.base + r] = rows.token[r];
+    for (int r = threadIdx.x; r < s.n; r += kThreads) a.place[s.base + r] = rows.place[r];
   }
   if (s.n == 0) return;
   const int chunks = a.H / 128;
@@ -227,9 +249,9 @@ __global__ __launch_bounds__(kThreads) void k_moe_up(ExpertArgs a) {
   __syncthreads();
   for (int row0 = 0; row0 < s.n; row0 += 16 * MAXF) {
     const int left = (s.n - row0 + 15) / 16;
-    if (MAXF == 1 || left == 1) up_rows<1, 4>(a, s, row0, col0, rows, scale_g, scale_u, red);
-    else if (MAXF == 2 || left == 2) up_rows<2 <= MAXF ? 2 : 1, 2>(a, s, row0, col0, rows, scale_g, scale_u, red);
-    else up_rows<MAXF, 2>(a, s, row0, col0, rows, scale_g, scale_u, red);
+    if (MAXF == 1 || left == 1) up_rows<1, NG, 3>(a, s, row0, col0, rows, scale_g, scale_u, red);
+    else if (MAXF == 2 || left == 2) up_rows<2 <= MAXF ? 2 : 1, NG, 2>(a, s, row0, col0, rows, scale_g, scale_u, red);
+    else up_rows<MAXF, NG, 2>(a, s, row0, col0, rows, scale_g, scale_u, red);
   }
 }
 
@@ -243,131 +265,131 @@ __device__ __forceinline__ v8bf to_bf16(uint32_t a, uint32_t b) {
   return v8bf{p[0], p[1], q[0], q[1], r[0], r[1], t[0], t[1]};
 }
 
-// One wave, one slot: chunks first, first + step, ... of I; adds its products to
-// the wave's own sums [token][16 columns].
-template <int MF, int U>
-__device__ __forceinline__ void down_rows(const ExpertArgs& a, const Slot& s, int row0, int col0, int first, int step,
-                                          const uint8_t* tokens, float* sums) {
-  const int lane = threadIdx.x % 64, fr = lane % 16, fg = lane / 16;
+// MF row fragments, NC column fragments; the waves take the chunks of I in turn.
+template <int MF, int NC, int U>
+__device__ __forceinline__ void down_rows(const ExpertArgs& a, const Slot& s, int row0, int col0, float* red) {
+  const int lane = threadIdx.x % 64, wave = wave_id(), fr = lane % 16, fg = lane / 16;
   const int chunks = a.I / 128;
   const int64_t panel = (int64_t)a.H * a.I;
   const auto wb = buffer(a.w2 + (int64_t)s.expert * panel, panel);
   const int64_t act = (int64_t)s.n * a.I * 2;        // rows of this slot (at most 2^24 bytes)
   const auto hb = buffer(a.hi + (int64_t)s.base * a.I, act), lb = buffer(a.lo + (int64_t)s.base * a.I, act);
   const float* sc = a.s2 + ((int64_t)s.expert * (a.H / 128) + col0 / 128) * chunks;
-  const uint32_t wrow = (uint32_t)((col0 + fr) * (int64_t)a.I + fg * 32);
-  uint32_t arow[MF];
+  uint32_t wrow[NC], arow[MF];
 #pragma unroll
-  for (int f = 0; f < MF; ++f) arow[f] = (uint32_t)((row0 + f * 16 + fr) * (int64_t)a.I + fg * 32) * 2;  // past n: outside
-  u32x4 w[U][2];
-  float scale[U];
-  auto fetch = [&](int i, int kb) {
+  for (int n = 0; n < NC; ++n) wrow[n] = (uint32_t)((col0 + n * 16 + fr) * (int64_t)a.I + fg * 16);
+#pragma unroll
+  for (int f = 0; f < MF; ++f) arow[f] = (uint32_t)((row0 + f * 16 + fr) * (int64_t)a.I + fg * 8) * 2;  // past n: outside
+  struct Chunk {
+    u32x4 w0[NC], w1[NC];
+    float scale;
+  } c[U];
+  auto fetch = [&](Chunk& k, int kb) {
     const uint32_t at = kb < chunks ? (uint32_t)kb * 128 : kNoChunk;
-    w[i][0] = load16(wb, wrow + at);
-    w[i][1] = load16(wb, wrow + at + 16);
-    scale[i] = sc[min(kb, chunks - 1)];
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      k.w0[n] = load16(wb, wrow[n] + at);
+      k.w1[n] = load16(wb, wrow[n] + at + 64);
+    }
+    k.scale = sc[min(kb, chunks - 1)];
   };
-  v4f acc[MF];
+  struct Acts {
+    u32x4 hi[MF][4], lo[MF][4];
+  };
+  auto fetch_acts = [&](Acts& k, int kb) {
+    const uint32_t at = kb < chunks ? (uint32_t)kb * 256 : kNoRow;
 #pragma unroll
-  for (int f = 0; f < MF; ++f) acc[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int f = 0; f < MF; ++f)
 #pragma unroll
-  for (int i = 0; i < U; ++i) fetch(i, first + i * step);
-  for (int k0 = first; k0 < chunks; k0 += U * step) {
+      for (int j = 0; j < 4; ++j) {
+        k.hi[f][j] = load16(hb, arow[f] + at + j * 64);
+        k.lo[f][j] = load16(lb, arow[f] + at + j * 64);
+      }
+  };
+  v4f acc[MF][NC];
+#pragma unroll
+  for (int f = 0; f < MF; ++f)
+#pragma unroll
+    for (int n = 0; n < NC; ++n) acc[f][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < U; ++i) fetch(c[i], wave + i * kWaves);
+  for (int k0 = wave; k0 < chunks; k0 += U * kWaves) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int kb = k0 + i * step;
-      const uint32_t at = kb < chunks ? (uint32_t)kb * 256 : kNoRow;
-      // 32 codes of a lane: four steps of eight
-      const v8bf b[4] = {to_bf16(w[i][0].x, w[i][0].y), to_bf16(w[i][0].z, w[i][0].w), to_bf16(w[i][1].x, w[i][1].y),
-                         to_bf16(w[i][1].z, w[i][1].w)};
+      const int kb = k0 + i * kWaves;
+      Acts x;
+      fetch_acts(x, kb);
 #pragma unroll
-      for (int f = 0; f < MF; ++f) {
-        v4f p{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int n = 0; n < NC; ++n) {
+        const v8bf b[4] = {to_bf16(c[i].w0[n].x, c[i].w0[n].y), to_bf16(c[i].w0[n].z, c[i].w0[n].w),
+                           to_bf16(c[i].w1[n].x, c[i].w1[n].y), to_bf16(c[i].w1[n].z, c[i].w1[n].w)};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t from = arow[f] + at + j * 16;
-          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, load16(hb, from)), p, 0, 0, 0);
-          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, load16(lb, from)), p, 0, 0, 0);
+        for (int f = 0; f < MF; ++f) {
+          v4f p{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, x.hi[f][j]), p, 0, 0, 0);
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, x.lo[f][j]), p, 0, 0, 0);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[f][n][e] = __builtin_fmaf(p[e], c[i].scale, acc[f][n][e]);
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[f][e] = __builtin_fmaf(p[e], scale[i], acc[f][e]);
       }
-      fetch(i, kb + U * step);
+      fetch(c[i], kb + U * kWaves);
     }
   }
+  leave(acc, red);
+  const int m = threadIdx.x / 16, col = threadIdx.x % 16;
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
-    const int r = row0 + f * 16 + fr;
-    if (r < s.n) {                                   // (rows of a slot have different tokens)
-      v4f* to = reinterpret_cast<v4f*>(sums + tokens[s.base + r] * 16 + fg * 4);
-      *to += acc[f];
-    }
+    const int r = row0 + f * 16 + m;
+    if (r >= s.n) continue;
+    float* to = a.part + (int64_t)a.place[s.base + r] * a.H + col0 + col;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) to[n * 16] = total<MF, NC>(red, f, n, m, col);
+  }
+  __syncthreads();
+}
+
+// One workgroup per slot and 16 NC columns of H.
+template <int MAXF, int NC>
+__global__ __launch_bounds__(kThreads) void k_moe_down(ExpertArgs a) {
+  __shared__ __align__(16) float red[kWaves * MAXF * NC * 256];
+  const int tiles = a.H / (16 * NC), slot = blockIdx.x / tiles, col0 = (blockIdx.x % tiles) * 16 * NC;
+  Slot s = a.slot[slot];
+  s.expert = __builtin_amdgcn_readfirstlane(s.expert);
+  s.base = __builtin_amdgcn_readfirstlane(s.base);
+  s.n = __builtin_amdgcn_readfirstlane(s.n);
+  for (int row0 = 0; row0 < s.n; row0 += 16 * MAXF) {
+    const int left = (s.n - row0 + 15) / 16;
+    if (MAXF == 1 || left == 1) down_rows<1, NC, 2>(a, s, row0, col0, red);
+    else if (MAXF == 2 || left == 2) down_rows<2 <= MAXF ? 2 : 1, NC, 2>(a, s, row0, col0, red);
+    else down_rows<MAXF, NC, 2>(a, s, row0, col0, red);
   }
 }
 
-// One workgroup per 16 columns of H and run of slots.  Waves take (slot, part of
-// I) items in turn, and add into sums of their own; those are added in order.
-template <int MAXF>
-__global__ __launch_bounds__(kThreads) void k_moe_down(ExpertArgs a, int parts) {
-  extern __shared__ __align__(16) float sums[];      // [kWaves][T][16]
-  __shared__ uint8_t tokens[kMaxPlaces];
-  const int tiles = a.H / 16, col0 = (blockIdx.x % tiles) * 16, run = blockIdx.x / tiles;
-  const int wave = wave_id();
-  for (int i = threadIdx.x; i < kWaves * a.T * 16; i += kThreads) sums[i] = 0.0f;
-  // (rows without a token are never read below)
-  for (int i = threadIdx.x; i < a.T * a.topk; i += kThreads) tokens[i] = (uint8_t)a.token[i];
-  __syncthreads();
-  float* mine = sums + wave * a.T * 16;
-  const int items = (a.slots - run + a.splits - 1) / a.splits * parts;
-  for (int i = wave; i < items; i += kWaves) {
-    Slot s = a.slot[run + i / parts * a.splits];
-    s.expert = __builtin_amdgcn_readfirstlane(s.expert);
-    s.base = __builtin_amdgcn_readfirstlane(s.base);
-    s.n = __builtin_amdgcn_readfirstlane(s.n);
-    for (int row0 = 0; row0 < s.n; row0 += 16 * MAXF) {
-      const int left = (s.n - row0 + 15) / 16;
-      if (MAXF == 1 || left == 1) down_rows<1, 4>(a, s, row0, col0, i % parts, parts, tokens, mine);
-      else if (MAXF == 2 || left == 2) down_rows<2 <= MAXF ? 2 : 1, 4>(a, s, row0, col0, i % parts, parts, tokens, mine);
-      else down_rows<MAXF, 4>(a, s, row0, col0, i % parts, parts, tokens, mine);
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.T * 16; i += kThreads) {
-    float v = sums[i];
-    for (int w = 1; w < kWaves; ++w) v += sums[w * a.T * 16 + i];
-    const int64_t at = (int64_t)(i / 16) * a.H + col0 + i % 16;
-    if (a.splits > 1) a.part[(int64_t)run * a.T * a.H + at] = v;
-    else if (a.out_f32) static_cast<float*>(a.out)[at] = v;
-    else static_cast<__bf16*>(a.out)[at] = (__bf16)v;
-  }
-}
-
+// out[t] = the rows of token t's places added up in turn.  Places without a row
+// (an id outside, or one that stands further left too) are left out.
 __global__ __launch_bounds__(kThreads) void k_moe_join(ExpertArgs a) {
-  const int64_t all = (int64_t)a.T * a.H, i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
-  if (i >= all) return;                              // (all is a multiple of 128)
-  v4f v = *reinterpret_cast<const v4f*>(a.part + i);
-  for (int g = 1; g < a.splits; ++g) v += *reinterpret_cast<const v4f*>(a.part + g * all + i);
-  if (a.out_f32) *reinterpret_cast<v4f*>(static_cast<float*>(a.out) + i) = v;
-  else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + i) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
+  const int h = (blockIdx.x * kThreads + threadIdx.x) * 4, t = blockIdx.y;
+  if (h >= a.H) return;
+  const int32_t* ids = a.ids + t * a.topk;
+  v4f v{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int c = 0; c < a.topk; ++c) {
+    bool counts = (uint32_t)ids[c] < (uint32_t)a.E;
+    for (int b = 0; b < c; ++b) counts = counts && ids[b] != ids[c];
+    if (counts) v += *reinterpret_cast<const v4f*>(a.part + (int64_t)(t * a.topk + c) * a.H + h);
+  }
+  const int64_t at = (int64_t)t * a.H + h;
+  if (a.out_f32) *reinterpret_cast<v4f*>(static_cast<float*>(a.out) + at) = v;
+  else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
 }
 
 int64_t aligned(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
-// Parts of I that a slot's second product is cut into, so that the waves of a
-// workgroup all have work where it has fewer slots than waves.
-int parts_of(const ExpertArgs& a) {
-  const int per = (a.slots + a.splits - 1) / a.splits;
-  return std::max(1, std::min(kWaves / per, a.I / 128));
-}
-
 }  // namespace
 
-void experts_plan(ExpertArgs& a) {
-  a.slots = std::min(a.E, a.T * a.topk);
-  // workgroups enough for four on each of 256 CUs
-  const int tiles = a.H / 16;
-  a.splits = std::max(1, std::min(a.slots, (1024 + tiles - 1) / tiles));
-}
+void experts_plan(ExpertArgs& a) { a.slots = std::min(a.E, a.T * a.topk); }
 
 int64_t experts_workspace(ExpertArgs& a, void* base) {
   const int64_t places = (int64_t)a.T * a.topk;
@@ -380,28 +402,26 @@ int64_t experts_workspace(ExpertArgs& a, void* base) {
   };
   a.hi = reinterpret_cast<uint16_t*>(take(places * a.I * 2));
   a.lo = reinterpret_cast<uint16_t*>(take(places * a.I * 2));
+  a.part = reinterpret_cast<float*>(take(places * a.H * 4));
   a.slot = reinterpret_cast<Slot*>(take(a.slots * (int64_t)sizeof(Slot)));
-  a.token = reinterpret_cast<int32_t*>(take(places * 4));
-  a.part = reinterpret_cast<float*>(take(a.splits > 1 ? (int64_t)a.splits * a.T * a.H * 4 : 0));
+  a.place = reinterpret_cast<int32_t*>(take(places * 4));
   return at;
 }
 
+namespace {
+
+template <int MAXF, int NG, int NC>
+void launch(const ExpertArgs& a, hipStream_t stream) {
+  k_moe_up<MAXF, NG><<<(unsigned)(a.I / (16 * NG) * a.slots), kThreads, 0, stream>>>(a);
+  k_moe_down<MAXF, NC><<<(unsigned)(a.H / (16 * NC) * a.slots), kThreads, 0, stream>>>(a);
+}
+
+}  // namespace
+
 hipError_t launch_moe_experts(const ExpertArgs& a, hipStream_t stream) {
-  const unsigned up = (unsigned)(a.I / 16 * a.slots), down = (unsigned)(a.H / 16 * a.splits);
-  const size_t lds = (size_t)kWaves * a.T * 16 * 4;
-  const int parts = parts_of(a);
-  if (a.T <= 16) {
-    k_moe_up<1><<<up, kThreads, 0, stream>>>(a);
-    k_moe_down<1><<<down, kThreads, lds, stream>>>(a, parts);
-  } else if (a.T <= 32) {
-    k_moe_up<2><<<up, kThreads, 0, stream>>>(a);
-    k_moe_down<2><<<down, kThreads, lds, stream>>>(a, parts);
-  } else {
-    k_moe_up<4><<<up, kThreads, 0, stream>>>(a);
-    k_moe_down<4><<<down, kThreads, lds, stream>>>(a, parts);
-  }
-  if (a.splits > 1)
-    k_moe_join<<<(unsigned)(((int64_t)a.T * a.H / 4 + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
+  if (a.T <= 16) launch<1, 2, 4>(a, stream);
+  else launch<2, 2, 4>(a, stream);
+  k_moe_join<<<dim3((unsigned)((a.H / 4 + kThreads - 1) / kThreads), (unsigned)a.T), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
