@@ -311,14 +311,17 @@ __device__ __forceinline__ void down_rows(const ExpertArgs& a, const Slot& s, in
   for (int f = 0; f < MF; ++f)
 #pragma unroll
     for (int n = 0; n < NC; ++n) acc[f][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  // Loads return in the order they were issued, so the activations of a chunk
+  // (from L2) go out ahead of weights (from memory) that are needed later.
+  Acts x;
+  fetch(c[0], wave);
+  fetch_acts(x, wave);
 #pragma unroll
-  for (int i = 0; i < U; ++i) fetch(c[i], wave + i * kWaves);
+  for (int i = 1; i < U; ++i) fetch(c[i], wave + i * kWaves);
   for (int k0 = wave; k0 < chunks; k0 += U * kWaves) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int kb = k0 + i * kWaves;
-      Acts x;
-      fetch_acts(x, kb);
 #pragma unroll
       for (int n = 0; n < NC; ++n) {
         const v8bf b[4] = {to_bf16(c[i].w0[n].x, c[i].w0[n].y), to_bf16(c[i].w0[n].z, c[i].w0[n].w),
@@ -335,6 +338,7 @@ __device__ __forceinline__ void down_rows(const ExpertArgs& a, const Slot& s, in
           for (int e = 0; e < 4; ++e) acc[f][n][e] = __builtin_fmaf(p[e], c[i].scale, acc[f][n][e]);
         }
       }
+      fetch_acts(x, kb + kWaves);
       fetch(c[i], kb + U * kWaves);
     }
   }
