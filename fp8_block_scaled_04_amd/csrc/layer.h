@@ -49,11 +49,6 @@ struct RouteArgs {
   void* dlogits;             // backward only
 };
 
-// One expert that has tokens: its rows [base, base + n) of the workspace.
-struct Slot {
-  int32_t expert, base, n, unused;
-};
-
 struct ExpertArgs {
   const uint8_t* x;
   const float* sx;
@@ -66,18 +61,14 @@ struct ExpertArgs {
   void* out;
   bool out_f32;
   int32_t T, H, I, E, topk;
-  int32_t slots;             // min(E, T topk): as many experts may have tokens
   // workspace
   uint16_t* hi;              // [T topk][I] BF16, weighted activations
   uint16_t* lo;              // what hi leaves
-  Slot* slot;                // [slots]
-  int32_t* place;            // [T topk] of each row, the place of the call it is for
   float* part;               // [T topk][H] second product, by place
 };
 
 int32_t norm_back_groups(int64_t M, int64_t K);
-// Sets slots from the sizes; the workspace's size and, from `base`, its layout.
-void experts_plan(ExpertArgs& a);
+// Bytes of the workspace; lays it out from `base`.
 int64_t experts_workspace(ExpertArgs& a, void* base);
 
 hipError_t launch_rms_norm(const NormArgs& a, bool pow2, hipStream_t stream);

@@ -24,7 +24,7 @@ bool route_sizes_fit(int64_t T, int32_t E, int32_t topk) {
   return T >= 0 && T <= kMaxRows && E > 0 && E <= 1024 && topk > 0 && topk <= std::min(E, 64);
 }
 
-bool width_fits(int64_t n) { return n > 0 && n <= 65536 && n % 128 == 0; }
+bool width_fits(int64_t n) { return n > 0 && n <= 32768 && n % 128 == 0; }
 
 bool expert_sizes_fit(int64_t T, int64_t H, int64_t I, int32_t E, int32_t topk) {
   return T >= 0 && T <= 128 && width_fits(H) && width_fits(I) && 2 * H * I < ((int64_t)1 << 31) && E > 0 && E <= 1024 &&
@@ -113,7 +113,6 @@ fp8bs_status fp8bs_moe_experts_workspace(int64_t T, int64_t H, int64_t I, int32_
   if (!bytes) return FP8BS_ERR_NULL;
   fp8bs::ExpertArgs a{};
   a.T = (int32_t)T, a.H = (int32_t)H, a.I = (int32_t)I, a.E = E, a.topk = topk;
-  experts_plan(a);
   *bytes = T == 0 ? 0 : experts_workspace(a, nullptr);
   return FP8BS_OK;
 }
@@ -124,8 +123,7 @@ fp8bs_status fp8bs_moe_experts(const uint8_t* x, const float* sx, const int32_t*
                                void* workspace, int64_t workspace_bytes, fp8bs_stream_t stream) {
   if (!expert_sizes_fit(T, H, I, E, topk)) return FP8BS_ERR_SHAPE;
   fp8bs::ExpertArgs a{x, sx, ids, weights, w13, s13, w2, s2, out, out_dtype == FP8BS_OUT_FP32, (int32_t)T, (int32_t)H,
-                      (int32_t)I, E, topk, 0, nullptr, nullptr, nullptr, nullptr, nullptr};
-  experts_plan(a);
+                      (int32_t)I, E, topk, nullptr, nullptr, nullptr};
   if (workspace_bytes < (T == 0 ? 0 : experts_workspace(a, workspace))) return FP8BS_ERR_SHAPE;
   if (out_dtype != FP8BS_OUT_BF16 && out_dtype != FP8BS_OUT_FP32) return FP8BS_ERR_FLAGS;
   if (T == 0) return FP8BS_OK;

@@ -10,11 +10,8 @@
 // registers that the matrix core takes them from, each code to one wave, several
 // loads ahead of their use; the tokens' rows come from L2.
 //
-// Rows.  A (token, expert) pair of the call is a row.  The rows of expert e lie
-// one after the other from base(e), the number of places with a smaller id, in
-// the order of their tokens; slot s is the s-th place of the call where E is
-// larger than their number (the first place of each expert has the work), else
-// expert s.
+// A (token, expert) pair of the call is a row.  The rows of an expert lie one
+// after the other in the order of their tokens, those of lower experts before.
 #include <algorithm>
 
 #include "layer.h"
@@ -29,8 +26,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kMaxTokens = 128;
-constexpr int kMaxChunks = 65536 / 128;
 
 // A buffer of `bytes` (below 2^31) from `base`: reads past them give 0 without
 // touching memory.  Offsets of chunks and rows that do not exist; either of them,
@@ -53,59 +48,107 @@ __device__ __forceinline__ v8i join(u32x4 a, u32x4 b) {
 // This wave's number, on the scalar unit.
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
 
-// ---- gate and up ----
+// ---- which rows each expert has ----
 
-// The rows of one slot, found by every workgroup of it.
-struct Rows {
-  int token[kMaxTokens], place[kMaxTokens];
-  float weight[kMaxTokens];
+// One expert's rows, at most `block` of them, packed: expert (10 bits), first row
+// (12), rows (8).
+struct Job {
+  int expert, start, n;
 };
+__device__ __forceinline__ uint32_t pack(int expert, int start, int n) { return expert | start << 10 | n << 22; }
 
-// Fills `rows` and returns the slot; n = 0 where it has no work.  Every thread
-// of the workgroup calls it.
-__device__ __forceinline__ Slot find_rows(const ExpertArgs& a, int slot, Rows& rows) {
-  __shared__ int below[kWaves], matches[kWaves], first[kWaves];
-  const int places = a.T * a.topk, tid = threadIdx.x, wave = wave_id();
-  const int e = __builtin_amdgcn_readfirstlane(a.slots < a.E ? a.ids[slot] : slot);
-  // thread t looks through token t's places
-  int lower = 0, hit = places;
-  float w = 0.0f;
-  if (tid < a.T) {
-    for (int c = a.topk - 1; c >= 0; --c) {
-      const int id = a.ids[tid * a.topk + c];
-      lower += id >= 0 && id < e;
-      if (id == e) {
-        w += a.weights[tid * a.topk + c];
-        hit = tid * a.topk + c;
-      }
-    }
+// The call's rows and jobs, worked out from ids by every workgroup in its own
+// LDS: a bit per (expert, token), so that the order in which they are set does
+// not matter; then sums over the experts.
+struct Plan {
+  uint32_t* mask;   // [E][words]
+  int* base;        // [E] rows of the experts before
+  uint32_t* job;    // [jobs]
+  uint32_t* row;    // token << 16 | place
+  float* weight;    // [rows]
+  int jobs;
+
+  __device__ __forceinline__ Job at(int j) const {
+    const uint32_t p = __builtin_amdgcn_readfirstlane(job[j]);
+    return {(int)(p & 1023), (int)(p >> 10 & 4095), (int)(p >> 22)};
   }
-  const uint64_t mask = __builtin_amdgcn_ballot_w64(hit < places);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) lower += __shfl_xor(lower, d);
-  int least = hit;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) least = min(least, __shfl_xor(least, d));
-  if (tid % 64 == 0) below[wave] = lower, matches[wave] = __builtin_popcountll(mask), first[wave] = least;
-  __syncthreads();
-  Slot s{e, 0, 0, 0};
-  int before = 0, lowest = places;
-  for (int i = 0; i < kWaves; ++i) {
-    s.base += below[i];
-    s.n += matches[i];
-    if (i < wave) before += matches[i];
-    lowest = min(lowest, first[i]);
-  }
-  if (hit < places) {
-    const int r = before + __builtin_popcountll(mask & ((1ull << (tid % 64)) - 1));
-    rows.token[r] = tid;
-    rows.place[r] = hit;
-    rows.weight[r] = w;
-  }
-  if ((uint32_t)e >= (uint32_t)a.E || (a.slots < a.E && lowest != slot)) s.n = 0;
-  __syncthreads();
-  return s;
+};
+__host__ __device__ __forceinline__ int mask_words(int T) { return (T + 31) / 32; }
+int plan_bytes(const ExpertArgs& a) {
+  return (a.E * (mask_words(a.T) + 1) + a.T * a.topk * 3) * 4;
 }
+
+// `block`: rows that one pass over an expert's weights serves.
+__device__ __forceinline__ Plan make_plan(const ExpertArgs& a, uint32_t* lds, int block) {
+  __shared__ int waves[kWaves];
+  const int tid = threadIdx.x, places = a.T * a.topk, words = mask_words(a.T);
+  Plan p;
+  p.mask = lds;
+  p.base = reinterpret_cast<int*>(p.mask + a.E * words);
+  p.job = reinterpret_cast<uint32_t*>(p.base + a.E);
+  p.row = p.job + places;
+  p.weight = reinterpret_cast<float*>(p.row + places);
+  for (int i = tid; i < a.E * words; i += kThreads) p.mask[i] = 0u;
+  __syncthreads();
+  for (int i = tid; i < places; i += kThreads) {
+    const uint32_t e = (uint32_t)a.ids[i];
+    const int t = i / a.topk;
+    if (e < (uint32_t)a.E) atomicOr(&p.mask[e * words + t / 32], 1u << (t % 32));
+  }
+  __syncthreads();
+  // thread -> `each` experts in a row; rows and jobs before them, as one number
+  const int each = (a.E + kThreads - 1) / kThreads;
+  int mine = 0;
+  auto rows_of = [&](int e) {
+    int n = 0;
+    for (int w = 0; w < words; ++w) n += __builtin_popcount(p.mask[e * words + w]);
+    return n;
+  };
+  for (int e = tid * each; e < min(a.E, (tid + 1) * each); ++e) {
+    const int n = rows_of(e);
+    mine += n | ((n + block - 1) / block) << 16;
+  }
+  int before = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(before, d);
+    if (tid % 64 >= d) before += o;
+  }
+  if (tid % 64 == 63) waves[tid / 64] = before;
+  __syncthreads();
+  before -= mine;
+  int all = 0;
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < tid / 64) before += waves[w];
+    all += waves[w];
+  }
+  p.jobs = __builtin_amdgcn_readfirstlane(all >> 16);
+  for (int e = tid * each; e < min(a.E, (tid + 1) * each); ++e) {
+    const int n = rows_of(e), start = before & 0xFFFF, job = before >> 16;
+    p.base[e] = start;
+    for (int r = 0; r < n; r += block) p.job[job + r / block] = pack(e, start + r, min(block, n - r));
+    before += n | ((n + block - 1) / block) << 16;
+  }
+  __syncthreads();
+  // a row per expert of a token: from the expert's first place there
+  for (int i = tid; i < places; i += kThreads) {
+    const int t = i / a.topk, id = a.ids[i];
+    bool first = (uint32_t)id < (uint32_t)a.E;
+    for (int c = t * a.topk; c < i; ++c) first = first && a.ids[c] != id;
+    if (!first) continue;
+    float w = 0.0f;
+    for (int c = i; c < (t + 1) * a.topk; ++c) w += a.ids[c] == id ? a.weights[c] : 0.0f;
+    int r = p.base[id];
+    for (int k = 0; k < t / 32; ++k) r += __builtin_popcount(p.mask[id * words + k]);
+    r += __builtin_popcount(p.mask[id * words + t / 32] & ((1u << (t % 32)) - 1));
+    p.row[r] = (uint32_t)t << 16 | (uint32_t)i;
+    p.weight[r] = w;
+  }
+  __syncthreads();
+  return p;
+}
+
+// ---- what both products share ----
 
 // Column c of the activations is kept at place_of(c) of its row: the 16 codes
 // that a lane of k_moe_down loads at once belong to two products, so the halves
@@ -135,35 +178,65 @@ __device__ __forceinline__ float total(const float* red, int f, int n, int m, in
   return t;
 }
 
-// MF: 16-row fragments of this pass; NG: 16-column fragments of gate and of up.
-// The waves take the 128-wide chunks of H in turn; U chunks are in flight.
-template <int MF, int NG, int U>
-__device__ __forceinline__ void up_rows(const ExpertArgs& a, const Slot& s, int row0, int col0, const Rows& rows,
-                                        const float* scale_g, const float* scale_u, float* red) {
+// The scales of one weight row block, chunk wave + kWaves l in lane l.
+__device__ __forceinline__ float lane_scale(const float* block, int chunks) {
+  const int kb = wave_id() + (threadIdx.x % 64) * kWaves;
+  return kb < chunks ? block[kb] : 0.0f;
+}
+__device__ __forceinline__ float of_lane(float v, int l) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+}
+// Chunks of one wave, in whole groups of U (those past the end are zeros).
+__device__ __forceinline__ int steps_of(int chunks, int U) { return (chunks + kWaves * U - 1) / (kWaves * U) * U; }
+
+// ---- gate and up ----
+
+// Items: one job and 16 NG columns of I (so 32 NG rows of w13).  A workgroup
+// walks its items; the four waves take the 128-wide chunks of H in turn and keep
+// U of them in flight, the first ones of the next item too.
+template <int MAXF, int NG, int U, int OCC>
+__global__ __launch_bounds__(kThreads, OCC) void k_moe_up(ExpertArgs a) {
   constexpr int NC = 2 * NG;
+  extern __shared__ __align__(16) uint32_t lds[];
+  __shared__ __align__(16) float red[kWaves * MAXF * NC * 256];
+  const Plan plan = make_plan(a, lds, 16 * MAXF);
   const int lane = threadIdx.x % 64, wave = wave_id(), fr = lane % 16, fg = lane / 16;
-  const int chunks = a.H / 128;
+  const int chunks = a.H / 128, steps = steps_of(chunks, U);
+  const int tiles = a.I / (16 * NG), items = plan.jobs * tiles;
   const int64_t panel = 2 * (int64_t)a.I * a.H;
-  const auto wb = buffer(a.w13 + (int64_t)s.expert * panel, panel);
   const auto xb = buffer(a.x, (int64_t)a.T * a.H);
   const auto sb = buffer(a.sx, (int64_t)a.T * chunks * 4);
-  uint32_t wrow[NC], xrow[MF], srow[MF];
-#pragma unroll
-  for (int n = 0; n < NC; ++n) wrow[n] = (uint32_t)(((n / NG) * a.I + col0 + (n % NG) * 16 + fr) * (int64_t)a.H + fg * 16);
-#pragma unroll
-  for (int f = 0; f < MF; ++f) {
-    const int r = row0 + f * 16 + fr;
-    const bool there = r < s.n;
-    const int t = there ? rows.token[r] : 0;
-    xrow[f] = there ? (uint32_t)(t * a.H + fg * 16) : kNoRow;
-    srow[f] = there ? (uint32_t)t * 4 : kNoRow;
-  }
 
+  // what is fetched next: chunk `step` (of this wave) of item `ahead`
+  int ahead = blockIdx.x, step = 0;
+  auto wb = buffer(a.w13, 0);
+  uint32_t wrow[NC], xrow[MAXF], srow[MAXF];
+  float next_g, next_u;                              // weight scales of item `ahead`
+  auto aim = [&]() {
+    const Job job = plan.at(min(ahead, items - 1) / tiles);
+    const int col0 = min(ahead, items - 1) % tiles * 16 * NG;
+    wb = buffer(a.w13 + job.expert * panel, ahead < items ? panel : 0);
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+      wrow[n] = (uint32_t)(((n / NG) * a.I + col0 + (n % NG) * 16 + fr) * (int64_t)a.H + fg * 16);
+#pragma unroll
+    for (int f = 0; f < MAXF; ++f) {
+      const int r = f * 16 + fr;
+      const bool there = r < job.n && ahead < items;
+      const uint32_t t = there ? plan.row[job.start + r] >> 16 : 0u;
+      xrow[f] = there ? t * (uint32_t)a.H + fg * 16 : kNoRow;
+      srow[f] = there ? t * 4 : kNoRow;
+    }
+    const float* sc = a.s13 + (int64_t)job.expert * (2 * a.I / 128) * chunks;
+    next_g = lane_scale(sc + (int64_t)(col0 / 128) * chunks, chunks);
+    next_u = lane_scale(sc + (int64_t)((a.I + col0) / 128) * chunks, chunks);
+  };
   struct Chunk {
-    u32x4 w0[NC], w1[NC], x0[MF], x1[MF];
-    float sx[MF];
+    u32x4 w0[NC], w1[NC], x0[MAXF], x1[MAXF];
+    float sx[MAXF];
   } c[U];
-  auto fetch = [&](Chunk& k, int kb) {
+  auto fetch = [&](Chunk& k) {
+    const int kb = wave + step * kWaves;
     const uint32_t at = kb < chunks ? (uint32_t)kb * 128 : kNoChunk;
     const uint32_t sat = kb < chunks ? (uint32_t)(kb * a.T * 4) : kNoChunk;
 #pragma unroll
@@ -172,86 +245,70 @@ __device__ __forceinline__ void up_rows(const ExpertArgs& a, const Slot& s, int 
       k.w1[n] = load16(wb, wrow[n] + at + 64);
     }
 #pragma unroll
-    for (int f = 0; f < MF; ++f) {
+    for (int f = 0; f < MAXF; ++f) {
       k.x0[f] = load16(xb, xrow[f] + at);
       k.x1[f] = load16(xb, xrow[f] + at + 64);
       k.sx[f] = load4(sb, srow[f] + sat);
     }
+    ++step;
   };
-  v4f acc[MF][NC];
+  if (ahead >= items) return;
+  aim();
 #pragma unroll
-  for (int f = 0; f < MF; ++f)
-#pragma unroll
-    for (int n = 0; n < NC; ++n) acc[f][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < U; ++i) fetch(c[i], wave + i * kWaves);
+  for (int i = 0; i < U; ++i) fetch(c[i]);
   const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k0 = wave; k0 < chunks; k0 += U * kWaves) {
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const Job job = plan.at(item / tiles);
+    const int col0 = item % tiles * 16 * NG, frags = (job.n + 15) / 16;
+    const float scale_g = next_g, scale_u = next_u;
+    v4f acc[MAXF][NC];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int kb = k0 + i * kWaves;
-      const float sg = scale_g[min(kb, chunks - 1)], su = scale_u[min(kb, chunks - 1)];
-      v8i x[MF];
+    for (int f = 0; f < MAXF; ++f)
 #pragma unroll
-      for (int f = 0; f < MF; ++f) x[f] = join(c[i].x0[f], c[i].x1[f]);
+      for (int n = 0; n < NC; ++n) acc[f][n] = zero;
+    for (int s0 = 0; s0 < steps; s0 += U) {
 #pragma unroll
-      for (int n = 0; n < NC; ++n) {
-        const v8i w = join(c[i].w0[n], c[i].w1[n]);
+      for (int i = 0; i < U; ++i) {
+        const float sg = of_lane(scale_g, s0 + i), su = of_lane(scale_u, s0 + i);
 #pragma unroll
-        for (int f = 0; f < MF; ++f) {
-          const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x[f], zero, 0, 0, 0, 0, 0, 0);
-          const float by = c[i].sx[f] * (n < NG ? sg : su);
+        for (int f = 0; f < MAXF; ++f) {
+          if (f && f >= frags) continue;
+          const v8i x = join(c[i].x0[f], c[i].x1[f]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[f][n][e] = __builtin_fmaf(p[e], by, acc[f][n][e]);
+          for (int n = 0; n < NC; ++n) {
+            const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(c[i].w0[n], c[i].w1[n]), x, zero, 0, 0,
+                                                                          0, 0, 0, 0);
+            const float by = c[i].sx[f] * (n < NG ? sg : su);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[f][n][e] = __builtin_fmaf(p[e], by, acc[f][n][e]);
+          }
         }
+        if (step == steps) {
+          ahead += gridDim.x;
+          step = 0;
+          aim();
+        }
+        fetch(c[i]);
       }
-      fetch(c[i], kb + U * kWaves);
     }
-  }
-  leave(acc, red);
-  const int m = threadIdx.x / 16, col = threadIdx.x % 16;
+    leave(acc, red);
+    const int m = threadIdx.x / 16, col = threadIdx.x % 16;
 #pragma unroll
-  for (int f = 0; f < MF; ++f) {
-    const int r = row0 + f * 16 + m;
-    if (r >= s.n) continue;
+    for (int f = 0; f < MAXF; ++f) {
+      const int r = f * 16 + m;
+      if (r >= job.n) continue;
+      const float share = plan.weight[job.start + r];
 #pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      const float g = total<MF, NC>(red, f, n, m, col), u = total<MF, NC>(red, f, NG + n, m, col);
-      const float v = rows.weight[r] * (g / (1.0f + expf(-g))) * u;
-      const __bf16 hi = (__bf16)v, lo = (__bf16)(v - (float)hi);
-      const int64_t at = (int64_t)(s.base + r) * a.I + place_of(col0 + n * 16 + col);
-      a.hi[at] = __builtin_bit_cast(uint16_t, hi);
-      a.lo[at] = __builtin_bit_cast(uint16_t, lo);
+      for (int n = 0; n < NG; ++n) {
+        const float g = total<MAXF, NC>(red, f, n, m, col), u = total<MAXF, NC>(red, f, NG + n, m, col);
+        const float v = share * (g / (1.0f + expf(-g))) * u;
+        const __bf16 hi = (__bf16)v, lo = (__bf16)(v - (float)hi);
+        const int64_t at = (int64_t)(job.start + r) * a.I + place_of(col0 + n * 16 + col);
+        a.hi[at] = __builtin_bit_cast(uint16_t, hi);
+        a.lo[at] = __builtin_bit_cast(uint16_t, lo);
+      }
     }
-  }
-  __syncthreads();
-}
-
-// One workgroup per slot and 16 NG columns of I.
-template <int MAXF, int NG>
-__global__ __launch_bounds__(kThreads) void k_moe_up(ExpertArgs a) {
-  __shared__ Rows rows;
-  __shared__ float scale_g[kMaxChunks], scale_u[kMaxChunks];
-  __shared__ __align__(16) float red[kWaves * MAXF * 2 * NG * 256];
-  const int tiles = a.I / (16 * NG), slot = blockIdx.x / tiles, col0 = (blockIdx.x % tiles) * 16 * NG;
-  const Slot s = find_rows(a, slot, rows);
-  if (blockIdx.x % tiles == 0) {                     // what k_moe_down needs to know
-    if (threadIdx.x == 0) a.slot[slot] = s;
-    for (int r = threadIdx.x; r < s.n; r += kThreads) a.place[s.base + r] = rows.place[r];
-  }
-  if (s.n == 0) return;
-  const int chunks = a.H / 128;
-  const float* sc = a.s13 + (int64_t)s.expert * (2 * a.I / 128) * chunks;
-  for (int k = threadIdx.x; k < chunks; k += kThreads) {
-    scale_g[k] = sc[(int64_t)(col0 / 128) * chunks + k];
-    scale_u[k] = sc[(int64_t)((a.I + col0) / 128) * chunks + k];
-  }
-  __syncthreads();
-  for (int row0 = 0; row0 < s.n; row0 += 16 * MAXF) {
-    const int left = (s.n - row0 + 15) / 16;
-    if (MAXF == 1 || left == 1) up_rows<1, NG, 3>(a, s, row0, col0, rows, scale_g, scale_u, red);
-    else if (MAXF == 2 || left == 2) up_rows<2 <= MAXF ? 2 : 1, NG, 2>(a, s, row0, col0, rows, scale_g, scale_u, red);
-    else up_rows<MAXF, NG, 2>(a, s, row0, col0, rows, scale_g, scale_u, red);
+    __syncthreads();
   }
 }
 
@@ -265,110 +322,125 @@ __device__ __forceinline__ v8bf to_bf16(uint32_t a, uint32_t b) {
   return v8bf{p[0], p[1], q[0], q[1], r[0], r[1], t[0], t[1]};
 }
 
-// MF row fragments, NC column fragments; the waves take the chunks of I in turn.
-template <int MF, int NC, int U>
-__device__ __forceinline__ void down_rows(const ExpertArgs& a, const Slot& s, int row0, int col0, float* red) {
+// Items: one job and 16 NC columns of H, walked like those of k_moe_up.
+template <int MAXF, int NC, int U, int OCC>
+__global__ __launch_bounds__(kThreads, OCC) void k_moe_down(ExpertArgs a) {
+  extern __shared__ __align__(16) uint32_t lds[];
+  __shared__ __align__(16) float red[kWaves * MAXF * NC * 256];
+  const Plan plan = make_plan(a, lds, 16 * MAXF);
   const int lane = threadIdx.x % 64, wave = wave_id(), fr = lane % 16, fg = lane / 16;
-  const int chunks = a.I / 128;
-  const int64_t panel = (int64_t)a.H * a.I;
-  const auto wb = buffer(a.w2 + (int64_t)s.expert * panel, panel);
-  const int64_t act = (int64_t)s.n * a.I * 2;        // rows of this slot (at most 2^24 bytes)
-  const auto hb = buffer(a.hi + (int64_t)s.base * a.I, act), lb = buffer(a.lo + (int64_t)s.base * a.I, act);
-  const float* sc = a.s2 + ((int64_t)s.expert * (a.H / 128) + col0 / 128) * chunks;
-  uint32_t wrow[NC], arow[MF];
+  const int chunks = a.I / 128, steps = steps_of(chunks, U);
+  const int tiles = a.H / (16 * NC), items = plan.jobs * tiles;
+  const int64_t panel = (int64_t)a.H * a.I, acts = (int64_t)a.T * a.topk * a.I * 2;
+  const auto hb = buffer(a.hi, acts), lb = buffer(a.lo, acts);
+
+  int ahead = blockIdx.x, step = 0;
+  auto wb = buffer(a.w2, 0);
+  uint32_t wrow[NC], arow[MAXF];
+  float next_scale;
+  auto aim = [&]() {
+    const Job job = plan.at(min(ahead, items - 1) / tiles);
+    const int col0 = min(ahead, items - 1) % tiles * 16 * NC;
+    wb = buffer(a.w2 + job.expert * panel, ahead < items ? panel : 0);
 #pragma unroll
-  for (int n = 0; n < NC; ++n) wrow[n] = (uint32_t)((col0 + n * 16 + fr) * (int64_t)a.I + fg * 16);
+    for (int n = 0; n < NC; ++n) wrow[n] = (uint32_t)((col0 + n * 16 + fr) * (int64_t)a.I + fg * 16);
+    next_scale = lane_scale(a.s2 + ((int64_t)job.expert * (a.H / 128) + col0 / 128) * chunks, chunks);
+  };
+  auto aim_acts = [&](int item) {
+    const Job job = plan.at(min(item, items - 1) / tiles);
 #pragma unroll
-  for (int f = 0; f < MF; ++f) arow[f] = (uint32_t)((row0 + f * 16 + fr) * (int64_t)a.I + fg * 8) * 2;  // past n: outside
+    for (int f = 0; f < MAXF; ++f) {
+      const int r = f * 16 + fr;
+      arow[f] = r < job.n && item < items ? (uint32_t)((job.start + r) * (int64_t)a.I + fg * 8) * 2 : kNoRow;
+    }
+  };
   struct Chunk {
     u32x4 w0[NC], w1[NC];
-    float scale;
   } c[U];
-  auto fetch = [&](Chunk& k, int kb) {
+  auto fetch = [&](Chunk& k) {
+    const int kb = wave + step * kWaves;
     const uint32_t at = kb < chunks ? (uint32_t)kb * 128 : kNoChunk;
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       k.w0[n] = load16(wb, wrow[n] + at);
       k.w1[n] = load16(wb, wrow[n] + at + 64);
     }
-    k.scale = sc[min(kb, chunks - 1)];
+    ++step;
   };
-  struct Acts {
-    u32x4 hi[MF][4], lo[MF][4];
-  };
-  auto fetch_acts = [&](Acts& k, int kb) {
-    const uint32_t at = kb < chunks ? (uint32_t)kb * 256 : kNoRow;
+  u32x4 hi[MAXF][4], lo[MAXF][4];
+  auto fetch_acts = [&](int s) {
+    const int kb = wave + s * kWaves;
+    const uint32_t at = kb < chunks ? (uint32_t)kb * 256 : kNoChunk;
 #pragma unroll
-    for (int f = 0; f < MF; ++f)
+    for (int f = 0; f < MAXF; ++f)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        k.hi[f][j] = load16(hb, arow[f] + at + j * 64);
-        k.lo[f][j] = load16(lb, arow[f] + at + j * 64);
+        hi[f][j] = load16(hb, arow[f] + at + j * 64);
+        lo[f][j] = load16(lb, arow[f] + at + j * 64);
       }
   };
-  v4f acc[MF][NC];
-#pragma unroll
-  for (int f = 0; f < MF; ++f)
-#pragma unroll
-    for (int n = 0; n < NC; ++n) acc[f][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  if (ahead >= items) return;
   // Loads return in the order they were issued, so the activations of a chunk
   // (from L2) go out ahead of weights (from memory) that are needed later.
-  Acts x;
-  fetch(c[0], wave);
-  fetch_acts(x, wave);
+  aim();
+  aim_acts(blockIdx.x);
+  fetch(c[0]);
+  fetch_acts(0);
 #pragma unroll
-  for (int i = 1; i < U; ++i) fetch(c[i], wave + i * kWaves);
-  for (int k0 = wave; k0 < chunks; k0 += U * kWaves) {
+  for (int i = 1; i < U; ++i) fetch(c[i]);
+  const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const Job job = plan.at(item / tiles);
+    const int col0 = item % tiles * 16 * NC, frags = (job.n + 15) / 16;
+    const float scales = next_scale;
+    v4f acc[MAXF][NC];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int kb = k0 + i * kWaves;
+    for (int f = 0; f < MAXF; ++f)
 #pragma unroll
-      for (int n = 0; n < NC; ++n) {
-        const v8bf b[4] = {to_bf16(c[i].w0[n].x, c[i].w0[n].y), to_bf16(c[i].w0[n].z, c[i].w0[n].w),
-                           to_bf16(c[i].w1[n].x, c[i].w1[n].y), to_bf16(c[i].w1[n].z, c[i].w1[n].w)};
+      for (int n = 0; n < NC; ++n) acc[f][n] = zero;
+    for (int s0 = 0; s0 < steps; s0 += U) {
 #pragma unroll
-        for (int f = 0; f < MF; ++f) {
-          v4f p{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int i = 0; i < U; ++i) {
+        const float scale = of_lane(scales, s0 + i);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, x.hi[f][j]), p, 0, 0, 0);
-            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, x.lo[f][j]), p, 0, 0, 0);
+        for (int n = 0; n < NC; ++n) {
+          const v8bf b[4] = {to_bf16(c[i].w0[n].x, c[i].w0[n].y), to_bf16(c[i].w0[n].z, c[i].w0[n].w),
+                             to_bf16(c[i].w1[n].x, c[i].w1[n].y), to_bf16(c[i].w1[n].z, c[i].w1[n].w)};
+#pragma unroll
+          for (int f = 0; f < MAXF; ++f) {
+            if (f && f >= frags) continue;
+            v4f p = zero;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, hi[f][j]), p, 0, 0, 0);
+              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, lo[f][j]), p, 0, 0, 0);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[f][n][e] = __builtin_fmaf(p[e], scale, acc[f][n][e]);
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[f][n][e] = __builtin_fmaf(p[e], c[i].scale, acc[f][n][e]);
         }
+        const bool last = s0 + i + 1 == steps;
+        if (last) aim_acts(item + gridDim.x);
+        fetch_acts(last ? 0 : s0 + i + 1);
+        if (step == steps) {
+          ahead += gridDim.x;
+          step = 0;
+          aim();
+        }
+        fetch(c[i]);
       }
-      fetch_acts(x, kb + kWaves);
-      fetch(c[i], kb + U * kWaves);
     }
-  }
-  leave(acc, red);
-  const int m = threadIdx.x / 16, col = threadIdx.x % 16;
+    leave(acc, red);
+    const int m = threadIdx.x / 16, col = threadIdx.x % 16;
 #pragma unroll
-  for (int f = 0; f < MF; ++f) {
-    const int r = row0 + f * 16 + m;
-    if (r >= s.n) continue;
-    float* to = a.part + (int64_t)a.place[s.base + r] * a.H + col0 + col;
+    for (int f = 0; f < MAXF; ++f) {
+      const int r = f * 16 + m;
+      if (r >= job.n) continue;
+      float* to = a.part + (int64_t)(plan.row[job.start + r] & 0xFFFF) * a.H + col0 + col;
 #pragma unroll
-    for (int n = 0; n < NC; ++n) to[n * 16] = total<MF, NC>(red, f, n, m, col);
-  }
-  __syncthreads();
-}
-
-// One workgroup per slot and 16 NC columns of H.
-template <int MAXF, int NC>
-__global__ __launch_bounds__(kThreads) void k_moe_down(ExpertArgs a) {
-  __shared__ __align__(16) float red[kWaves * MAXF * NC * 256];
-  const int tiles = a.H / (16 * NC), slot = blockIdx.x / tiles, col0 = (blockIdx.x % tiles) * 16 * NC;
-  Slot s = a.slot[slot];
-  s.expert = __builtin_amdgcn_readfirstlane(s.expert);
-  s.base = __builtin_amdgcn_readfirstlane(s.base);
-  s.n = __builtin_amdgcn_readfirstlane(s.n);
-  for (int row0 = 0; row0 < s.n; row0 += 16 * MAXF) {
-    const int left = (s.n - row0 + 15) / 16;
-    if (MAXF == 1 || left == 1) down_rows<1, NC, 2>(a, s, row0, col0, red);
-    else if (MAXF == 2 || left == 2) down_rows<2 <= MAXF ? 2 : 1, NC, 2>(a, s, row0, col0, red);
-    else down_rows<MAXF, NC, 2>(a, s, row0, col0, red);
+      for (int n = 0; n < NC; ++n) to[n * 16] = total<MAXF, NC>(red, f, n, m, col);
+    }
+    __syncthreads();
   }
 }
 
@@ -393,8 +465,6 @@ int64_t aligned(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 }  // namespace
 
-void experts_plan(ExpertArgs& a) { a.slots = std::min(a.E, a.T * a.topk); }
-
 int64_t experts_workspace(ExpertArgs& a, void* base) {
   const int64_t places = (int64_t)a.T * a.topk;
   uint8_t* p = static_cast<uint8_t*>(base);
@@ -407,24 +477,31 @@ int64_t experts_workspace(ExpertArgs& a, void* base) {
   a.hi = reinterpret_cast<uint16_t*>(take(places * a.I * 2));
   a.lo = reinterpret_cast<uint16_t*>(take(places * a.I * 2));
   a.part = reinterpret_cast<float*>(take(places * a.H * 4));
-  a.slot = reinterpret_cast<Slot*>(take(a.slots * (int64_t)sizeof(Slot)));
-  a.place = reinterpret_cast<int32_t*>(take(places * 4));
   return at;
 }
 
 namespace {
 
-template <int MAXF, int NG, int NC>
+constexpr int kCus = 256;
+
+// As many workgroups as run at once, or as may have an item.
+unsigned grid_of(const ExpertArgs& a, int tiles, int per_cu) {
+  const int64_t most = (int64_t)tiles * a.T * a.topk;
+  return (unsigned)std::min<int64_t>(most, (int64_t)kCus * per_cu);
+}
+
+template <int MAXF, int NG, int NC, int OCC_UP, int OCC_DOWN>
 void launch(const ExpertArgs& a, hipStream_t stream) {
-  k_moe_up<MAXF, NG><<<(unsigned)(a.I / (16 * NG) * a.slots), kThreads, 0, stream>>>(a);
-  k_moe_down<MAXF, NC><<<(unsigned)(a.H / (16 * NC) * a.slots), kThreads, 0, stream>>>(a);
+  const size_t lds = plan_bytes(a);
+  k_moe_up<MAXF, NG, 2, OCC_UP><<<grid_of(a, a.I / (16 * NG), OCC_UP), kThreads, lds, stream>>>(a);
+  k_moe_down<MAXF, NC, 2, OCC_DOWN><<<grid_of(a, a.H / (16 * NC), OCC_DOWN), kThreads, lds, stream>>>(a);
 }
 
 }  // namespace
 
 hipError_t launch_moe_experts(const ExpertArgs& a, hipStream_t stream) {
-  if (a.T <= 16) launch<1, 2, 4>(a, stream);
-  else launch<2, 2, 4>(a, stream);
+  if (a.T <= 16) launch<1, 2, 4, 3, 3>(a, stream);
+  else launch<2, 2, 4, 3, 2>(a, stream);
   k_moe_join<<<dim3((unsigned)((a.H / 4 + kThreads - 1) / kThreads), (unsigned)a.T), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }

@@ -118,7 +118,7 @@ fp8bs_status fp8bs_moe_route_backward(const void* logits, int32_t logits_type, c
  * activations are held as two BF16 parts (2^-17 of a value is lost) and meet the
  * codes of w2, which BF16 holds exactly; sums are FP32, in a fixed order.
  * Requires 0 <= T <= 128 (more tokens: the grouped GEMMs), 0 < topk <= 16,
- * 0 < E <= 1024, H and I multiples of 128 from 128 to 65536 with 2 H I < 2^31.
+ * 0 < E <= 1024, H and I multiples of 128 from 128 to 32768 with 2 H I < 2^31.
  */
 fp8bs_status fp8bs_moe_experts(const uint8_t* x, const float* sx, const int32_t* ids, const float* weights,
                                const uint8_t* w13, const float* s13, const uint8_t* w2, const float* s2, void* out,

@@ -116,7 +116,7 @@ def check_exact(w, **kw):
                                           (15, 128, 128, 1, 1), (16, 128, 128, 2, 2), (17, 128, 128, 1, 1),
                                           (31, 256, 128, 2, 1), (33, 128, 128, 2, 2), (49, 128, 256, 3, 2),
                                           (64, 128, 128, 1, 1), (65, 128, 128, 1, 1), (100, 256, 128, 2, 1),
-                                          (128, 128, 128, 2, 2), (128, 128, 128, 20, 16), (7, 640, 128, 64, 4)])
+                                          (128, 128, 128, 2, 2), (128, 128, 128, 20, 16), (7, 640, 128, 64, 4), (128, 128, 128, 1024, 16)])
 def test_experts_exactly(T, H, I, E, topk):
     check_exact(exact_case(T, H, I, E, topk, seed=T * 3 + H))
 

@@ -114,13 +114,13 @@ def test_experts(lib):
     n = I64(-1)
     assert ws(0, 256, 128, 4, 2, ctypes.byref(n)) == OK and n.value == 0
     assert ws(3, 256, 128, 4, 2, None) == NULL and ws(129, 256, 128, 4, 2, ctypes.byref(n)) == SHAPE
-    assert ws(128, 65536, 8192, 1024, 16, ctypes.byref(n)) == OK and n.value > 0
+    assert ws(128, 32768, 8192, 1024, 16, ctypes.byref(n)) == OK and n.value > 0
     assert ws(3, 256, 128, 4, 2, ctypes.byref(n)) == OK and n.value >= 3 * 2 * 128 * 4
     call = caller(lib, "fp8bs_moe_experts", [P, P, P, P, P, P, P, P, P, I64, I64, I64, I32, I32, I32, P, I64, P],
                   dict(x=FAKE, sx=FAKE, ids=FAKE, w=FAKE, w13=FAKE, s13=FAKE, w2=FAKE, s2=FAKE, out=FAKE, T=3, H=256,
                        I=128, E=4, k=2, dt=0, ws=FAKE, n=n.value, stream=None))
-    for bad in (dict(T=-1), dict(T=129), dict(H=0), dict(H=64), dict(H=65536 + 128), dict(I=0), dict(I=192), dict(E=0),
-                dict(E=1025), dict(k=0), dict(k=17), dict(H=65536, I=16384), dict(n=n.value - 1), dict(n=0)):
+    for bad in (dict(T=-1), dict(T=129), dict(H=0), dict(H=64), dict(H=32768 + 128), dict(I=0), dict(I=192), dict(E=0),
+                dict(E=1025), dict(k=0), dict(k=17), dict(H=32768, I=32768), dict(n=n.value - 1), dict(n=0)):
         assert call(**bad) == SHAPE, bad
     assert call(dt=2) == FLAGS and call(dt=-1) == FLAGS
     assert call(T=0, n=0, x=None, ws=None) == OK
