@@ -65,6 +65,7 @@ struct ExpertArgs {
   uint16_t* hi;              // [T topk][I] BF16, weighted activations
   uint16_t* lo;              // what hi leaves
   float* part;               // [T topk][H] second product, by place
+  uint32_t* image;           // jobs, their number, rows
 };
 
 int32_t norm_back_groups(int64_t M, int64_t K);

@@ -123,7 +123,7 @@ fp8bs_status fp8bs_moe_experts(const uint8_t* x, const float* sx, const int32_t*
                                void* workspace, int64_t workspace_bytes, fp8bs_stream_t stream) {
   if (!expert_sizes_fit(T, H, I, E, topk)) return FP8BS_ERR_SHAPE;
   fp8bs::ExpertArgs a{x, sx, ids, weights, w13, s13, w2, s2, out, out_dtype == FP8BS_OUT_FP32, (int32_t)T, (int32_t)H,
-                      (int32_t)I, E, topk, nullptr, nullptr, nullptr};
+                      (int32_t)I, E, topk, nullptr, nullptr, nullptr, nullptr};
   if (workspace_bytes < (T == 0 ? 0 : experts_workspace(a, workspace))) return FP8BS_ERR_SHAPE;
   if (out_dtype != FP8BS_OUT_BF16 && out_dtype != FP8BS_OUT_FP32) return FP8BS_ERR_FLAGS;
   if (T == 0) return FP8BS_OK;

@@ -57,15 +57,14 @@ struct Job {
 };
 __device__ __forceinline__ uint32_t pack(int expert, int start, int n) { return expert | start << 10 | n << 22; }
 
-// The call's rows and jobs, worked out from ids by every workgroup in its own
-// LDS: a bit per (expert, token), so that the order in which they are set does
-// not matter; then sums over the experts.
+// The call's rows and jobs.  k_moe_up works them out from ids, every workgroup in
+// its own LDS: a bit per (expert, token), so that the order in which the bits are
+// set does not matter; then sums over the experts.  The first workgroup leaves
+// them in the workspace for k_moe_down.
 struct Plan {
-  uint32_t* mask;   // [E][words]
-  int* base;        // [E] rows of the experts before
   uint32_t* job;    // [jobs]
-  uint32_t* row;    // token << 16 | place
-  float* weight;    // [rows]
+  uint32_t* row;    // [rows] token << 16 | place
+  float* weight;    // [rows]; k_moe_up only
   int jobs;
 
   __device__ __forceinline__ Job at(int j) const {
@@ -74,26 +73,29 @@ struct Plan {
   }
 };
 __host__ __device__ __forceinline__ int mask_words(int T) { return (T + 31) / 32; }
-int plan_bytes(const ExpertArgs& a) {
-  return (a.E * (mask_words(a.T) + 1) + a.T * a.topk * 3) * 4;
-}
+// (LDS of k_moe_up: jobs, rows, weights, places' ids; bits and base of each expert)
+int plan_bytes(const ExpertArgs& a) { return (a.T * a.topk * 4 + a.E * (mask_words(a.T) + 1)) * 4; }
+int image_words(const ExpertArgs& a) { return 1 + 2 * a.T * a.topk; }
 
 // `block`: rows that one pass over an expert's weights serves.
 __device__ __forceinline__ Plan make_plan(const ExpertArgs& a, uint32_t* lds, int block) {
   __shared__ int waves[kWaves];
   const int tid = threadIdx.x, places = a.T * a.topk, words = mask_words(a.T);
   Plan p;
-  p.mask = lds;
-  p.base = reinterpret_cast<int*>(p.mask + a.E * words);
-  p.job = reinterpret_cast<uint32_t*>(p.base + a.E);
+  p.job = lds;
   p.row = p.job + places;
   p.weight = reinterpret_cast<float*>(p.row + places);
-  for (int i = tid; i < a.E * words; i += kThreads) p.mask[i] = 0u;
+  int* id = reinterpret_cast<int*>(p.weight + places);
+  uint32_t* mask = reinterpret_cast<uint32_t*>(id + places);   // [E][words]
+  int* base = reinterpret_cast<int*>(mask + a.E * words);      // rows of the experts before
+  const float early = tid < places ? a.weights[tid] : 0.0f;    // (in flight with the ids)
+  for (int i = tid; i < places; i += kThreads) id[i] = a.ids[i];
+  for (int i = tid; i < a.E * words; i += kThreads) mask[i] = 0u;
   __syncthreads();
   for (int i = tid; i < places; i += kThreads) {
-    const uint32_t e = (uint32_t)a.ids[i];
+    const uint32_t e = (uint32_t)id[i];
     const int t = i / a.topk;
-    if (e < (uint32_t)a.E) atomicOr(&p.mask[e * words + t / 32], 1u << (t % 32));
+    if (e < (uint32_t)a.E) atomicOr(&mask[e * words + t / 32], 1u << (t % 32));
   }
   __syncthreads();
   // thread -> `each` experts in a row; rows and jobs before them, as one number
@@ -101,7 +103,7 @@ __device__ __forceinline__ Plan make_plan(const ExpertArgs& a, uint32_t* lds, in
   int mine = 0;
   auto rows_of = [&](int e) {
     int n = 0;
-    for (int w = 0; w < words; ++w) n += __builtin_popcount(p.mask[e * words + w]);
+    for (int w = 0; w < words; ++w) n += __builtin_popcount(mask[e * words + w]);
     return n;
   };
   for (int e = tid * each; e < min(a.E, (tid + 1) * each); ++e) {
@@ -125,25 +127,38 @@ __device__ __forceinline__ Plan make_plan(const ExpertArgs& a, uint32_t* lds, in
   p.jobs = __builtin_amdgcn_readfirstlane(all >> 16);
   for (int e = tid * each; e < min(a.E, (tid + 1) * each); ++e) {
     const int n = rows_of(e), start = before & 0xFFFF, job = before >> 16;
-    p.base[e] = start;
+    base[e] = start;
     for (int r = 0; r < n; r += block) p.job[job + r / block] = pack(e, start + r, min(block, n - r));
     before += n | ((n + block - 1) / block) << 16;
   }
   __syncthreads();
   // a row per expert of a token: from the expert's first place there
   for (int i = tid; i < places; i += kThreads) {
-    const int t = i / a.topk, id = a.ids[i];
-    bool first = (uint32_t)id < (uint32_t)a.E;
-    for (int c = t * a.topk; c < i; ++c) first = first && a.ids[c] != id;
+    const int t = i / a.topk, e = id[i];
+    bool first = (uint32_t)e < (uint32_t)a.E;
+    for (int c = t * a.topk; c < i; ++c) first = first && id[c] != e;
     if (!first) continue;
-    float w = 0.0f;
-    for (int c = i; c < (t + 1) * a.topk; ++c) w += a.ids[c] == id ? a.weights[c] : 0.0f;
-    int r = p.base[id];
-    for (int k = 0; k < t / 32; ++k) r += __builtin_popcount(p.mask[id * words + k]);
-    r += __builtin_popcount(p.mask[id * words + t / 32] & ((1u << (t % 32)) - 1));
+    float w = i == tid ? early : a.weights[i];
+    for (int c = i + 1; c < (t + 1) * a.topk; ++c)
+      if (id[c] == e) w += a.weights[c];
+    int r = base[e];
+    for (int k = 0; k < t / 32; ++k) r += __builtin_popcount(mask[e * words + k]);
+    r += __builtin_popcount(mask[e * words + t / 32] & ((1u << (t % 32)) - 1));
     p.row[r] = (uint32_t)t << 16 | (uint32_t)i;
     p.weight[r] = w;
   }
+  __syncthreads();
+  if (blockIdx.x == 0) {                             // (places without a row hold what LDS held: never used)
+    for (int i = tid; i < 2 * places; i += kThreads) a.image[1 + i] = p.job[i];
+    if (tid == 0) a.image[0] = (uint32_t)p.jobs;
+  }
+  return p;
+}
+
+__device__ __forceinline__ Plan load_plan(const ExpertArgs& a, uint32_t* lds) {
+  const int places = a.T * a.topk;
+  Plan p{lds, lds + places, nullptr, __builtin_amdgcn_readfirstlane((int)a.image[0])};
+  for (int i = threadIdx.x; i < 2 * places; i += kThreads) lds[i] = a.image[1 + i];
   __syncthreads();
   return p;
 }
@@ -327,7 +342,7 @@ template <int MAXF, int NC, int U, int OCC>
 __global__ __launch_bounds__(kThreads, OCC) void k_moe_down(ExpertArgs a) {
   extern __shared__ __align__(16) uint32_t lds[];
   __shared__ __align__(16) float red[kWaves * MAXF * NC * 256];
-  const Plan plan = make_plan(a, lds, 16 * MAXF);
+  const Plan plan = load_plan(a, lds);
   const int lane = threadIdx.x % 64, wave = wave_id(), fr = lane % 16, fg = lane / 16;
   const int chunks = a.I / 128, steps = steps_of(chunks, U);
   const int tiles = a.H / (16 * NC), items = plan.jobs * tiles;
@@ -444,18 +459,33 @@ __global__ __launch_bounds__(kThreads, OCC) void k_moe_down(ExpertArgs a) {
   }
 }
 
-// out[t] = the rows of token t's places added up in turn.  Places without a row
-// (an id outside, or one that stands further left too) are left out.
+// Bit c: place c of token t has a row (its id is inside, and stands no further
+// left).  The same for the whole wave.
+__device__ __forceinline__ uint32_t places_with_rows(const ExpertArgs& a, int t) {
+  const int lane = threadIdx.x % 64;
+  const int id = lane < a.topk ? a.ids[t * a.topk + lane] : -1;
+  bool counts = (uint32_t)id < (uint32_t)a.E;
+  for (int c = 0; c < a.topk; ++c) counts = counts && !(c < lane && __builtin_amdgcn_readlane(id, c) == id);
+  return (uint32_t)__builtin_amdgcn_ballot_w64(counts);
+}
+
+// out[t] = the rows of token t's places added up in turn.  (Places without a row
+// are read, inside the workspace, and left out.)
 __global__ __launch_bounds__(kThreads) void k_moe_join(ExpertArgs a) {
-  const int h = (blockIdx.x * kThreads + threadIdx.x) * 4, t = blockIdx.y;
-  if (h >= a.H) return;
-  const int32_t* ids = a.ids + t * a.topk;
+  const int t = blockIdx.y, h0 = (blockIdx.x * kThreads + threadIdx.x) * 4, h = min(h0, a.H - 4);
   v4f v{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int c = 0; c < a.topk; ++c) {
-    bool counts = (uint32_t)ids[c] < (uint32_t)a.E;
-    for (int b = 0; b < c; ++b) counts = counts && ids[b] != ids[c];
-    if (counts) v += *reinterpret_cast<const v4f*>(a.part + (int64_t)(t * a.topk + c) * a.H + h);
+  const v4f* from = reinterpret_cast<const v4f*>(a.part + (int64_t)t * a.topk * a.H + h);
+  const int step = a.H / 4;
+  const uint32_t there = places_with_rows(a, t);
+  for (int c0 = 0; c0 < a.topk; c0 += 8) {           // eight rows in flight (16 at most)
+    v4f r[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) r[c] = from[min(c0 + c, a.topk - 1) * step];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (there >> (c0 + c) & 1) v += r[c];
   }
+  if (h0 >= a.H) return;
   const int64_t at = (int64_t)t * a.H + h;
   if (a.out_f32) *reinterpret_cast<v4f*>(static_cast<float*>(a.out) + at) = v;
   else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
@@ -477,6 +507,7 @@ int64_t experts_workspace(ExpertArgs& a, void* base) {
   a.hi = reinterpret_cast<uint16_t*>(take(places * a.I * 2));
   a.lo = reinterpret_cast<uint16_t*>(take(places * a.I * 2));
   a.part = reinterpret_cast<float*>(take(places * a.H * 4));
+  a.image = reinterpret_cast<uint32_t*>(take(image_words(a) * 4));
   return at;
 }
 
@@ -500,8 +531,7 @@ void launch(const ExpertArgs& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_moe_experts(const ExpertArgs& a, hipStream_t stream) {
-  if (a.T <= 16) launch<1, 2, 4, 3, 3>(a, stream);
-  else launch<2, 2, 4, 3, 2>(a, stream);
+  launch<1, 2, 4, 3, 3>(a, stream);
   k_moe_join<<<dim3((unsigned)((a.H / 4 + kThreads - 1) / kThreads), (unsigned)a.T), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
