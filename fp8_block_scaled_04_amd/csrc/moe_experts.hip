@@ -459,6 +459,280 @@ __global__ __launch_bounds__(kThreads, OCC) void k_moe_down(ExpertArgs a) {
   }
 }
 
+// ---- many rows per expert ----
+//
+// The tokens' rows of a job go through LDS, once per workgroup; its waves take
+// different columns, all of K.  A piece of the rows is in flight while the one
+// before is in use, in two buffers; one barrier per piece.
+
+constexpr int kPiece = 4;   // chunks of H per piece in k_moe_up_wide
+
+// Segment s (16 bytes) of a row of 8 (16) segments is kept at s ^ key: the 16
+// rows that a wave reads at one segment fall on different banks.
+__device__ __forceinline__ int swizzle8(int row, int s) { return s ^ ((row >> 1) & 7); }
+__device__ __forceinline__ int swizzle16(int row, int s) { return s ^ (row & 15); }
+
+// One workgroup per job and 64 columns of I, 16 per wave.
+template <int MF, int U>
+__device__ __forceinline__ void up_wide(const ExpertArgs& a, const Plan& plan, const Job& job, int col0, uint8_t* stage) {
+  // stage: [2][kPiece][16 MF rows][128], then scales [2][kPiece][16 MF + 2]
+  constexpr int kRows = 16 * MF, kBuf = kPiece * kRows * 128, kPer = kRows * 8 * kPiece / kThreads;
+  constexpr int kScales = kPiece * (kRows + 2);
+  static_assert(U == kPiece, "a chunk's place in the ring is its place in the piece");
+  float* scales = reinterpret_cast<float*>(stage + 2 * kBuf);
+  const int tid = threadIdx.x, lane = tid % 64, wave = wave_id(), fr = lane % 16, fg = lane / 16;
+  const int chunks = a.H / 128, pieces = (chunks + kPiece - 1) / kPiece;
+  const int64_t panel = 2 * (int64_t)a.I * a.H;
+  const auto wb = buffer(a.w13 + job.expert * panel, panel);
+  const auto xb = buffer(a.x, (int64_t)a.T * a.H);
+  const int col = col0 + wave * 16;
+  const uint32_t gate = (uint32_t)((col + fr) * (int64_t)a.H + fg * 16);
+  const uint32_t up = gate + (uint32_t)(a.I * (int64_t)a.H);
+
+  // this thread's segments of a piece: row, chunk and place in the chunk
+  u32x4 x[kPer];
+  uint32_t from[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int p = i * kThreads + tid, r = p / (8 * kPiece), s = p % (8 * kPiece);
+    from[i] = r < job.n ? (plan.row[job.start + min(r, job.n - 1)] >> 16) * (uint32_t)a.H + s * 16 : kNoRow;
+  }
+  // and its scales: of rows (one chunk each), of the weights
+  constexpr int kPerScale = (kScales + kThreads - 1) / kThreads;
+  float sc[kPerScale];
+  auto fetch_piece = [&](int piece) {
+    const uint32_t at = (uint32_t)piece * kPiece * 128;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int s = (i * kThreads + tid) % (8 * kPiece);
+      x[i] = load16(xb, piece * kPiece + s / 8 < chunks ? from[i] + at : kNoRow);
+    }
+#pragma unroll
+    for (int i = 0; i < kPerScale; ++i) {
+      const int p = i * kThreads + tid, c = p / (kRows + 2), r = p % (kRows + 2), kb = piece * kPiece + c;
+      sc[i] = 0.0f;
+      if (p < kScales && kb < chunks) {
+        const int64_t block = r == kRows ? col0 / 128 : (a.I + col0) / 128;
+        if (r >= kRows) sc[i] = a.s13[((int64_t)job.expert * (2 * a.I / 128) + block) * chunks + kb];
+        else if (r < job.n) sc[i] = a.sx[(int64_t)kb * a.T + (plan.row[job.start + r] >> 16)];
+      }
+    }
+  };
+  auto keep_piece = [&](int piece) {
+    uint8_t* to = stage + (piece & 1) * kBuf;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int p = i * kThreads + tid, r = p / (8 * kPiece), s = p % (8 * kPiece);
+      *reinterpret_cast<u32x4*>(to + ((s / 8) * kRows + r) * 128 + swizzle8(r, s % 8) * 16) = x[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kPerScale; ++i)
+      if (i * kThreads + tid < kScales) scales[(piece & 1) * kScales + i * kThreads + tid] = sc[i];
+  };
+  u32x4 w[U][4];
+  auto fetch = [&](int i, int kb) {
+    const uint32_t at = kb < chunks ? (uint32_t)kb * 128 : kNoChunk;
+    w[i][0] = load16(wb, gate + at);
+    w[i][1] = load16(wb, gate + at + 64);
+    w[i][2] = load16(wb, up + at);
+    w[i][3] = load16(wb, up + at + 64);
+  };
+  const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
+  v4f ag[MF], au[MF];
+#pragma unroll
+  for (int f = 0; f < MF; ++f) ag[f] = au[f] = zero;
+  fetch_piece(0);
+#pragma unroll
+  for (int i = 0; i < U; ++i) fetch(i, i);
+  for (int piece = 0; piece < pieces; ++piece) {
+    keep_piece(piece);
+    __syncthreads();
+    fetch_piece(piece + 1);
+    const uint8_t* xs = stage + (piece & 1) * kBuf;
+    const float* ss = scales + (piece & 1) * kScales;
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) {
+      const v8i g = join(w[i][0], w[i][1]), u = join(w[i][2], w[i][3]);
+      const float sg = ss[i * (kRows + 2) + kRows], su = ss[i * (kRows + 2) + kRows + 1];
+#pragma unroll
+      for (int f = 0; f < MF; ++f) {
+        const int r = f * 16 + fr;
+        const uint8_t* row = xs + (i * kRows + r) * 128;
+        const v8i xf = join(*reinterpret_cast<const u32x4*>(row + swizzle8(r, fg) * 16),
+                            *reinterpret_cast<const u32x4*>(row + swizzle8(r, fg + 4) * 16));
+        const float sx = ss[i * (kRows + 2) + r];
+        const v4f pg = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(g, xf, zero, 0, 0, 0, 0, 0, 0);
+        const v4f pu = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(u, xf, zero, 0, 0, 0, 0, 0, 0);
+        const float wg = sx * sg, wu = sx * su;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          ag[f][e] = __builtin_fmaf(pg[e], wg, ag[f][e]);
+          au[f][e] = __builtin_fmaf(pu[e], wu, au[f][e]);
+        }
+      }
+      fetch(i, (piece + 1) * kPiece + i);
+    }
+  }
+  // a lane has four columns of a row
+#pragma unroll
+  for (int f = 0; f < MF; ++f) {
+    const int r = f * 16 + fr;
+    if (r >= job.n) continue;
+    const float share = plan.weight[job.start + r];
+    float hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float g = ag[f][e], v = share * (g / (1.0f + expf(-g))) * au[f][e];
+      hi[e] = v;
+      lo[e] = v - (float)(__bf16)v;
+    }
+    const int64_t at = (int64_t)(job.start + r) * a.I + place_of(col + fg * 4);
+    *reinterpret_cast<uint2*>(a.hi + at) = make_uint2(pack2_bf16(hi[0], hi[1]), pack2_bf16(hi[2], hi[3]));
+    *reinterpret_cast<uint2*>(a.lo + at) = make_uint2(pack2_bf16(lo[0], lo[1]), pack2_bf16(lo[2], lo[3]));
+  }
+}
+
+constexpr int kUpStage = 2 * kPiece * (64 * 128 + 66 * 4);   // bytes, for 64 rows
+
+__global__ __launch_bounds__(kThreads, 2) void k_moe_up_wide(ExpertArgs a) {
+  extern __shared__ __align__(16) uint32_t lds[];
+  const Plan plan = make_plan(a, lds + kUpStage / 4, 64);
+  const int tiles = a.I / 64;
+  if ((int)blockIdx.x >= plan.jobs * tiles) return;
+  const Job job = plan.at(blockIdx.x / tiles);
+  const int col0 = blockIdx.x % tiles * 64;
+  uint8_t* stage = reinterpret_cast<uint8_t*>(lds);
+  if (job.n <= 16) up_wide<1, kPiece>(a, plan, job, col0, stage);
+  else if (job.n <= 32) up_wide<2, kPiece>(a, plan, job, col0, stage);
+  else up_wide<4, kPiece>(a, plan, job, col0, stage);
+}
+
+// One workgroup per job and 64 NC columns of H, 16 NC per wave; a piece is one
+// chunk of I.
+template <int MF, int NC, int U>
+__device__ __forceinline__ void down_wide(const ExpertArgs& a, const Plan& plan, const Job& job, int col0,
+                                          uint8_t* stage) {
+  // stage: [2][hi, lo][16 MF rows][256]
+  constexpr int kRows = 16 * MF, kBuf = 2 * kRows * 256, kPer = kBuf / 16 / kThreads;
+  const int tid = threadIdx.x, lane = tid % 64, wave = wave_id(), fr = lane % 16, fg = lane / 16;
+  const int chunks = a.I / 128;
+  const int64_t panel = (int64_t)a.H * a.I, acts = (int64_t)a.T * a.topk * a.I * 2;
+  const auto wb = buffer(a.w2 + job.expert * panel, panel);
+  const auto hb = buffer(a.hi, acts), lb = buffer(a.lo, acts);
+  const float* sc = a.s2 + ((int64_t)job.expert * (a.H / 128) + col0 / 128) * chunks;
+  const int col = col0 + wave * 16 * NC;
+  uint32_t wrow[NC];
+#pragma unroll
+  for (int n = 0; n < NC; ++n) wrow[n] = (uint32_t)((col + n * 16 + fr) * (int64_t)a.I + fg * 16);
+  u32x4 x[kPer];
+  uint32_t from[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int r = (i * kThreads + tid) / 16 % kRows, s = tid % 16;
+    from[i] = r < job.n ? (uint32_t)((job.start + r) * (int64_t)a.I) * 2 + s * 16 : kNoRow;
+  }
+  auto fetch_piece = [&](int kb) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const uint32_t at = kb < chunks ? from[i] + (uint32_t)kb * 256 : kNoRow;
+      x[i] = i < kPer / 2 ? load16(hb, at) : load16(lb, at);
+    }
+  };
+  auto keep_piece = [&](int kb) {
+    uint8_t* to = stage + (kb & 1) * kBuf;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int p = i * kThreads + tid, r = p / 16;     // (rows of lo after those of hi)
+      *reinterpret_cast<u32x4*>(to + r * 256 + swizzle16(r, tid % 16) * 16) = x[i];
+    }
+  };
+  u32x4 w[U][NC][2];
+  float scale[U];
+  auto fetch = [&](int i, int kb) {
+    const uint32_t at = kb < chunks ? (uint32_t)kb * 128 : kNoChunk;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      w[i][n][0] = load16(wb, wrow[n] + at);
+      w[i][n][1] = load16(wb, wrow[n] + at + 64);
+    }
+    scale[i] = sc[min(kb, chunks - 1)];
+  };
+  const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
+  v4f acc[MF][NC];
+#pragma unroll
+  for (int f = 0; f < MF; ++f)
+#pragma unroll
+    for (int n = 0; n < NC; ++n) acc[f][n] = zero;
+  fetch_piece(0);
+#pragma unroll
+  for (int i = 0; i < U; ++i) fetch(i, i);
+  for (int k0 = 0; k0 < chunks; k0 += U) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int kb = k0 + i;
+      keep_piece(kb);
+      __syncthreads();
+      fetch_piece(kb + 1);
+      const uint8_t* xs = stage + (kb & 1) * kBuf;
+      v8bf b[NC][4];
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        b[n][0] = to_bf16(w[i][n][0].x, w[i][n][0].y);
+        b[n][1] = to_bf16(w[i][n][0].z, w[i][n][0].w);
+        b[n][2] = to_bf16(w[i][n][1].x, w[i][n][1].y);
+        b[n][3] = to_bf16(w[i][n][1].z, w[i][n][1].w);
+      }
+#pragma unroll
+      for (int f = 0; f < MF; ++f) {
+        const int r = f * 16 + fr;
+        v4f p[NC];
+#pragma unroll
+        for (int n = 0; n < NC; ++n) p[n] = zero;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const v8bf hi = *reinterpret_cast<const v8bf*>(xs + r * 256 + swizzle16(r, j * 4 + fg) * 16);
+          const v8bf lo = *reinterpret_cast<const v8bf*>(xs + (kRows + r) * 256 + swizzle16(r, j * 4 + fg) * 16);
+#pragma unroll
+          for (int n = 0; n < NC; ++n) p[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[n][j], hi, p[n], 0, 0, 0);
+#pragma unroll
+          for (int n = 0; n < NC; ++n) p[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[n][j], lo, p[n], 0, 0, 0);
+        }
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[f][n][e] = __builtin_fmaf(p[n][e], scale[i], acc[f][n][e]);
+      }
+      fetch(i, kb + U);
+    }
+  }
+#pragma unroll
+  for (int f = 0; f < MF; ++f) {
+    const int r = f * 16 + fr;
+    if (r >= job.n) continue;
+    float* to = a.part + (int64_t)(plan.row[job.start + r] & 0xFFFF) * a.H + col + fg * 4;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) *reinterpret_cast<v4f*>(to + n * 16) = acc[f][n];
+  }
+}
+
+constexpr int kDownStage = 2 * 2 * 64 * 256;   // bytes, for 64 rows
+
+template <int NC>
+__global__ __launch_bounds__(kThreads, 2) void k_moe_down_wide(ExpertArgs a) {
+  extern __shared__ __align__(16) uint32_t lds[];
+  const Plan plan = load_plan(a, lds + kDownStage / 4);
+  const int tiles = a.H / (64 * NC);
+  if ((int)blockIdx.x >= plan.jobs * tiles) return;
+  const Job job = plan.at(blockIdx.x / tiles);
+  const int col0 = blockIdx.x % tiles * 64 * NC;
+  uint8_t* stage = reinterpret_cast<uint8_t*>(lds);
+  if (job.n <= 16) down_wide<1, NC, 4>(a, plan, job, col0, stage);
+  else if (job.n <= 32) down_wide<2, NC, 4>(a, plan, job, col0, stage);
+  else down_wide<4, NC, 4>(a, plan, job, col0, stage);
+}
+
+// ---- the sum over a token's experts ----
+
 // Bit c: place c of token t has a row (its id is inside, and stands no further
 // left).  The same for the whole wave.
 __device__ __forceinline__ uint32_t places_with_rows(const ExpertArgs& a, int t) {
@@ -528,10 +802,21 @@ void launch(const ExpertArgs& a, hipStream_t stream) {
   k_moe_down<MAXF, NC, 2, OCC_DOWN><<<grid_of(a, a.H / (16 * NC), OCC_DOWN), kThreads, lds, stream>>>(a);
 }
 
+// Whether an expert has enough rows, were they spread evenly.
+bool wide(const ExpertArgs& a) { return a.T * a.topk >= 4 * std::min(a.E, a.T * a.topk); }
+
 }  // namespace
 
 hipError_t launch_moe_experts(const ExpertArgs& a, hipStream_t stream) {
-  launch<1, 2, 4, 3, 3>(a, stream);
+  if (wide(a)) {
+    // (jobs of up to 64 rows: at most one per expert with a row, and one more per 64 rows)
+    const int64_t jobs = std::min(a.E, a.T * a.topk) + a.T * a.topk / 64;
+    const size_t plan = plan_bytes(a);
+    k_moe_up_wide<<<(unsigned)(jobs * (a.I / 64)), kThreads, kUpStage + plan, stream>>>(a);
+    k_moe_down_wide<2><<<(unsigned)(jobs * (a.H / 128)), kThreads, kDownStage + plan, stream>>>(a);
+  } else {
+    launch<1, 2, 4, 3, 3>(a, stream);
+  }
   k_moe_join<<<dim3((unsigned)((a.H / 4 + kThreads - 1) / kThreads), (unsigned)a.T), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
