@@ -619,11 +619,11 @@ __device__ __forceinline__ void down_wide(const ExpertArgs& a, const Plan& plan,
   const int64_t panel = (int64_t)a.H * a.I, acts = (int64_t)a.T * a.topk * a.I * 2;
   const auto wb = buffer(a.w2 + job.expert * panel, panel);
   const auto hb = buffer(a.hi, acts), lb = buffer(a.lo, acts);
-  const float* sc = a.s2 + ((int64_t)job.expert * (a.H / 128) + col0 / 128) * chunks;
-  const int col = col0 + wave * 16 * NC;
+  const int col = col0 + wave * 16 * NC;             // (past H: nothing is read or written)
+  const float* sc = a.s2 + ((int64_t)job.expert * (a.H / 128) + min(col, a.H - 1) / 128) * chunks;
   uint32_t wrow[NC];
 #pragma unroll
-  for (int n = 0; n < NC; ++n) wrow[n] = (uint32_t)((col + n * 16 + fr) * (int64_t)a.I + fg * 16);
+  for (int n = 0; n < NC; ++n) wrow[n] = col < a.H ? (uint32_t)((col + n * 16 + fr) * (int64_t)a.I + fg * 16) : kNoRow;
   u32x4 x[kPer];
   uint32_t from[kPer];
 #pragma unroll
@@ -708,7 +708,7 @@ __device__ __forceinline__ void down_wide(const ExpertArgs& a, const Plan& plan,
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
     const int r = f * 16 + fr;
-    if (r >= job.n) continue;
+    if (r >= job.n || col >= a.H) continue;
     float* to = a.part + (int64_t)(plan.row[job.start + r] & 0xFFFF) * a.H + col + fg * 4;
 #pragma unroll
     for (int n = 0; n < NC; ++n) *reinterpret_cast<v4f*>(to + n * 16) = acc[f][n];
@@ -717,18 +717,24 @@ __device__ __forceinline__ void down_wide(const ExpertArgs& a, const Plan& plan,
 
 constexpr int kDownStage = 2 * 2 * 64 * 256;   // bytes, for 64 rows
 
-template <int NC>
+// 256 columns (more rows: 128, twice, for their accumulators).
 __global__ __launch_bounds__(kThreads, 2) void k_moe_down_wide(ExpertArgs a) {
   extern __shared__ __align__(16) uint32_t lds[];
   const Plan plan = load_plan(a, lds + kDownStage / 4);
-  const int tiles = a.H / (64 * NC);
+  const int tiles = (a.H + 255) / 256;
   if ((int)blockIdx.x >= plan.jobs * tiles) return;
   const Job job = plan.at(blockIdx.x / tiles);
-  const int col0 = blockIdx.x % tiles * 64 * NC;
+  const int col0 = blockIdx.x % tiles * 256;
   uint8_t* stage = reinterpret_cast<uint8_t*>(lds);
-  if (job.n <= 16) down_wide<1, NC, 4>(a, plan, job, col0, stage);
-  else if (job.n <= 32) down_wide<2, NC, 4>(a, plan, job, col0, stage);
-  else down_wide<4, NC, 4>(a, plan, job, col0, stage);
+  if (job.n <= 16) {
+    down_wide<1, 4, 2>(a, plan, job, col0, stage);
+  } else if (job.n <= 32) {
+    down_wide<2, 4, 2>(a, plan, job, col0, stage);
+  } else {
+    down_wide<4, 2, 4>(a, plan, job, col0, stage);
+    __syncthreads();
+    down_wide<4, 2, 4>(a, plan, job, col0 + 128, stage);
+  }
 }
 
 // ---- the sum over a token's experts ----
@@ -813,7 +819,7 @@ hipError_t launch_moe_experts(const ExpertArgs& a, hipStream_t stream) {
     const int64_t jobs = std::min(a.E, a.T * a.topk) + a.T * a.topk / 64;
     const size_t plan = plan_bytes(a);
     k_moe_up_wide<<<(unsigned)(jobs * (a.I / 64)), kThreads, kUpStage + plan, stream>>>(a);
-    k_moe_down_wide<2><<<(unsigned)(jobs * (a.H / 128)), kThreads, kDownStage + plan, stream>>>(a);
+    k_moe_down_wide<<<(unsigned)(jobs * ((a.H + 255) / 256)), kThreads, kDownStage + plan, stream>>>(a);
   } else {
     launch<1, 2, 4, 3, 3>(a, stream);
   }
