@@ -48,6 +48,10 @@ __device__ __forceinline__ v8i join(u32x4 a, u32x4 b) {
 // This wave's number, on the scalar unit.
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
 
+__device__ __forceinline__ float of_lane(float v, int l) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+}
+
 // ---- which rows each expert has ----
 
 // One expert's rows, at most `block` of them, packed: expert (10 bits), first row
@@ -148,11 +152,14 @@ __device__ __forceinline__ Plan make_plan(const ExpertArgs& a, uint32_t* lds, in
     p.weight[r] = w;
   }
   __syncthreads();
-  if (blockIdx.x == 0) {                             // (places without a row hold what LDS held: never used)
-    for (int i = tid; i < 2 * places; i += kThreads) a.image[1 + i] = p.job[i];
-    if (tid == 0) a.image[0] = (uint32_t)p.jobs;
-  }
   return p;
+}
+
+// (Places without a row hold what LDS held: never used.)
+__device__ __forceinline__ void save_plan(const ExpertArgs& a, const Plan& p) {
+  if (blockIdx.x != 0) return;
+  for (int i = threadIdx.x; i < 2 * a.T * a.topk; i += kThreads) a.image[1 + i] = p.job[i];
+  if (threadIdx.x == 0) a.image[0] = (uint32_t)p.jobs;
 }
 
 __device__ __forceinline__ Plan load_plan(const ExpertArgs& a, uint32_t* lds) {
@@ -198,11 +205,9 @@ __device__ __forceinline__ float lane_scale(const float* block, int chunks) {
   const int kb = wave_id() + (threadIdx.x % 64) * kWaves;
   return kb < chunks ? block[kb] : 0.0f;
 }
-__device__ __forceinline__ float of_lane(float v, int l) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
-}
-// Chunks of one wave, in whole groups of U (those past the end are zeros).
-__device__ __forceinline__ int steps_of(int chunks, int U) { return (chunks + kWaves * U - 1) / (kWaves * U) * U; }
+// Chunks of one wave, at least the U that it fetches ahead (those past the end are
+// zeros): what is fetched is never more than one item ahead.
+__device__ __forceinline__ int steps_of(int chunks, int U) { return max((chunks + kWaves - 1) / kWaves, U); }
 
 // ---- gate and up ----
 
@@ -215,6 +220,7 @@ __global__ __launch_bounds__(kThreads, OCC) void k_moe_up(ExpertArgs a) {
   extern __shared__ __align__(16) uint32_t lds[];
   __shared__ __align__(16) float red[kWaves * MAXF * NC * 256];
   const Plan plan = make_plan(a, lds, 16 * MAXF);
+  save_plan(a, plan);
   const int lane = threadIdx.x % 64, wave = wave_id(), fr = lane % 16, fg = lane / 16;
   const int chunks = a.H / 128, steps = steps_of(chunks, U);
   const int tiles = a.I / (16 * NG), items = plan.jobs * tiles;
@@ -272,40 +278,19 @@ __global__ __launch_bounds__(kThreads, OCC) void k_moe_up(ExpertArgs a) {
 #pragma unroll
   for (int i = 0; i < U; ++i) fetch(c[i]);
   const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const Job job = plan.at(item / tiles);
-    const int col0 = item % tiles * 16 * NG, frags = (job.n + 15) / 16;
-    const float scale_g = next_g, scale_u = next_u;
-    v4f acc[MAXF][NC];
+  v4f acc[MAXF][NC];
+  auto clear = [&]() {
 #pragma unroll
     for (int f = 0; f < MAXF; ++f)
 #pragma unroll
       for (int n = 0; n < NC; ++n) acc[f][n] = zero;
-    for (int s0 = 0; s0 < steps; s0 += U) {
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const float sg = of_lane(scale_g, s0 + i), su = of_lane(scale_u, s0 + i);
-#pragma unroll
-        for (int f = 0; f < MAXF; ++f) {
-          if (f && f >= frags) continue;
-          const v8i x = join(c[i].x0[f], c[i].x1[f]);
-#pragma unroll
-          for (int n = 0; n < NC; ++n) {
-            const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(c[i].w0[n], c[i].w1[n]), x, zero, 0, 0,
-                                                                          0, 0, 0, 0);
-            const float by = c[i].sx[f] * (n < NG ? sg : su);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[f][n][e] = __builtin_fmaf(p[e], by, acc[f][n][e]);
-          }
-        }
-        if (step == steps) {
-          ahead += gridDim.x;
-          step = 0;
-          aim();
-        }
-        fetch(c[i]);
-      }
-    }
+  };
+  clear();
+  int item = blockIdx.x, done = 0;
+  float scale_g = next_g, scale_u = next_u;
+  auto finish = [&]() {                              // item is whole: its activations
+    const Job job = plan.at(item / tiles);
+    const int col0 = item % tiles * 16 * NG;
     leave(acc, red);
     const int m = threadIdx.x / 16, col = threadIdx.x % 16;
 #pragma unroll
@@ -324,6 +309,39 @@ __global__ __launch_bounds__(kThreads, OCC) void k_moe_up(ExpertArgs a) {
       }
     }
     __syncthreads();
+  };
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const float sg = of_lane(scale_g, done), su = of_lane(scale_u, done);
+#pragma unroll
+      for (int f = 0; f < MAXF; ++f) {
+        const v8i x = join(c[i].x0[f], c[i].x1[f]);
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+          const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(c[i].w0[n], c[i].w1[n]), x, zero, 0, 0, 0,
+                                                                        0, 0, 0);
+          const float by = c[i].sx[f] * (n < NG ? sg : su);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[f][n][e] = __builtin_fmaf(p[e], by, acc[f][n][e]);
+        }
+      }
+      if (step == steps) {
+        ahead += gridDim.x;
+        step = 0;
+        aim();
+      }
+      fetch(c[i]);
+      if (++done == steps) {
+        finish();
+        item += gridDim.x;
+        if (item >= items) return;
+        done = 0;
+        scale_g = next_g;
+        scale_u = next_u;
+        clear();
+      }
+    }
   }
 }
 
@@ -404,47 +422,19 @@ __global__ __launch_bounds__(kThreads, OCC) void k_moe_down(ExpertArgs a) {
 #pragma unroll
   for (int i = 1; i < U; ++i) fetch(c[i]);
   const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const Job job = plan.at(item / tiles);
-    const int col0 = item % tiles * 16 * NC, frags = (job.n + 15) / 16;
-    const float scales = next_scale;
-    v4f acc[MAXF][NC];
+  v4f acc[MAXF][NC];
+  auto clear = [&]() {
 #pragma unroll
     for (int f = 0; f < MAXF; ++f)
 #pragma unroll
       for (int n = 0; n < NC; ++n) acc[f][n] = zero;
-    for (int s0 = 0; s0 < steps; s0 += U) {
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const float scale = of_lane(scales, s0 + i);
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-          const v8bf b[4] = {to_bf16(c[i].w0[n].x, c[i].w0[n].y), to_bf16(c[i].w0[n].z, c[i].w0[n].w),
-                             to_bf16(c[i].w1[n].x, c[i].w1[n].y), to_bf16(c[i].w1[n].z, c[i].w1[n].w)};
-#pragma unroll
-          for (int f = 0; f < MAXF; ++f) {
-            if (f && f >= frags) continue;
-            v4f p = zero;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, hi[f][j]), p, 0, 0, 0);
-              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, lo[f][j]), p, 0, 0, 0);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[f][n][e] = __builtin_fmaf(p[e], scale, acc[f][n][e]);
-          }
-        }
-        const bool last = s0 + i + 1 == steps;
-        if (last) aim_acts(item + gridDim.x);
-        fetch_acts(last ? 0 : s0 + i + 1);
-        if (step == steps) {
-          ahead += gridDim.x;
-          step = 0;
-          aim();
-        }
-        fetch(c[i]);
-      }
-    }
+  };
+  clear();
+  int item = blockIdx.x, done = 0;
+  float scales = next_scale;
+  auto finish = [&]() {
+    const Job job = plan.at(item / tiles);
+    const int col0 = item % tiles * 16 * NC;
     leave(acc, red);
     const int m = threadIdx.x / 16, col = threadIdx.x % 16;
 #pragma unroll
@@ -456,6 +446,45 @@ __global__ __launch_bounds__(kThreads, OCC) void k_moe_down(ExpertArgs a) {
       for (int n = 0; n < NC; ++n) to[n * 16] = total<MAXF, NC>(red, f, n, m, col);
     }
     __syncthreads();
+  };
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const float scale = of_lane(scales, done);
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        const v8bf b[4] = {to_bf16(c[i].w0[n].x, c[i].w0[n].y), to_bf16(c[i].w0[n].z, c[i].w0[n].w),
+                           to_bf16(c[i].w1[n].x, c[i].w1[n].y), to_bf16(c[i].w1[n].z, c[i].w1[n].w)};
+#pragma unroll
+        for (int f = 0; f < MAXF; ++f) {
+          v4f p = zero;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, hi[f][j]), p, 0, 0, 0);
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, lo[f][j]), p, 0, 0, 0);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[f][n][e] = __builtin_fmaf(p[e], scale, acc[f][n][e]);
+        }
+      }
+      const bool last = ++done == steps;
+      if (last) aim_acts(item + gridDim.x);
+      fetch_acts(last ? 0 : done);
+      if (step == steps) {
+        ahead += gridDim.x;
+        step = 0;
+        aim();
+      }
+      fetch(c[i]);
+      if (last) {
+        finish();
+        item += gridDim.x;
+        if (item >= items) return;
+        done = 0;
+        scales = next_scale;
+        clear();
+      }
+    }
   }
 }
 
@@ -597,6 +626,7 @@ constexpr int kUpStage = 2 * kPiece * (64 * 128 + 66 * 4);   // bytes, for 64 ro
 __global__ __launch_bounds__(kThreads, 2) void k_moe_up_wide(ExpertArgs a) {
   extern __shared__ __align__(16) uint32_t lds[];
   const Plan plan = make_plan(a, lds + kUpStage / 4, 64);
+  save_plan(a, plan);
   const int tiles = a.I / 64;
   if ((int)blockIdx.x >= plan.jobs * tiles) return;
   const Job job = plan.at(blockIdx.x / tiles);

@@ -43,23 +43,42 @@ __device__ __forceinline__ float wave_max(float v) {
   for (int d = 1; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
   return v;
 }
+// The largest of the wave's values, by DPP (a shuffle through LDS costs several
+// times as much, and topk of these follow one another).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t max_step(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false));
+}
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
-  return v;
+  v = max_step<0x111, 0xF>(v);                       // row_shr 1, 2, 4, 8: a row's last lane has its largest
+  v = max_step<0x112, 0xF>(v);
+  v = max_step<0x114, 0xF>(v);
+  v = max_step<0x118, 0xF>(v);
+  v = max_step<0x142, 0xA>(v);                       // row_bcast 15, 31: into the rows after
+  v = max_step<0x143, 0xC>(v);
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 // N: experts per lane.
 template <int N>
 __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
   const int lane = threadIdx.x % 64;
-  for (int64_t t = (int64_t)blockIdx.x * kWaves + threadIdx.x / 64; t < a.T; t += (int64_t)gridDim.x * kWaves) {
-    uint32_t v[N];
+  const int64_t step = (int64_t)gridDim.x * kWaves;
+  float next[N];
+  auto fetch = [&](int64_t t) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int e = 64 * n + lane;
-      v[n] = e < a.E ? rank_of(logit(a, t * a.E + e)) : 0u;
+      next[n] = e < a.E ? logit(a, t * a.E + e) : -__builtin_inff();
     }
+  };
+  int64_t t = (int64_t)blockIdx.x * kWaves + threadIdx.x / 64;
+  if (t < a.T) fetch(t);
+  for (; t < a.T; t += step) {
+    uint32_t v[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = rank_of(next[n]);
+    if (t + step < a.T) fetch(t + step);
     float all = 0.0f, top = 0.0f;
     // lane j keeps place j
     int id = -1;
@@ -68,7 +87,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
       uint32_t best = v[0];
 #pragma unroll
       for (int n = 1; n < N; ++n) best = max(best, v[n]);
-      best = __builtin_amdgcn_readfirstlane(wave_max(best));
+      best = wave_max(best);
       if (j == 0) {
         top = logit_of(best);
         if (!a.renorm && best) {
@@ -155,7 +174,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_back(RouteArgs a) {
   }
 }
 
-unsigned grid_of(int64_t T) { return (unsigned)std::min<int64_t>((T + kWaves - 1) / kWaves, 1 << 20); }
+// As many workgroups as run at once: starting one takes longer than a token.
+unsigned grid_of(int64_t T) { return (unsigned)std::min<int64_t>((T + kWaves - 1) / kWaves, 2048); }
 
 }  // namespace
 

@@ -18,9 +18,9 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ u32x4 piece(const void* row, int p) {
   return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row) + p);
 }
-__device__ __forceinline__ void put_piece(void* row, int p, u32x4 v) {
-  __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(row) + p);
-}
+// (Ordinary stores: nontemporal ones took 84 instead of 79 us in the backward
+// pass of 8192 x 7168, and the same in the forward pass; ordinary loads 91.)
+__device__ __forceinline__ void put_piece(void* row, int p, u32x4 v) { reinterpret_cast<u32x4*>(row)[p] = v; }
 __device__ __forceinline__ void unpack8(float (&f)[8], u32x4 v) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) f[2 * e] = bf16_lo(v[e]), f[2 * e + 1] = bf16_hi(v[e]);
@@ -187,22 +187,29 @@ __global__ __launch_bounds__(1024) void k_rms_norm_back(NormBackArgs a) {
   }
 }
 
-// dweight = the groups' partial rows added up; 16 lanes of four columns, 16
-// runs of groups.
+// dweight = the groups' partial rows added up: four lanes of four columns, 64 runs
+// of groups, joined in order.
 __global__ __launch_bounds__(256) void k_rms_norm_dweight(const float* part, int groups, int K, float* dweight,
                                                           bool accumulate) {
-  __shared__ float4 red[16][16];
-  const int c = threadIdx.x % 16, r = threadIdx.x / 16;
-  const int col = (blockIdx.x * 16 + c) * 4;         // (K is a multiple of 64)
+  __shared__ float4 red[64][4];
+  const int c = threadIdx.x % 4, r = threadIdx.x / 4;
+  const int col = (blockIdx.x * 4 + c) * 4;          // (K is a multiple of 16)
   float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int g = r; g < groups; g += 16) {
+#pragma unroll 8
+  for (int g = r; g < groups; g += 64) {
     const float4 p = *reinterpret_cast<const float4*>(part + (int64_t)g * K + col);
     t.x += p.x, t.y += p.y, t.z += p.z, t.w += p.w;
   }
-  red[r][c] = t;
-  __syncthreads();
+  for (int half = 32; half >= 1; half /= 2) {
+    red[r][c] = t;
+    __syncthreads();
+    if (r < half) {
+      const float4 o = red[r + half][c];
+      t.x += o.x, t.y += o.y, t.z += o.z, t.w += o.w;
+    }
+    __syncthreads();
+  }
   if (r) return;
-  for (int i = 1; i < 16; ++i) t.x += red[i][c].x, t.y += red[i][c].y, t.z += red[i][c].z, t.w += red[i][c].w;
   float4* out = reinterpret_cast<float4*>(dweight + col);
   if (accumulate) t.x += out->x, t.y += out->y, t.z += out->z, t.w += out->w;
   *out = t;
@@ -238,7 +245,7 @@ hipError_t launch_rms_norm_back(const NormBackArgs& a, hipStream_t stream) {
     k<<<a.groups, s.threads, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  k_rms_norm_dweight<<<a.K / 64, 256, 0, stream>>>(a.part, a.groups, a.K, a.dweight, a.accumulate);
+  k_rms_norm_dweight<<<a.K / 16, 256, 0, stream>>>(a.part, a.groups, a.K, a.dweight, a.accumulate);
   return hipGetLastError();
 }
 
