@@ -1,8 +1,13 @@
 // The router's choice of experts and its gradient (include/fp8bs_layer.h,
 // fp8bs_moe_route and fp8bs_moe_route_backward).
 //
-// A wave holds one token's logits, expert 64 n + lane at v[n] of a lane.
+// Bound by instructions: each choice is a maximum over a token's logits, and one
+// wave instruction takes four cycles.  So 16 lanes hold a token where they can
+// (up to 256 experts and 16 places): lane l has experts 16 n + l, four tokens share
+// each instruction, and a maximum over 16 lanes is four DPP steps.  Otherwise a
+// wave holds one token, expert 64 n + lane at v[n] of a lane.
 #include <algorithm>
+#include <type_traits>
 
 #include "layer.h"
 #include "quant_common.h"
@@ -15,6 +20,11 @@ constexpr int kWaves = 4;   // tokens per workgroup
 __device__ __forceinline__ float logit(const RouteArgs& a, int64_t at) {
   if (a.logits_f32) return static_cast<const float*>(a.logits)[at];
   return __builtin_bit_cast(float, (uint32_t) static_cast<const uint16_t*>(a.logits)[at] << 16);
+}
+
+__device__ __forceinline__ void put(const RouteArgs& a, int64_t at, float v) {
+  if (a.logits_f32) static_cast<float*>(a.dlogits)[at] = v;
+  else static_cast<__bf16*>(a.dlogits)[at] = (__bf16)v;
 }
 
 // Logits as whole numbers of the same order; 0 for an expert that is left out
@@ -168,27 +178,215 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_back(RouteArgs a) {
     for (int n = 0; n < N; ++n) {
       const int e = 64 * n + lane;
       if (e >= a.E) continue;
-      if (a.logits_f32) static_cast<float*>(a.dlogits)[t * a.E + e] = add[n];
-      else static_cast<__bf16*>(a.dlogits)[t * a.E + e] = (__bf16)add[n];
+      put(a, t * a.E + e, add[n]);
     }
   }
 }
 
-// As many workgroups as run at once: starting one takes longer than a token.
-unsigned grid_of(int64_t T) { return (unsigned)std::min<int64_t>((T + kWaves - 1) / kWaves, 2048); }
+// ---- four tokens per wave ----
+
+// A value of every lane of the row of 16, joined by f, on all of its lanes.
+template <class T, class F>
+__device__ __forceinline__ T row_join(T v, F f) {
+  const auto other = [](T x, auto ctrl) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  v = f(v, other(v, std::integral_constant<int, 0xB1>()));    // quad_perm 1,0,3,2
+  v = f(v, other(v, std::integral_constant<int, 0x4E>()));    // quad_perm 2,3,0,1
+  v = f(v, other(v, std::integral_constant<int, 0x141>()));   // row_half_mirror
+  return f(v, other(v, std::integral_constant<int, 0x140>()));  // row_mirror
+}
+__device__ __forceinline__ float row_sum(float v) {
+  return row_join(v, [](float x, float y) { return x + y; });
+}
+__device__ __forceinline__ float row_max(float v) {
+  return row_join(v, [](float x, float y) { return fmaxf(x, y); });
+}
+
+constexpr int kTokens = 4 * kWaves;   // per workgroup
+
+// A logit's rank and its expert as one whole number, exact in a double: keys of
+// a token all differ, the lower expert first among equal logits, and v_max_f64
+// takes the larger of two in one instruction.  Keys below kFirst are left out.
+constexpr double kFirst = 1024.0;
+__device__ __forceinline__ double key_of(uint32_t rank, int e) {
+  return __builtin_fma((double)rank, kFirst, rank ? (double)(1023 - e) : 0.0);
+}
+__device__ __forceinline__ uint32_t rank_in(double key) { return (uint32_t)(key * 0x1p-10); }
+__device__ __forceinline__ int expert_in(double key) {
+  return 1023 - (int)(key - (double)rank_in(key) * kFirst);
+}
+
+__device__ __forceinline__ double row_max(double v) {
+  const auto step = [](double x, auto ctrl) {
+    constexpr int kCtrl = decltype(ctrl)::value;
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, kCtrl, 0xF, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), kCtrl, 0xF, 0xF, true);
+    return __builtin_fmax(x, __builtin_bit_cast(double, (uint64_t)hi << 32 | lo));
+  };
+  v = step(v, std::integral_constant<int, 0xB1>());
+  v = step(v, std::integral_constant<int, 0x4E>());
+  v = step(v, std::integral_constant<int, 0x141>());
+  return step(v, std::integral_constant<int, 0x140>());
+}
+
+// Falling order, by odd-even merging (N a power of two; all indexes are known when
+// compiled).
+template <int N>
+__device__ __forceinline__ void sort_falling(double (&k)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int d = p; d >= 1; d /= 2)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int j = i + d;
+        if (j >= N || i < d % p || (i - d % p) / d % 2 || i / (2 * p) != j / (2 * p)) continue;
+        const double hi = __builtin_fmax(k[i], k[j]), lo = __builtin_fmin(k[i], k[j]);
+        k[i] = hi;
+        k[j] = lo;
+      }
+}
+
+// Each lane sorts its own N logits and keeps them in LDS; a choice is then the
+// largest of the 16 lists' heads, and one list moves on.
+template <int N>
+__global__ __launch_bounds__(64 * kWaves) void k_route_rows(RouteArgs a) {
+  __shared__ double lists[N + 1][64 * kWaves];
+  const int l = threadIdx.x % 16, tid = threadIdx.x;
+  const int64_t step = (int64_t)gridDim.x * kTokens;
+  float x[N];
+  auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) x[n] = t < a.T && 16 * n + l < a.E ? logit(a, t * a.E + 16 * n + l) : -__builtin_inff();
+  };
+  lists[N][tid] = 0.0;                               // (each lane reads and writes its own column only)
+  // (the four rows of a wave go on together, so that their DPP steps see live lanes)
+  int64_t t = (int64_t)blockIdx.x * kTokens + tid / 16;
+  fetch(t);
+  for (int64_t first = (int64_t)blockIdx.x * kTokens; first < a.T; first += step, t += step) {
+    double k[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) k[n] = key_of(rank_of(x[n]), 16 * n + l);
+    float sum = 0.0f, top = 0.0f;
+    if (!a.renorm) {
+      double best = k[0];
+#pragma unroll
+      for (int n = 1; n < N; ++n) best = __builtin_fmax(best, k[n]);
+      best = row_max(best);
+      if (best >= kFirst) top = logit_of(rank_in(best));
+#pragma unroll
+      for (int n = 0; n < N; ++n) sum += weight_of(x[n], top);
+    }
+    fetch(t + step);
+    sort_falling(k);
+#pragma unroll
+    for (int n = 0; n < N; ++n) lists[n][tid] = k[n];
+    // lane j keeps place j
+    double head = k[0], mine = 0.0;
+    int at = 0;
+    for (int j = 0; j < a.topk; ++j) {
+      const double best = row_max(head);
+      if (l == j) mine = best;
+      if (j == 0 && a.renorm && best >= kFirst) top = logit_of(rank_in(best));
+      if (head == best && at < N) head = lists[++at][tid];
+    }
+    const bool there = mine >= kFirst;
+    const float w = there ? weight_of(logit_of(rank_in(mine)), top) : 0.0f;
+    sum = row_sum(a.renorm ? w : sum);
+    if (l < a.topk && t < a.T) {
+      a.ids[t * a.topk + l] = there ? expert_in(mine) : -1;
+      a.weights[t * a.topk + l] = there ? w / sum : 0.0f;
+    }
+  }
+}
+
+template <int N>
+__global__ __launch_bounds__(64 * kWaves) void k_route_back_rows(RouteArgs a) {
+  const int l = threadIdx.x % 16;
+  const int64_t step = (int64_t)gridDim.x * kTokens;
+  int64_t t = (int64_t)blockIdx.x * kTokens + threadIdx.x / 16;
+  for (int64_t first = (int64_t)blockIdx.x * kTokens; first < a.T; first += step, t += step) {
+    const bool live = t < a.T;
+    // place l: its expert, logit and gradient
+    const int id = live && l < a.topk ? a.ids[t * a.topk + l] : -1;
+    const bool there = (uint32_t)id < (uint32_t)a.E;
+    float x = there ? logit(a, t * a.E + id) : -__builtin_inff();
+    if (!(x > -__builtin_inff())) x = -__builtin_inff();
+    const float g = there ? a.weights[t * a.topk + l] : 0.0f;
+    float p[N], place;                               // p_i of each expert; of this place's
+    if (a.renorm) {
+      const float w = weight_of(x, row_max(x)), sum = row_sum(w);
+      place = sum > 0.0f ? w / sum : 0.0f;
+#pragma unroll
+      for (int n = 0; n < N; ++n) p[n] = 0.0f;
+    } else {
+      float top = -__builtin_inff(), sum = 0.0f;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        p[n] = live && 16 * n + l < a.E ? logit(a, t * a.E + 16 * n + l) : -__builtin_inff();
+        if (!(p[n] > -__builtin_inff())) p[n] = -__builtin_inff();
+        top = fmaxf(top, p[n]);
+      }
+      top = row_max(top);
+#pragma unroll
+      for (int n = 0; n < N; ++n) p[n] = weight_of(p[n], top), sum += p[n];
+      sum = row_sum(sum);
+#pragma unroll
+      for (int n = 0; n < N; ++n) p[n] = sum > 0.0f ? p[n] / sum : 0.0f;
+      place = sum > 0.0f ? weight_of(x, top) / sum : 0.0f;
+    }
+    const float mean = row_sum(place > 0.0f ? place * g : 0.0f);
+    const int key = place > 0.0f ? id : -1;          // (places that count)
+    const float d = place > 0.0f ? place * (a.renorm ? g - mean : g) : 0.0f;
+    // an expert that stands in several places gets the sum of theirs, the same on
+    // each of their lanes
+    float total = 0.0f;
+    for (int j = 0; j < a.topk; ++j) {
+      const int from = (threadIdx.x & ~15) + j;      // (lane of the wave: shuffles take it modulo 64)
+      const int other = __shfl(key, from);
+      const float add = __shfl(d, from);
+      total += other == key ? add : 0.0f;
+    }
+    if (!a.renorm) total -= place * mean;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (live && 16 * n + l < a.E) put(a, t * a.E + 16 * n + l, -(p[n] * mean));
+    // the places' own experts, over what other lanes of this wave have just
+    // written there (a wave's stores to one address stay in order)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (key >= 0) put(a, t * a.E + key, total);
+  }
+}
+
+// As many workgroups as run at once.
+unsigned grid_of(int64_t T, int tokens) { return (unsigned)std::min<int64_t>((T + tokens - 1) / tokens, 2048); }
+
+bool by_rows(const RouteArgs& a) { return a.E <= 256 && a.topk <= 16; }
 
 }  // namespace
 
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream) {
-  const auto k = a.E <= 64 ? k_route<1> : a.E <= 128 ? k_route<2> : a.E <= 256 ? k_route<4> : k_route<16>;
-  k<<<grid_of(a.T), 64 * kWaves, 0, stream>>>(a);
+  if (by_rows(a)) {
+    const auto k = a.E <= 64 ? k_route_rows<4> : a.E <= 128 ? k_route_rows<8> : k_route_rows<16>;
+    k<<<grid_of(a.T, kTokens), 64 * kWaves, 0, stream>>>(a);
+  } else {
+    const auto k = a.E <= 256 ? k_route<4> : k_route<16>;
+    k<<<grid_of(a.T, kWaves), 64 * kWaves, 0, stream>>>(a);
+  }
   return hipGetLastError();
 }
 
 hipError_t launch_moe_route_back(const RouteArgs& a, hipStream_t stream) {
-  const auto k =
-      a.E <= 64 ? k_route_back<1> : a.E <= 128 ? k_route_back<2> : a.E <= 256 ? k_route_back<4> : k_route_back<16>;
-  k<<<grid_of(a.T), 64 * kWaves, 0, stream>>>(a);
+  if (by_rows(a)) {
+    const auto k = a.E <= 64 ? k_route_back_rows<4> : a.E <= 128 ? k_route_back_rows<8> : k_route_back_rows<16>;
+    k<<<grid_of(a.T, kTokens), 64 * kWaves, 0, stream>>>(a);
+  } else {
+    const auto k = a.E <= 256 ? k_route_back<4> : k_route_back<16>;
+    k<<<grid_of(a.T, kWaves), 64 * kWaves, 0, stream>>>(a);
+  }
   return hipGetLastError();
 }
 

@@ -70,7 +70,8 @@ def check(x, dev, topk, renorm, seed=0):
 
 
 @pytest.mark.parametrize("t,e,topk", [(1, 1, 1), (1, 8, 2), (3, 64, 6), (5, 65, 1), (37, 128, 8), (9, 256, 8), (4, 257, 16),
-                                      (2, 1024, 64), (7, 60, 60), (6, 64, 64), (130, 32, 4), (3, 200, 9)])
+                                      (2, 1024, 64), (7, 60, 60), (6, 64, 64), (130, 32, 4), (3, 200, 9),
+                                      (18, 256, 16), (5, 256, 17), (66, 16, 16), (3, 5, 4), (33, 100, 1)])
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_route(t, e, topk, kind, renorm):
@@ -126,12 +127,16 @@ def test_route_infinite_and_far_logits(renorm):
     assert torch.isfinite(dl).all()
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("renorm", [False, True])
-def test_route_backward_of_other_ids(renorm):
+def test_route_backward_of_other_ids(renorm, wide):
     # an id twice, ids outside, places without one
     rng = np.random.default_rng(4)
     x = rng.standard_normal((6, 10)).astype(np.float32)
     ids = np.array([[1, 1, 3], [-1, -1, -1], [9, 10, 2], [4, -5, 4], [1 << 30, 0, -1], [7, 7, 7]], np.int32)
+    if wide:                                            # (more experts than 16 lanes hold)
+        x = np.concatenate([x, np.full((6, 290), -np.inf, np.float32)], 1)
+        ids[2, 1] = 300
     dw = rng.standard_normal((6, 3)).astype(np.float32)
     dl = fb.moe_route_backward(f32_dev(x), i32_dev(ids), f32_dev(dw), renormalize=renorm).cpu().numpy()
     assert np.allclose(dl, layer.route_backward(x, ids, dw, renorm), rtol=0, atol=400 * U)
