@@ -31,5 +31,6 @@ __all__ = list(_PUBLIC)
 def __getattr__(name):
     if name in _PUBLIC:
         from . import fp8bs
-        return getattr(fp8bs, name)
+        value = globals()[name] = getattr(fp8bs, name)   # (later lookups find it at once)
+        return value
     raise AttributeError(name)

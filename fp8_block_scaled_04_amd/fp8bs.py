@@ -11,6 +11,7 @@ inputs and viewed as codes); scales are float32; BF16 data is torch.bfloat16.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -739,9 +740,9 @@ def rms_norm_quantize(x, weight, eps: float = 1e-6, residual=None, pow2: bool = 
             _shaped(h, "h", torch.bfloat16, x.shape, dev)
     elif h is not None:
         raise ValueError("h is the sum with a residual: give one")
-    q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
-    s = torch.empty((K // 128, M), dtype=torch.float32, device=x.device)
-    rstd = torch.empty((M,), dtype=torch.float32, device=x.device)
+    q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    s = x.new_empty((K // 128, M), dtype=torch.float32)
+    rstd = x.new_empty((M,), dtype=torch.float32)
     y = torch.empty_like(x) if return_y else None
     _launch(dev, _norm, "rms_norm_quantize", x.data_ptr(), residual.data_ptr() if residual is not None else None,
             weight.data_ptr(), code, eps, M, K, h.data_ptr() if h is not None else None,
@@ -750,6 +751,7 @@ def rms_norm_quantize(x, weight, eps: float = 1e-6, residual=None, pow2: bool = 
     return (q, s, h, rstd, y) if return_y else (q, s, h, rstd)
 
 
+@functools.lru_cache(maxsize=4096)
 def rms_norm_backward_workspace_bytes(M: int, K: int) -> int:
     """Workspace bytes of rms_norm_backward for [M][K]."""
     out = ctypes.c_int64(0)
@@ -780,7 +782,7 @@ def rms_norm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, accum
     if dweight is None:
         if accumulate:
             raise ValueError("accumulate needs an existing dweight")
-        dweight = torch.empty((K,), dtype=torch.float32, device=h.device)
+        dweight = rstd.new_empty((K,))
     else:
         _shaped(dweight, "dweight", torch.float32, (K,), dev)
     workspace, ws, ws_bytes = _workspace(workspace, rms_norm_backward_workspace_bytes(M, K), dev)
@@ -803,8 +805,8 @@ def moe_route(logits, topk: int, renormalize: bool = True):
     _fits(E, topk)
     if topk < 1 or topk > E:
         raise ValueError(f"topk must be 1 .. {E}, got {topk}")
-    ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
+    ids = logits.new_empty((T, topk), dtype=torch.int32)
+    weights = logits.new_empty((T, topk), dtype=torch.float32)
     _launch(dev, _route, "moe_route", logits.data_ptr(), code, T, E, topk, ids.data_ptr(), weights.data_ptr(),
             ROUTE_RENORM if renormalize else 0)
     return ids, weights
@@ -828,6 +830,7 @@ def moe_route_backward(logits, ids, dweights, renormalize: bool = True):
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def moe_experts_workspace_bytes(T: int, H: int, I: int, E: int, topk: int) -> int:
     """Workspace bytes of moe_experts for T tokens of width H, E experts of
     inner width I."""
@@ -864,7 +867,7 @@ def moe_experts(x, sx, ids, weights, w13, s13, w2, s2, out_dtype=torch.bfloat16,
     _shaped(s2, "s2", torch.float32, (E, H // 128, I // 128), dev)
     code = _out_code(out_dtype)
     if out is None:
-        out = torch.empty((T, H), dtype=out_dtype, device=x.device)
+        out = sx.new_empty((T, H), dtype=out_dtype)
     else:
         _shaped(out, "out", out_dtype, (T, H), dev)
     workspace, ws, ws_bytes = _workspace(workspace, moe_experts_workspace_bytes(T, H, I, E, topk), dev)
