@@ -501,22 +501,37 @@ constexpr int kPiece = 4;   // chunks of H per piece in k_moe_up_wide
 __device__ __forceinline__ int swizzle8(int row, int s) { return s ^ ((row >> 1) & 7); }
 __device__ __forceinline__ int swizzle16(int row, int s) { return s ^ (row & 15); }
 
-// One workgroup per job and 64 columns of I, 16 per wave.
-template <int MF, int U>
+// Work of one workgroup: a job and a unit of columns, or half of one.  Whole units
+// read a job's rows half as often, halves leave less undone at the end: so as many
+// whole units as fill the chip in rounds of two workgroups per CU come first, and
+// the rest in halves.
+struct Share {
+  int unit, half;   // half: 0, 1, or -1 for both
+};
+__device__ __forceinline__ Share share_of(int block, int units) {
+  const int whole = units & ~511;
+  if (block < whole) return {block, -1};
+  return {whole + (block - whole) / 2, (block - whole) % 2};
+}
+
+// One workgroup per job and 64 NG columns of I, 16 NG per wave.
+template <int MF, int NG, int U>
 __device__ __forceinline__ void up_wide(const ExpertArgs& a, const Plan& plan, const Job& job, int col0, uint8_t* stage) {
   // stage: [2][kPiece][16 MF rows][128], then scales [2][kPiece][16 MF + 2]
-  constexpr int kRows = 16 * MF, kBuf = kPiece * kRows * 128, kPer = kRows * 8 * kPiece / kThreads;
+  constexpr int kRows = 16 * MF, kBuf = kPiece * kRows * 128, kPer = kRows * 8 * kPiece / kThreads, NC = 2 * NG;
   constexpr int kScales = kPiece * (kRows + 2);
-  static_assert(U == kPiece, "a chunk's place in the ring is its place in the piece");
+  static_assert(kPiece % U == 0, "a chunk's place in the ring goes by its place in the piece");
   float* scales = reinterpret_cast<float*>(stage + 2 * kBuf);
   const int tid = threadIdx.x, lane = tid % 64, wave = wave_id(), fr = lane % 16, fg = lane / 16;
   const int chunks = a.H / 128, pieces = (chunks + kPiece - 1) / kPiece;
   const int64_t panel = 2 * (int64_t)a.I * a.H;
   const auto wb = buffer(a.w13 + job.expert * panel, panel);
   const auto xb = buffer(a.x, (int64_t)a.T * a.H);
-  const int col = col0 + wave * 16;
-  const uint32_t gate = (uint32_t)((col + fr) * (int64_t)a.H + fg * 16);
-  const uint32_t up = gate + (uint32_t)(a.I * (int64_t)a.H);
+  const int col = col0 + wave * 16 * NG;
+  uint32_t wrow[NC];
+#pragma unroll
+  for (int n = 0; n < NC; ++n)
+    wrow[n] = (uint32_t)(((n / NG) * a.I + col + (n % NG) * 16 + fr) * (int64_t)a.H + fg * 16);
 
   // this thread's segments of a piece: row, chunk and place in the chunk
   u32x4 x[kPer];
@@ -558,18 +573,21 @@ __device__ __forceinline__ void up_wide(const ExpertArgs& a, const Plan& plan, c
     for (int i = 0; i < kPerScale; ++i)
       if (i * kThreads + tid < kScales) scales[(piece & 1) * kScales + i * kThreads + tid] = sc[i];
   };
-  u32x4 w[U][4];
+  u32x4 w[U][NC][2];
   auto fetch = [&](int i, int kb) {
     const uint32_t at = kb < chunks ? (uint32_t)kb * 128 : kNoChunk;
-    w[i][0] = load16(wb, gate + at);
-    w[i][1] = load16(wb, gate + at + 64);
-    w[i][2] = load16(wb, up + at);
-    w[i][3] = load16(wb, up + at + 64);
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      w[i][n][0] = load16(wb, wrow[n] + at);
+      w[i][n][1] = load16(wb, wrow[n] + at + 64);
+    }
   };
   const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
-  v4f ag[MF], au[MF];
+  v4f acc[MF][NC];
 #pragma unroll
-  for (int f = 0; f < MF; ++f) ag[f] = au[f] = zero;
+  for (int f = 0; f < MF; ++f)
+#pragma unroll
+    for (int n = 0; n < NC; ++n) acc[f][n] = zero;
   fetch_piece(0);
 #pragma unroll
   for (int i = 0; i < U; ++i) fetch(i, i);
@@ -581,7 +599,6 @@ __device__ __forceinline__ void up_wide(const ExpertArgs& a, const Plan& plan, c
     const float* ss = scales + (piece & 1) * kScales;
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) {
-      const v8i g = join(w[i][0], w[i][1]), u = join(w[i][2], w[i][3]);
       const float sg = ss[i * (kRows + 2) + kRows], su = ss[i * (kRows + 2) + kRows + 1];
 #pragma unroll
       for (int f = 0; f < MF; ++f) {
@@ -590,16 +607,16 @@ __device__ __forceinline__ void up_wide(const ExpertArgs& a, const Plan& plan, c
         const v8i xf = join(*reinterpret_cast<const u32x4*>(row + swizzle8(r, fg) * 16),
                             *reinterpret_cast<const u32x4*>(row + swizzle8(r, fg + 4) * 16));
         const float sx = ss[i * (kRows + 2) + r];
-        const v4f pg = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(g, xf, zero, 0, 0, 0, 0, 0, 0);
-        const v4f pu = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(u, xf, zero, 0, 0, 0, 0, 0, 0);
-        const float wg = sx * sg, wu = sx * su;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          ag[f][e] = __builtin_fmaf(pg[e], wg, ag[f][e]);
-          au[f][e] = __builtin_fmaf(pu[e], wu, au[f][e]);
+        for (int n = 0; n < NC; ++n) {
+          const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(w[i % U][n][0], w[i % U][n][1]), xf, zero, 0,
+                                                                        0, 0, 0, 0, 0);
+          const float by = sx * (n < NG ? sg : su);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[f][n][e] = __builtin_fmaf(p[e], by, acc[f][n][e]);
         }
       }
-      fetch(i, (piece + 1) * kPiece + i);
+      fetch(i % U, piece * kPiece + i + U);
     }
   }
   // a lane has four columns of a row
@@ -608,33 +625,48 @@ __device__ __forceinline__ void up_wide(const ExpertArgs& a, const Plan& plan, c
     const int r = f * 16 + fr;
     if (r >= job.n) continue;
     const float share = plan.weight[job.start + r];
-    float hi[4], lo[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float g = ag[f][e], v = share * (g / (1.0f + expf(-g))) * au[f][e];
-      hi[e] = v;
-      lo[e] = v - (float)(__bf16)v;
+    for (int n = 0; n < NG; ++n) {
+      float hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float g = acc[f][n][e], v = share * (g / (1.0f + expf(-g))) * acc[f][NG + n][e];
+        hi[e] = v;
+        lo[e] = v - (float)(__bf16)v;
+      }
+      const int64_t at = (int64_t)(job.start + r) * a.I + place_of(col + n * 16 + fg * 4);
+      *reinterpret_cast<uint2*>(a.hi + at) = make_uint2(pack2_bf16(hi[0], hi[1]), pack2_bf16(hi[2], hi[3]));
+      *reinterpret_cast<uint2*>(a.lo + at) = make_uint2(pack2_bf16(lo[0], lo[1]), pack2_bf16(lo[2], lo[3]));
     }
-    const int64_t at = (int64_t)(job.start + r) * a.I + place_of(col + fg * 4);
-    *reinterpret_cast<uint2*>(a.hi + at) = make_uint2(pack2_bf16(hi[0], hi[1]), pack2_bf16(hi[2], hi[3]));
-    *reinterpret_cast<uint2*>(a.lo + at) = make_uint2(pack2_bf16(lo[0], lo[1]), pack2_bf16(lo[2], lo[3]));
   }
 }
 
 constexpr int kUpStage = 2 * kPiece * (64 * 128 + 66 * 4);   // bytes, for 64 rows
 
+// A unit is 128 columns of I; with more than 32 rows its halves go one after the
+// other, for their accumulators.
 __global__ __launch_bounds__(kThreads, 2) void k_moe_up_wide(ExpertArgs a) {
   extern __shared__ __align__(16) uint32_t lds[];
   const Plan plan = make_plan(a, lds + kUpStage / 4, 64);
   save_plan(a, plan);
-  const int tiles = a.I / 64;
-  if ((int)blockIdx.x >= plan.jobs * tiles) return;
-  const Job job = plan.at(blockIdx.x / tiles);
-  const int col0 = blockIdx.x % tiles * 64;
+  const int tiles = a.I / 128, units = plan.jobs * tiles;
+  const Share share = share_of(blockIdx.x, units);
+  if (share.unit >= units) return;
+  const Job job = plan.at(share.unit / tiles);
+  const int col0 = share.unit % tiles * 128;
   uint8_t* stage = reinterpret_cast<uint8_t*>(lds);
-  if (job.n <= 16) up_wide<1, kPiece>(a, plan, job, col0, stage);
-  else if (job.n <= 32) up_wide<2, kPiece>(a, plan, job, col0, stage);
-  else up_wide<4, kPiece>(a, plan, job, col0, stage);
+  if (share.half < 0 && job.n <= 16) {
+    up_wide<1, 2, 2>(a, plan, job, col0, stage);
+  } else if (share.half < 0 && job.n <= 32) {
+    up_wide<2, 2, 2>(a, plan, job, col0, stage);
+  } else {
+    for (int half = max(share.half, 0); half <= (share.half < 0 ? 1 : share.half); ++half) {
+      __syncthreads();
+      if (job.n <= 16) up_wide<1, 1, 4>(a, plan, job, col0 + half * 64, stage);
+      else if (job.n <= 32) up_wide<2, 1, 4>(a, plan, job, col0 + half * 64, stage);
+      else up_wide<4, 1, 4>(a, plan, job, col0 + half * 64, stage);
+    }
+  }
 }
 
 // One workgroup per job and 64 NC columns of H, 16 NC per wave; a piece is one
@@ -747,23 +779,29 @@ __device__ __forceinline__ void down_wide(const ExpertArgs& a, const Plan& plan,
 
 constexpr int kDownStage = 2 * 2 * 64 * 256;   // bytes, for 64 rows
 
-// 256 columns (more rows: 128, twice, for their accumulators).
+// A unit is 256 columns of H (the last one may have 128).
 __global__ __launch_bounds__(kThreads, 2) void k_moe_down_wide(ExpertArgs a) {
   extern __shared__ __align__(16) uint32_t lds[];
   const Plan plan = load_plan(a, lds + kDownStage / 4);
-  const int tiles = (a.H + 255) / 256;
-  if ((int)blockIdx.x >= plan.jobs * tiles) return;
-  const Job job = plan.at(blockIdx.x / tiles);
-  const int col0 = blockIdx.x % tiles * 256;
+  const int tiles = (a.H + 255) / 256, units = plan.jobs * tiles;
+  const Share share = share_of(blockIdx.x, units);
+  if (share.unit >= units) return;
+  const Job job = plan.at(share.unit / tiles);
+  const int col0 = share.unit % tiles * 256;
   uint8_t* stage = reinterpret_cast<uint8_t*>(lds);
-  if (job.n <= 16) {
+  if (share.half < 0 && job.n <= 16) {
     down_wide<1, 4, 2>(a, plan, job, col0, stage);
-  } else if (job.n <= 32) {
+  } else if (share.half < 0 && job.n <= 32) {
     down_wide<2, 4, 2>(a, plan, job, col0, stage);
   } else {
-    down_wide<4, 2, 4>(a, plan, job, col0, stage);
-    __syncthreads();
-    down_wide<4, 2, 4>(a, plan, job, col0 + 128, stage);
+    for (int half = max(share.half, 0); half <= (share.half < 0 ? 1 : share.half); ++half) {
+      const int col = col0 + half * 128;
+      if (col >= a.H) break;
+      __syncthreads();
+      if (job.n <= 16) down_wide<1, 2, 4>(a, plan, job, col, stage);
+      else if (job.n <= 32) down_wide<2, 2, 4>(a, plan, job, col, stage);
+      else down_wide<4, 2, 4>(a, plan, job, col, stage);
+    }
   }
 }
 
@@ -849,7 +887,7 @@ hipError_t launch_moe_experts(const ExpertArgs& a, hipStream_t stream) {
     const int64_t jobs = std::min(a.E, a.T * a.topk) + a.T * a.topk / 64;
     const size_t plan = plan_bytes(a);
     k_moe_up_wide<<<(unsigned)(jobs * (a.I / 64)), kThreads, kUpStage + plan, stream>>>(a);
-    k_moe_down_wide<<<(unsigned)(jobs * ((a.H + 255) / 256)), kThreads, kDownStage + plan, stream>>>(a);
+    k_moe_down_wide<<<(unsigned)(jobs * ((a.H + 255) / 256) * 2), kThreads, kDownStage + plan, stream>>>(a);
   } else {
     launch<1, 2, 4, 3, 3>(a, stream);
   }
