@@ -82,8 +82,10 @@ int plan_bytes(const ExpertArgs& a) { return (a.T * a.topk * 4 + a.E * (mask_wor
 int image_words(const ExpertArgs& a) { return 1 + 2 * a.T * a.topk; }
 
 // `block`: rows that one pass over an expert's weights serves.
+template <int WAVES>
 __device__ __forceinline__ Plan make_plan(const ExpertArgs& a, uint32_t* lds, int block) {
-  __shared__ int waves[kWaves];
+  constexpr int kThreads = 64 * WAVES;
+  __shared__ int waves[WAVES];
   const int tid = threadIdx.x, places = a.T * a.topk, words = mask_words(a.T);
   Plan p;
   p.job = lds;
@@ -124,7 +126,7 @@ __device__ __forceinline__ Plan make_plan(const ExpertArgs& a, uint32_t* lds, in
   __syncthreads();
   before -= mine;
   int all = 0;
-  for (int w = 0; w < kWaves; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     if (w < tid / 64) before += waves[w];
     all += waves[w];
   }
@@ -158,14 +160,14 @@ __device__ __forceinline__ Plan make_plan(const ExpertArgs& a, uint32_t* lds, in
 // (Places without a row hold what LDS held: never used.)
 __device__ __forceinline__ void save_plan(const ExpertArgs& a, const Plan& p) {
   if (blockIdx.x != 0) return;
-  for (int i = threadIdx.x; i < 2 * a.T * a.topk; i += kThreads) a.image[1 + i] = p.job[i];
+  for (int i = threadIdx.x; i < 2 * a.T * a.topk; i += blockDim.x) a.image[1 + i] = p.job[i];
   if (threadIdx.x == 0) a.image[0] = (uint32_t)p.jobs;
 }
 
 __device__ __forceinline__ Plan load_plan(const ExpertArgs& a, uint32_t* lds) {
   const int places = a.T * a.topk;
   Plan p{lds, lds + places, nullptr, __builtin_amdgcn_readfirstlane((int)a.image[0])};
-  for (int i = threadIdx.x; i < 2 * places; i += kThreads) lds[i] = a.image[1 + i];
+  for (int i = threadIdx.x; i < 2 * places; i += blockDim.x) lds[i] = a.image[1 + i];
   __syncthreads();
   return p;
 }
@@ -179,85 +181,88 @@ __device__ __forceinline__ int place_of(int c) {
   return (c & ~63) + ((c >> 3) & 1) * 32 + ((c >> 4) & 3) * 8 + (c & 7);
 }
 
-// Adds up the waves' accumulators of MF x NC fragments and hands each sum to
-// f(row, column, gate or only value, up), columns 16 per fragment.  `red` holds
-// kWaves * MF * NC * 256 floats.
-template <int MF, int NC>
-__device__ __forceinline__ void leave(const v4f (&acc)[MF][NC], float* red) {
-  v4f* mine = reinterpret_cast<v4f*>(red) + wave_id() * MF * NC * 64 + threadIdx.x % 64;
+// The waves' accumulators of NC fragments, in LDS (WAVES * NC * 256 floats) for
+// the sums over them.
+template <int NC>
+__device__ __forceinline__ void leave(const v4f (&acc)[NC], float* red) {
+  v4f* mine = reinterpret_cast<v4f*>(red) + wave_id() * NC * 64 + threadIdx.x % 64;
 #pragma unroll
-  for (int f = 0; f < MF; ++f)
-#pragma unroll
-    for (int n = 0; n < NC; ++n) mine[(f * NC + n) * 64] = acc[f][n];
+  for (int n = 0; n < NC; ++n) mine[n * 64] = acc[n];
   __syncthreads();
 }
-// Row m, column c of fragment (f, n): lane (c / 4) 16 + m has c % 4.
-template <int MF, int NC>
-__device__ __forceinline__ float total(const float* red, int f, int n, int m, int c) {
+// Row m of tokens, row c of the weights of fragment n: lane (c / 4) 16 + m has c % 4.
+template <int WAVES, int NC>
+__device__ __forceinline__ float total(const float* red, int n, int m, int c) {
   float t = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) t += red[((w * MF + f) * NC + n) * 256 + ((c / 4) * 16 + m) * 4 + c % 4];
+  for (int w = 0; w < WAVES; ++w) t += red[(w * NC + n) * 256 + ((c / 4) * 16 + m) * 4 + c % 4];
   return t;
 }
 
-// The scales of one weight row block, chunk wave + kWaves l in lane l.
+// The scales of one weight row block, chunk wave + WAVES l in lane l.
+template <int WAVES>
 __device__ __forceinline__ float lane_scale(const float* block, int chunks) {
-  const int kb = wave_id() + (threadIdx.x % 64) * kWaves;
+  const int kb = wave_id() + (threadIdx.x % 64) * WAVES;
   return kb < chunks ? block[kb] : 0.0f;
 }
 // Chunks of one wave, at least the U that it fetches ahead (those past the end are
 // zeros): what is fetched is never more than one item ahead.
-__device__ __forceinline__ int steps_of(int chunks, int U) { return max((chunks + kWaves - 1) / kWaves, U); }
+template <int WAVES>
+__device__ __forceinline__ int steps_of(int chunks, int U) {
+  return max((chunks + WAVES - 1) / WAVES, U);
+}
 
 // ---- gate and up ----
 
-// Items: one job and 16 NG columns of I (so 32 NG rows of w13).  A workgroup
-// walks its items; the four waves take the 128-wide chunks of H in turn and keep
-// U of them in flight, the first ones of the next item too.
-template <int MAXF, int NG, int U, int OCC>
-__global__ __launch_bounds__(kThreads, OCC) void k_moe_up(ExpertArgs a) {
-  constexpr int NC = 2 * NG;
+// Items: one job (at most 16 rows) and COLS columns of I, so 2 COLS rows of w13 in
+// fragments of 16: COLS / 16 of gate, then as many of up; with COLS = 8 one
+// fragment of eight rows of each.  A workgroup walks its items; its waves take the
+// 128-wide chunks of H in turn and keep U of them in flight, the first ones of the
+// next item too.
+template <int COLS, int WAVES, int OCC>
+__global__ __launch_bounds__(64 * WAVES, OCC) void k_moe_up(ExpertArgs a) {
+  constexpr int NC = COLS / 8, U = 2, kHalf = COLS < 16 ? 8 : 16;
   extern __shared__ __align__(16) uint32_t lds[];
-  __shared__ __align__(16) float red[kWaves * MAXF * NC * 256];
-  const Plan plan = make_plan(a, lds, 16 * MAXF);
+  __shared__ __align__(16) float red[WAVES * NC * 256];
+  const Plan plan = make_plan<WAVES>(a, lds, 16);
   save_plan(a, plan);
   const int lane = threadIdx.x % 64, wave = wave_id(), fr = lane % 16, fg = lane / 16;
-  const int chunks = a.H / 128, steps = steps_of(chunks, U);
-  const int tiles = a.I / (16 * NG), items = plan.jobs * tiles;
+  const int chunks = a.H / 128, steps = steps_of<WAVES>(chunks, U);
+  const int tiles = a.I / COLS, items = plan.jobs * tiles;
   const int64_t panel = 2 * (int64_t)a.I * a.H;
   const auto xb = buffer(a.x, (int64_t)a.T * a.H);
   const auto sb = buffer(a.sx, (int64_t)a.T * chunks * 4);
+  // whether fragment n, at this lane's row of it (r of a column, or of the result), is of gate
+  auto is_gate = [&](int n, int r) { return COLS < 16 ? r < 8 : n < NC / 2; };
 
   // what is fetched next: chunk `step` (of this wave) of item `ahead`
   int ahead = blockIdx.x, step = 0;
   auto wb = buffer(a.w13, 0);
-  uint32_t wrow[NC], xrow[MAXF], srow[MAXF];
+  uint32_t wrow[NC], xrow, srow;
   float next_g, next_u;                              // weight scales of item `ahead`
   auto aim = [&]() {
     const Job job = plan.at(min(ahead, items - 1) / tiles);
-    const int col0 = min(ahead, items - 1) % tiles * 16 * NG;
+    const int col0 = min(ahead, items - 1) % tiles * COLS;
     wb = buffer(a.w13 + job.expert * panel, ahead < items ? panel : 0);
 #pragma unroll
-    for (int n = 0; n < NC; ++n)
-      wrow[n] = (uint32_t)(((n / NG) * a.I + col0 + (n % NG) * 16 + fr) * (int64_t)a.H + fg * 16);
-#pragma unroll
-    for (int f = 0; f < MAXF; ++f) {
-      const int r = f * 16 + fr;
-      const bool there = r < job.n && ahead < items;
-      const uint32_t t = there ? plan.row[job.start + r] >> 16 : 0u;
-      xrow[f] = there ? t * (uint32_t)a.H + fg * 16 : kNoRow;
-      srow[f] = there ? t * 4 : kNoRow;
+    for (int n = 0; n < NC; ++n) {
+      const int col = col0 + (COLS < 16 ? fr % 8 : n % (COLS / kHalf) * 16 + fr);
+      wrow[n] = (uint32_t)(((is_gate(n, fr) ? 0 : a.I) + col) * (int64_t)a.H + fg * 16);
     }
+    const bool there = fr < job.n && ahead < items;
+    const uint32_t t = there ? plan.row[job.start + fr] >> 16 : 0u;
+    xrow = there ? t * (uint32_t)a.H + fg * 16 : kNoRow;
+    srow = there ? t * 4 : kNoRow;
     const float* sc = a.s13 + (int64_t)job.expert * (2 * a.I / 128) * chunks;
-    next_g = lane_scale(sc + (int64_t)(col0 / 128) * chunks, chunks);
-    next_u = lane_scale(sc + (int64_t)((a.I + col0) / 128) * chunks, chunks);
+    next_g = lane_scale<WAVES>(sc + (int64_t)(col0 / 128) * chunks, chunks);
+    next_u = lane_scale<WAVES>(sc + (int64_t)((a.I + col0) / 128) * chunks, chunks);
   };
   struct Chunk {
-    u32x4 w0[NC], w1[NC], x0[MAXF], x1[MAXF];
-    float sx[MAXF];
+    u32x4 w0[NC], w1[NC], x0, x1;
+    float sx;
   } c[U];
   auto fetch = [&](Chunk& k) {
-    const int kb = wave + step * kWaves;
+    const int kb = wave + step * WAVES;
     const uint32_t at = kb < chunks ? (uint32_t)kb * 128 : kNoChunk;
     const uint32_t sat = kb < chunks ? (uint32_t)(kb * a.T * 4) : kNoChunk;
 #pragma unroll
@@ -265,12 +270,9 @@ __global__ __launch_bounds__(kThreads, OCC) void k_moe_up(ExpertArgs a) {
       k.w0[n] = load16(wb, wrow[n] + at);
       k.w1[n] = load16(wb, wrow[n] + at + 64);
     }
-#pragma unroll
-    for (int f = 0; f < MAXF; ++f) {
-      k.x0[f] = load16(xb, xrow[f] + at);
-      k.x1[f] = load16(xb, xrow[f] + at + 64);
-      k.sx[f] = load4(sb, srow[f] + sat);
-    }
+    k.x0 = load16(xb, xrow + at);
+    k.x1 = load16(xb, xrow + at + 64);
+    k.sx = load4(sb, srow + sat);
     ++step;
   };
   if (ahead >= items) return;
@@ -278,35 +280,25 @@ __global__ __launch_bounds__(kThreads, OCC) void k_moe_up(ExpertArgs a) {
 #pragma unroll
   for (int i = 0; i < U; ++i) fetch(c[i]);
   const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
-  v4f acc[MAXF][NC];
-  auto clear = [&]() {
+  v4f acc[NC];
 #pragma unroll
-    for (int f = 0; f < MAXF; ++f)
-#pragma unroll
-      for (int n = 0; n < NC; ++n) acc[f][n] = zero;
-  };
-  clear();
+  for (int n = 0; n < NC; ++n) acc[n] = zero;
   int item = blockIdx.x, done = 0;
   float scale_g = next_g, scale_u = next_u;
   auto finish = [&]() {                              // item is whole: its activations
     const Job job = plan.at(item / tiles);
-    const int col0 = item % tiles * 16 * NG;
+    const int col0 = item % tiles * COLS;
     leave(acc, red);
-    const int m = threadIdx.x / 16, col = threadIdx.x % 16;
-#pragma unroll
-    for (int f = 0; f < MAXF; ++f) {
-      const int r = f * 16 + m;
-      if (r >= job.n) continue;
-      const float share = plan.weight[job.start + r];
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        const float g = total<MAXF, NC>(red, f, n, m, col), u = total<MAXF, NC>(red, f, NG + n, m, col);
-        const float v = share * (g / (1.0f + expf(-g))) * u;
-        const __bf16 hi = (__bf16)v, lo = (__bf16)(v - (float)hi);
-        const int64_t at = (int64_t)(job.start + r) * a.I + place_of(col0 + n * 16 + col);
-        a.hi[at] = __builtin_bit_cast(uint16_t, hi);
-        a.lo[at] = __builtin_bit_cast(uint16_t, lo);
-      }
+    for (int i = threadIdx.x; i < 16 * COLS; i += 64 * WAVES) {
+      const int m = i / COLS, c = i % COLS;
+      if (m >= job.n) break;
+      const float g = total<WAVES, NC>(red, c / 16, m, c % 16);
+      const float u = COLS < 16 ? total<WAVES, NC>(red, 0, m, 8 + c) : total<WAVES, NC>(red, NC / 2 + c / 16, m, c % 16);
+      const float v = plan.weight[job.start + m] * (g / (1.0f + expf(-g))) * u;
+      const __bf16 hi = (__bf16)v, lo = (__bf16)(v - (float)hi);
+      const int64_t at = (int64_t)(job.start + m) * a.I + place_of(col0 + c);
+      a.hi[at] = __builtin_bit_cast(uint16_t, hi);
+      a.lo[at] = __builtin_bit_cast(uint16_t, lo);
     }
     __syncthreads();
   };
@@ -314,17 +306,14 @@ __global__ __launch_bounds__(kThreads, OCC) void k_moe_up(ExpertArgs a) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const float sg = of_lane(scale_g, done), su = of_lane(scale_u, done);
+      const v8i x = join(c[i].x0, c[i].x1);
 #pragma unroll
-      for (int f = 0; f < MAXF; ++f) {
-        const v8i x = join(c[i].x0[f], c[i].x1[f]);
+      for (int n = 0; n < NC; ++n) {
+        const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(c[i].w0[n], c[i].w1[n]), x, zero, 0, 0, 0, 0, 0,
+                                                                      0);
+        const float by = c[i].sx * (is_gate(n, fg * 4) ? sg : su);
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-          const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(c[i].w0[n], c[i].w1[n]), x, zero, 0, 0, 0,
-                                                                        0, 0, 0);
-          const float by = c[i].sx[f] * (n < NG ? sg : su);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[f][n][e] = __builtin_fmaf(p[e], by, acc[f][n][e]);
-        }
+        for (int e = 0; e < 4; ++e) acc[n][e] = __builtin_fmaf(p[e], by, acc[n][e]);
       }
       if (step == steps) {
         ahead += gridDim.x;
@@ -339,7 +328,8 @@ __global__ __launch_bounds__(kThreads, OCC) void k_moe_up(ExpertArgs a) {
         done = 0;
         scale_g = next_g;
         scale_u = next_u;
-        clear();
+#pragma unroll
+        for (int n = 0; n < NC; ++n) acc[n] = zero;
       }
     }
   }
@@ -355,43 +345,40 @@ __device__ __forceinline__ v8bf to_bf16(uint32_t a, uint32_t b) {
   return v8bf{p[0], p[1], q[0], q[1], r[0], r[1], t[0], t[1]};
 }
 
-// Items: one job and 16 NC columns of H, walked like those of k_moe_up.
-template <int MAXF, int NC, int U, int OCC>
-__global__ __launch_bounds__(kThreads, OCC) void k_moe_down(ExpertArgs a) {
+// Items: one job and COLS columns of H, walked like those of k_moe_up.
+template <int COLS, int WAVES, int OCC>
+__global__ __launch_bounds__(64 * WAVES, OCC) void k_moe_down(ExpertArgs a) {
+  constexpr int NC = COLS / 16, U = 2;
   extern __shared__ __align__(16) uint32_t lds[];
-  __shared__ __align__(16) float red[kWaves * MAXF * NC * 256];
+  __shared__ __align__(16) float red[WAVES * NC * 256];
   const Plan plan = load_plan(a, lds);
   const int lane = threadIdx.x % 64, wave = wave_id(), fr = lane % 16, fg = lane / 16;
-  const int chunks = a.I / 128, steps = steps_of(chunks, U);
-  const int tiles = a.H / (16 * NC), items = plan.jobs * tiles;
+  const int chunks = a.I / 128, steps = steps_of<WAVES>(chunks, U);
+  const int tiles = a.H / COLS, items = plan.jobs * tiles;
   const int64_t panel = (int64_t)a.H * a.I, acts = (int64_t)a.T * a.topk * a.I * 2;
   const auto hb = buffer(a.hi, acts), lb = buffer(a.lo, acts);
 
   int ahead = blockIdx.x, step = 0;
   auto wb = buffer(a.w2, 0);
-  uint32_t wrow[NC], arow[MAXF];
+  uint32_t wrow[NC], arow;
   float next_scale;
   auto aim = [&]() {
     const Job job = plan.at(min(ahead, items - 1) / tiles);
-    const int col0 = min(ahead, items - 1) % tiles * 16 * NC;
+    const int col0 = min(ahead, items - 1) % tiles * COLS;
     wb = buffer(a.w2 + job.expert * panel, ahead < items ? panel : 0);
 #pragma unroll
     for (int n = 0; n < NC; ++n) wrow[n] = (uint32_t)((col0 + n * 16 + fr) * (int64_t)a.I + fg * 16);
-    next_scale = lane_scale(a.s2 + ((int64_t)job.expert * (a.H / 128) + col0 / 128) * chunks, chunks);
+    next_scale = lane_scale<WAVES>(a.s2 + ((int64_t)job.expert * (a.H / 128) + col0 / 128) * chunks, chunks);
   };
   auto aim_acts = [&](int item) {
     const Job job = plan.at(min(item, items - 1) / tiles);
-#pragma unroll
-    for (int f = 0; f < MAXF; ++f) {
-      const int r = f * 16 + fr;
-      arow[f] = r < job.n && item < items ? (uint32_t)((job.start + r) * (int64_t)a.I + fg * 8) * 2 : kNoRow;
-    }
+    arow = fr < job.n && item < items ? (uint32_t)((job.start + fr) * (int64_t)a.I + fg * 8) * 2 : kNoRow;
   };
   struct Chunk {
     u32x4 w0[NC], w1[NC];
   } c[U];
   auto fetch = [&](Chunk& k) {
-    const int kb = wave + step * kWaves;
+    const int kb = wave + step * WAVES;
     const uint32_t at = kb < chunks ? (uint32_t)kb * 128 : kNoChunk;
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
@@ -400,17 +387,15 @@ __global__ __launch_bounds__(kThreads, OCC) void k_moe_down(ExpertArgs a) {
     }
     ++step;
   };
-  u32x4 hi[MAXF][4], lo[MAXF][4];
+  u32x4 hi[4], lo[4];
   auto fetch_acts = [&](int s) {
-    const int kb = wave + s * kWaves;
+    const int kb = wave + s * WAVES;
     const uint32_t at = kb < chunks ? (uint32_t)kb * 256 : kNoChunk;
 #pragma unroll
-    for (int f = 0; f < MAXF; ++f)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        hi[f][j] = load16(hb, arow[f] + at + j * 64);
-        lo[f][j] = load16(lb, arow[f] + at + j * 64);
-      }
+    for (int j = 0; j < 4; ++j) {
+      hi[j] = load16(hb, arow + at + j * 64);
+      lo[j] = load16(lb, arow + at + j * 64);
+    }
   };
   if (ahead >= items) return;
   // Loads return in the order they were issued, so the activations of a chunk
@@ -422,28 +407,20 @@ __global__ __launch_bounds__(kThreads, OCC) void k_moe_down(ExpertArgs a) {
 #pragma unroll
   for (int i = 1; i < U; ++i) fetch(c[i]);
   const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
-  v4f acc[MAXF][NC];
-  auto clear = [&]() {
+  v4f acc[NC];
 #pragma unroll
-    for (int f = 0; f < MAXF; ++f)
-#pragma unroll
-      for (int n = 0; n < NC; ++n) acc[f][n] = zero;
-  };
-  clear();
+  for (int n = 0; n < NC; ++n) acc[n] = zero;
   int item = blockIdx.x, done = 0;
   float scales = next_scale;
   auto finish = [&]() {
     const Job job = plan.at(item / tiles);
-    const int col0 = item % tiles * 16 * NC;
+    const int col0 = item % tiles * COLS;
     leave(acc, red);
-    const int m = threadIdx.x / 16, col = threadIdx.x % 16;
-#pragma unroll
-    for (int f = 0; f < MAXF; ++f) {
-      const int r = f * 16 + m;
-      if (r >= job.n) continue;
-      float* to = a.part + (int64_t)(plan.row[job.start + r] & 0xFFFF) * a.H + col0 + col;
-#pragma unroll
-      for (int n = 0; n < NC; ++n) to[n * 16] = total<MAXF, NC>(red, f, n, m, col);
+    for (int i = threadIdx.x; i < 16 * COLS; i += 64 * WAVES) {
+      const int m = i / COLS, c = i % COLS;
+      if (m >= job.n) break;
+      const int place = plan.row[job.start + m] & 0xFFFF;
+      a.part[(int64_t)place * a.H + col0 + c] = total<WAVES, NC>(red, c / 16, m, c % 16);
     }
     __syncthreads();
   };
@@ -455,17 +432,14 @@ __global__ __launch_bounds__(kThreads, OCC) void k_moe_down(ExpertArgs a) {
       for (int n = 0; n < NC; ++n) {
         const v8bf b[4] = {to_bf16(c[i].w0[n].x, c[i].w0[n].y), to_bf16(c[i].w0[n].z, c[i].w0[n].w),
                            to_bf16(c[i].w1[n].x, c[i].w1[n].y), to_bf16(c[i].w1[n].z, c[i].w1[n].w)};
+        v4f p = zero;
 #pragma unroll
-        for (int f = 0; f < MAXF; ++f) {
-          v4f p = zero;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, hi[f][j]), p, 0, 0, 0);
-            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, lo[f][j]), p, 0, 0, 0);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[f][n][e] = __builtin_fmaf(p[e], scale, acc[f][n][e]);
+        for (int j = 0; j < 4; ++j) {
+          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, hi[j]), p, 0, 0, 0);
+          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, lo[j]), p, 0, 0, 0);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][e] = __builtin_fmaf(p[e], scale, acc[n][e]);
       }
       const bool last = ++done == steps;
       if (last) aim_acts(item + gridDim.x);
@@ -482,7 +456,8 @@ __global__ __launch_bounds__(kThreads, OCC) void k_moe_down(ExpertArgs a) {
         if (item >= items) return;
         done = 0;
         scales = next_scale;
-        clear();
+#pragma unroll
+        for (int n = 0; n < NC; ++n) acc[n] = zero;
       }
     }
   }
@@ -647,7 +622,7 @@ constexpr int kUpStage = 2 * kPiece * (64 * 128 + 66 * 4);   // bytes, for 64 ro
 // other, for their accumulators.
 __global__ __launch_bounds__(kThreads, 2) void k_moe_up_wide(ExpertArgs a) {
   extern __shared__ __align__(16) uint32_t lds[];
-  const Plan plan = make_plan(a, lds + kUpStage / 4, 64);
+  const Plan plan = make_plan<kWaves>(a, lds + kUpStage / 4, 64);
   save_plan(a, plan);
   const int tiles = a.I / 128, units = plan.jobs * tiles;
   const Share share = share_of(blockIdx.x, units);
@@ -869,11 +844,17 @@ unsigned grid_of(const ExpertArgs& a, int tiles, int per_cu) {
   return (unsigned)std::min<int64_t>(most, (int64_t)kCus * per_cu);
 }
 
-template <int MAXF, int NG, int NC, int OCC_UP, int OCC_DOWN>
-void launch(const ExpertArgs& a, hipStream_t stream) {
-  const size_t lds = plan_bytes(a);
-  k_moe_up<MAXF, NG, 2, OCC_UP><<<grid_of(a, a.I / (16 * NG), OCC_UP), kThreads, lds, stream>>>(a);
-  k_moe_down<MAXF, NC, 2, OCC_DOWN><<<grid_of(a, a.H / (16 * NC), OCC_DOWN), kThreads, lds, stream>>>(a);
+#ifndef UPC
+#define UPC 32
+#define UPW 4
+#define UPO 3
+#define DNC 64
+#define DNW 4
+#define DNO 3
+#endif
+void launch_narrow(const ExpertArgs& a, hipStream_t stream) {
+  k_moe_up<UPC, UPW, UPO><<<grid_of(a, a.I / UPC, UPO * 4 / UPW), 64 * UPW, plan_bytes(a), stream>>>(a);
+  k_moe_down<DNC, DNW, DNO><<<grid_of(a, a.H / DNC, DNO * 4 / DNW), 64 * DNW, a.T * a.topk * 8, stream>>>(a);
 }
 
 // Whether an expert has enough rows, were they spread evenly.
@@ -889,7 +870,7 @@ hipError_t launch_moe_experts(const ExpertArgs& a, hipStream_t stream) {
     k_moe_up_wide<<<(unsigned)(jobs * (a.I / 64)), kThreads, kUpStage + plan, stream>>>(a);
     k_moe_down_wide<<<(unsigned)(jobs * ((a.H + 255) / 256) * 2), kThreads, kDownStage + plan, stream>>>(a);
   } else {
-    launch<1, 2, 4, 3, 3>(a, stream);
+    launch_narrow(a, stream);
   }
   k_moe_join<<<dim3((unsigned)((a.H / 4 + kThreads - 1) / kThreads), (unsigned)a.T), kThreads, 0, stream>>>(a);
   return hipGetLastError();
