@@ -345,30 +345,33 @@ __device__ __forceinline__ v8bf to_bf16(uint32_t a, uint32_t b) {
   return v8bf{p[0], p[1], q[0], q[1], r[0], r[1], t[0], t[1]};
 }
 
-// Items: one job and COLS columns of H, walked like those of k_moe_up.
-template <int COLS, int WAVES, int OCC>
-__global__ __launch_bounds__(64 * WAVES, OCC) void k_moe_down(ExpertArgs a) {
+// Items: one job and COLS columns of H, walked like those of k_moe_up by KS waves
+// that take the chunks of I in turn: one wave where there are items enough for all
+// (nothing is shared but the plan then), else four.
+template <int COLS, int KS>
+__global__ __launch_bounds__(kThreads, 3) void k_moe_down(ExpertArgs a) {
   constexpr int NC = COLS / 16, U = 2;
   extern __shared__ __align__(16) uint32_t lds[];
-  __shared__ __align__(16) float red[WAVES * NC * 256];
+  __shared__ __align__(16) float red[KS > 1 ? KS * NC * 256 : 1];
   const Plan plan = load_plan(a, lds);
-  const int lane = threadIdx.x % 64, wave = wave_id(), fr = lane % 16, fg = lane / 16;
-  const int chunks = a.I / 128, steps = steps_of<WAVES>(chunks, U);
-  const int tiles = a.H / COLS, items = plan.jobs * tiles;
+  const int lane = threadIdx.x % 64, fr = lane % 16, fg = lane / 16;
+  const int chunks = a.I / 128, steps = steps_of<KS>(chunks, U), part = wave_id() % KS;
+  const int tiles = a.H / COLS, items = plan.jobs * tiles, stride = gridDim.x * (kWaves / KS);
   const int64_t panel = (int64_t)a.H * a.I, acts = (int64_t)a.T * a.topk * a.I * 2;
   const auto hb = buffer(a.hi, acts), lb = buffer(a.lo, acts);
 
-  int ahead = blockIdx.x, step = 0;
+  int item = blockIdx.x * (kWaves / KS) + wave_id() / KS, ahead = item, step = 0;
+  if (item >= items) return;
   auto wb = buffer(a.w2, 0);
   uint32_t wrow[NC], arow;
-  float next_scale;
+  const float *scale, *next_scale;
   auto aim = [&]() {
     const Job job = plan.at(min(ahead, items - 1) / tiles);
     const int col0 = min(ahead, items - 1) % tiles * COLS;
     wb = buffer(a.w2 + job.expert * panel, ahead < items ? panel : 0);
 #pragma unroll
     for (int n = 0; n < NC; ++n) wrow[n] = (uint32_t)((col0 + n * 16 + fr) * (int64_t)a.I + fg * 16);
-    next_scale = lane_scale<WAVES>(a.s2 + ((int64_t)job.expert * (a.H / 128) + col0 / 128) * chunks, chunks);
+    next_scale = a.s2 + ((int64_t)job.expert * (a.H / 128) + col0 / 128) * chunks;
   };
   auto aim_acts = [&](int item) {
     const Job job = plan.at(min(item, items - 1) / tiles);
@@ -378,7 +381,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_moe_down(ExpertArgs a) {
     u32x4 w0[NC], w1[NC];
   } c[U];
   auto fetch = [&](Chunk& k) {
-    const int kb = wave + step * WAVES;
+    const int kb = part + step * KS;
     const uint32_t at = kb < chunks ? (uint32_t)kb * 128 : kNoChunk;
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
@@ -389,7 +392,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_moe_down(ExpertArgs a) {
   };
   u32x4 hi[4], lo[4];
   auto fetch_acts = [&](int s) {
-    const int kb = wave + s * WAVES;
+    const int kb = part + s * KS;
     const uint32_t at = kb < chunks ? (uint32_t)kb * 256 : kNoChunk;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -397,11 +400,10 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_moe_down(ExpertArgs a) {
       lo[j] = load16(lb, arow + at + j * 64);
     }
   };
-  if (ahead >= items) return;
   // Loads return in the order they were issued, so the activations of a chunk
   // (from L2) go out ahead of weights (from memory) that are needed later.
   aim();
-  aim_acts(blockIdx.x);
+  aim_acts(item);
   fetch(c[0]);
   fetch_acts(0);
 #pragma unroll
@@ -410,24 +412,31 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_moe_down(ExpertArgs a) {
   v4f acc[NC];
 #pragma unroll
   for (int n = 0; n < NC; ++n) acc[n] = zero;
-  int item = blockIdx.x, done = 0;
-  float scales = next_scale;
   auto finish = [&]() {
     const Job job = plan.at(item / tiles);
-    const int col0 = item % tiles * COLS;
-    leave(acc, red);
-    for (int i = threadIdx.x; i < 16 * COLS; i += 64 * WAVES) {
-      const int m = i / COLS, c = i % COLS;
-      if (m >= job.n) break;
-      const int place = plan.row[job.start + m] & 0xFFFF;
-      a.part[(int64_t)place * a.H + col0 + c] = total<WAVES, NC>(red, c / 16, m, c % 16);
+    float* out = a.part + item % tiles * COLS;
+    if (KS == 1) {
+      if (fr >= job.n) return;                       // a lane has four columns of a row
+      const int64_t place = plan.row[job.start + fr] & 0xFFFF;
+#pragma unroll
+      for (int n = 0; n < NC; ++n) *reinterpret_cast<v4f*>(out + place * a.H + n * 16 + fg * 4) = acc[n];
+    } else {
+      leave(acc, red);
+      for (int i = threadIdx.x; i < 16 * COLS; i += kThreads) {
+        const int m = i / COLS, c = i % COLS;
+        if (m >= job.n) break;
+        const int64_t place = plan.row[job.start + m] & 0xFFFF;
+        out[place * a.H + c] = total<KS, NC>(red, c / 16, m, c % 16);
+      }
+      __syncthreads();
     }
-    __syncthreads();
   };
+  int done = 0;
+  scale = next_scale;
   for (;;) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const float scale = of_lane(scales, done);
+      const float s = scale[min(part + done * KS, chunks - 1)];
 #pragma unroll
       for (int n = 0; n < NC; ++n) {
         const v8bf b[4] = {to_bf16(c[i].w0[n].x, c[i].w0[n].y), to_bf16(c[i].w0[n].z, c[i].w0[n].w),
@@ -439,23 +448,23 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_moe_down(ExpertArgs a) {
           p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, lo[j]), p, 0, 0, 0);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][e] = __builtin_fmaf(p[e], scale, acc[n][e]);
+        for (int e = 0; e < 4; ++e) acc[n][e] = __builtin_fmaf(p[e], s, acc[n][e]);
       }
       const bool last = ++done == steps;
-      if (last) aim_acts(item + gridDim.x);
+      if (last) aim_acts(item + stride);
       fetch_acts(last ? 0 : done);
       if (step == steps) {
-        ahead += gridDim.x;
+        ahead += stride;
         step = 0;
         aim();
       }
       fetch(c[i]);
       if (last) {
         finish();
-        item += gridDim.x;
+        item += stride;
         if (item >= items) return;
         done = 0;
-        scales = next_scale;
+        scale = next_scale;
 #pragma unroll
         for (int n = 0; n < NC; ++n) acc[n] = zero;
       }
@@ -844,21 +853,34 @@ unsigned grid_of(const ExpertArgs& a, int tiles, int per_cu) {
   return (unsigned)std::min<int64_t>(most, (int64_t)kCus * per_cu);
 }
 
-#ifndef UPC
-#define UPC 32
-#define UPW 4
-#define UPO 3
-#define DNC 64
-#define DNW 4
-#define DNO 3
-#endif
-void launch_narrow(const ExpertArgs& a, hipStream_t stream) {
-  k_moe_up<UPC, UPW, UPO><<<grid_of(a, a.I / UPC, UPO * 4 / UPW), 64 * UPW, plan_bytes(a), stream>>>(a);
-  k_moe_down<DNC, DNW, DNO><<<grid_of(a, a.H / DNC, DNO * 4 / DNW), 64 * DNW, a.T * a.topk * 8, stream>>>(a);
+template <int COLS>
+void launch_up(const ExpertArgs& a, hipStream_t stream) {
+  k_moe_up<COLS, kWaves, 4><<<grid_of(a, a.I / COLS, 4), kThreads, plan_bytes(a), stream>>>(a);
 }
 
-// Whether an expert has enough rows, were they spread evenly.
-bool wide(const ExpertArgs& a) { return a.T * a.topk >= 4 * std::min(a.E, a.T * a.topk); }
+template <int COLS, int KS>
+void launch_down(const ExpertArgs& a, hipStream_t stream) {
+  const int groups = (a.H / COLS + kWaves / KS - 1) / (kWaves / KS);
+  k_moe_down<COLS, KS><<<grid_of(a, groups, 3), kThreads, a.T * a.topk * 8, stream>>>(a);
+}
+
+// Few items: narrower ones, so that more workgroups (waves) share the reading.
+void launch_narrow(const ExpertArgs& a, hipStream_t stream) {
+  const int experts = std::min(a.E, a.T * a.topk);   // that may have rows
+  if (experts * (a.I / 16) < 200) launch_up<8>(a, stream);
+  else launch_up<16>(a, stream);
+  if (experts * (a.H / 64) >= 800) launch_down<64, 1>(a, stream);
+  else if (a.I <= 256) launch_down<32, 1>(a, stream);
+  else if (experts * (a.H / 32) > 128) launch_down<32, 4>(a, stream);
+  else launch_down<16, 4>(a, stream);
+}
+
+// Whether an expert has many rows, were they spread evenly, and the chip is full
+// with fewer and larger shares.
+bool wide(const ExpertArgs& a) {
+  const int experts = std::min(a.E, a.T * a.topk);
+  return a.T * a.topk >= 8 * experts && experts * (a.I / 128) >= 64;
+}
 
 }  // namespace
 
