@@ -21,7 +21,7 @@ _PUBLIC = (
     "cache_append", "cache_attention", "cache_attention_tile", "cache_attention_workspace_bytes",
     "cache_attention_weights", "cache_attention_weights_workspace_bytes", "cache_evict",
     "rms_norm_quantize", "rms_norm_backward", "rms_norm_backward_workspace_bytes", "moe_route", "moe_route_backward",
-    "moe_experts", "moe_experts_workspace_bytes",
+    "moe_experts", "moe_experts_tile", "moe_experts_workspace_bytes",
     "cast_to_e4m3", "gemm_tile", "stream_reference", "abi_version", "Fp8bsError", "library",
 )
 

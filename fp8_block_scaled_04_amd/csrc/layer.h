@@ -69,6 +69,12 @@ struct ExpertArgs {
 };
 
 int32_t norm_back_groups(int64_t M, int64_t K);
+// How a call of these sizes runs: rows per pass, columns of the two products,
+// waves that share the second's.
+struct ExpertTile {
+  int32_t rows, up, down, waves;
+};
+ExpertTile experts_tile(const ExpertArgs& a);
 // Bytes of the workspace; lays it out from `base`.
 int64_t experts_workspace(ExpertArgs& a, void* base);
 

@@ -108,6 +108,17 @@ fp8bs_status fp8bs_moe_route_backward(const void* logits, int32_t logits_type, c
   return launched(fp8bs::launch_moe_route_back(a, (hipStream_t)stream));
 }
 
+fp8bs_status fp8bs_moe_experts_tile(int64_t T, int64_t H, int64_t I, int32_t E, int32_t topk, int32_t* rows,
+                                    int32_t* up_columns, int32_t* down_columns, int32_t* down_waves) {
+  if (!expert_sizes_fit(T, H, I, E, topk)) return FP8BS_ERR_SHAPE;
+  if (!rows || !up_columns || !down_columns || !down_waves) return FP8BS_ERR_NULL;
+  fp8bs::ExpertArgs a{};
+  a.T = (int32_t)T, a.H = (int32_t)H, a.I = (int32_t)I, a.E = E, a.topk = topk;
+  const fp8bs::ExpertTile t = experts_tile(a);
+  *rows = t.rows, *up_columns = t.up, *down_columns = t.down, *down_waves = t.waves;
+  return FP8BS_OK;
+}
+
 fp8bs_status fp8bs_moe_experts_workspace(int64_t T, int64_t H, int64_t I, int32_t E, int32_t topk, int64_t* bytes) {
   if (!expert_sizes_fit(T, H, I, E, topk)) return FP8BS_ERR_SHAPE;
   if (!bytes) return FP8BS_ERR_NULL;

@@ -350,6 +350,7 @@ __device__ __forceinline__ v8bf to_bf16(uint32_t a, uint32_t b) {
 // (nothing is shared but the plan then), else four.
 template <int COLS, int KS>
 __global__ __launch_bounds__(kThreads, 3) void k_moe_down(ExpertArgs a) {
+  static_assert(KS == 1 || KS == kWaves, "the sums over waves and their barriers are the whole workgroup's");
   constexpr int NC = COLS / 16, U = 2;
   extern __shared__ __align__(16) uint32_t lds[];
   __shared__ __align__(16) float red[KS > 1 ? KS * NC * 256 : 1];
@@ -864,19 +865,29 @@ void launch_down(const ExpertArgs& a, hipStream_t stream) {
   k_moe_down<COLS, KS><<<grid_of(a, groups, 3), kThreads, a.T * a.topk * 8, stream>>>(a);
 }
 
-// Few items: narrower ones, so that more workgroups (waves) share the reading.
-void launch_narrow(const ExpertArgs& a, hipStream_t stream) {
+// Narrow items where there are few, so that more workgroups share the reading.
+// Kernel times in us of both sides, by (tokens, experts, topk, H, I):
+//   up, 8 columns against 16: (1, 2, 2, 6400, 256) 9.6 / 12.4, (1, 48, 5, 1792, 384)
+//     7.6 / 8.4, (4, 64, 1, 2048, 768) 8.4 / 8.4, (3, 128, 5, 4224, 768) 25.3 / 24.0
+//   down, one wave per item against four: (1, 32, 8, 7168, 2048) 24.5 / 26.5,
+//     (35, 32, 5, 4992, 256) 14.8 / 23.6, (16, 32, 8, 7168, 2048) 98.9 / 92.3; of few
+//     items (39, 32, 5, 1408, 2048) 29.6 / 25.0, (1, 4, 2, 7168, 4096) 39.0 / 15.6
+//   down, four waves, 64 columns against 32: (58, 32, 4, 1024, 1024) 12.1 / 14.4,
+//     (4, 64, 1, 2048, 768) 6.2 / 5.2; 32 against 16: the same 5.2 / 6.0, (1, 8, 2,
+//     1024, 512) 4.4 / 4.1
+ExpertTile narrow_tile(const ExpertArgs& a) {
   const int experts = std::min(a.E, a.T * a.topk);   // that may have rows
-  if (experts * (a.I / 16) < 200) launch_up<8>(a, stream);
-  else launch_up<16>(a, stream);
-  if (experts * (a.H / 64) >= 800) launch_down<64, 1>(a, stream);
-  else if (a.I <= 256) launch_down<32, 1>(a, stream);
-  else if (experts * (a.H / 32) > 128) launch_down<32, 4>(a, stream);
-  else launch_down<16, 4>(a, stream);
+  const int up = experts * (a.I / 16) < 200 ? 8 : 16;
+  const int items = experts * (a.H / 64);
+  if (items >= 800 && (a.I <= 512 || a.T * a.topk < 4 * experts)) return {16, up, 64, 1};
+  if (a.I <= 256) return {16, up, 32, 1};
+  return {16, up, items >= 250 ? 64 : items > 64 ? 32 : 16, 4};
 }
 
 // Whether an expert has many rows, were they spread evenly, and the chip is full
-// with fewer and larger shares.
+// with fewer and larger shares.  Both products, wide against narrow: (32, 32, 8,
+// 7168, 2048) 256 / 267 us, (24, 32, 8, 7168, 2048) 255 / 257, (64, 8, 4, 4096,
+// 1536) 61 / 77, (32, 8, 8, 2048, 512) 26 / 24, (36, 4, 3, 2816, 256) 26 / 15.
 bool wide(const ExpertArgs& a) {
   const int experts = std::min(a.E, a.T * a.topk);
   return a.T * a.topk >= 8 * experts && experts * (a.I / 128) >= 64;
@@ -884,15 +895,24 @@ bool wide(const ExpertArgs& a) {
 
 }  // namespace
 
+ExpertTile experts_tile(const ExpertArgs& a) { return wide(a) ? ExpertTile{64, 128, 256, 4} : narrow_tile(a); }
+
 hipError_t launch_moe_experts(const ExpertArgs& a, hipStream_t stream) {
-  if (wide(a)) {
+  const ExpertTile t = experts_tile(a);
+  if (t.rows == 64) {
     // (jobs of up to 64 rows: at most one per expert with a row, and one more per 64 rows)
     const int64_t jobs = std::min(a.E, a.T * a.topk) + a.T * a.topk / 64;
     const size_t plan = plan_bytes(a);
     k_moe_up_wide<<<(unsigned)(jobs * (a.I / 64)), kThreads, kUpStage + plan, stream>>>(a);
     k_moe_down_wide<<<(unsigned)(jobs * ((a.H + 255) / 256) * 2), kThreads, kDownStage + plan, stream>>>(a);
   } else {
-    launch_narrow(a, stream);
+    if (t.up == 8) launch_up<8>(a, stream);
+    else launch_up<16>(a, stream);
+    if (t.waves == 1 && t.down == 64) launch_down<64, 1>(a, stream);
+    else if (t.waves == 1) launch_down<32, 1>(a, stream);
+    else if (t.down == 64) launch_down<64, 4>(a, stream);
+    else if (t.down == 32) launch_down<32, 4>(a, stream);
+    else launch_down<16, 4>(a, stream);
   }
   k_moe_join<<<dim3((unsigned)((a.H / 4 + kThreads - 1) / kThreads), (unsigned)a.T), kThreads, 0, stream>>>(a);
   return hipGetLastError();

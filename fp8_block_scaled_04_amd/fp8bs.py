@@ -86,6 +86,7 @@ _route = _sig("fp8bs_moe_route", [_P, _I32, _I64, _I32, _I32, _P, _P, _U32, _P])
 _route_back = _sig("fp8bs_moe_route_backward", [_P, _I32, _P, _P, _I64, _I32, _I32, _P, _U32, _P])
 _experts = _sig("fp8bs_moe_experts",
                 [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _P, _I64, _P])
+_experts_tile = _sig("fp8bs_moe_experts_tile", [_I64, _I64, _I64, _I32, _I32, _P, _P, _P, _P])
 _experts_ws = _sig("fp8bs_moe_experts_workspace", [_I64, _I64, _I64, _I32, _I32, _P])
 _lib.fp8bs_status_str.argtypes = [ctypes.c_int]
 _lib.fp8bs_status_str.restype = ctypes.c_char_p
@@ -838,6 +839,17 @@ def moe_experts_workspace_bytes(T: int, H: int, I: int, E: int, topk: int) -> in
     out = ctypes.c_int64(0)
     _check(_experts_ws(T, H, I, E, topk, ctypes.byref(out)), "moe_experts_workspace")
     return int(out.value)
+
+
+def moe_experts_tile(T: int, H: int, I: int, E: int, topk: int):
+    """(rows per pass over an expert's weights, columns of the first product, of
+    the second, waves that share the second's) of the kernels that moe_experts
+    would run on for these sizes; host-side, no device work."""
+    _fits(E, topk)
+    out = (ctypes.c_int32 * 4)()
+    base = ctypes.addressof(out)
+    _check(_experts_tile(T, H, I, E, topk, base, base + 4, base + 8, base + 12), "moe_experts_tile")
+    return tuple(int(v) for v in out)
 
 
 def moe_experts(x, sx, ids, weights, w13, s13, w2, s2, out_dtype=torch.bfloat16, out=None, workspace=None):

@@ -5,8 +5,8 @@
  * tokens.  Part of the library that fp8bs.h declares; its formats, quantization
  * rule and conventions (device pointers, streams, argument checks and their
  * order, status codes, nothing allocated or kept) hold here too.  Scalars are
- * checked with the flags (FP8BS_ERR_FLAGS); two queries of workspace sizes run
- * on the host alone.
+ * checked with the flags (FP8BS_ERR_FLAGS); two queries of workspace sizes and one of
+ * tiles run on the host alone.
  */
 #ifndef FP8BS_LAYER_H
 #define FP8BS_LAYER_H
@@ -124,6 +124,13 @@ fp8bs_status fp8bs_moe_experts(const uint8_t* x, const float* sx, const int32_t*
                                const uint8_t* w13, const float* s13, const uint8_t* w2, const float* s2, void* out,
                                int64_t T, int64_t H, int64_t I, int32_t E, int32_t topk, int32_t out_dtype,
                                void* workspace, int64_t workspace_bytes, fp8bs_stream_t stream);
+
+/* Kernels that a fp8bs_moe_experts call of these sizes would run on (host-side
+ * query for tests and tuning): rows that one pass over an expert's weights serves
+ * (16 or 64), columns of a workgroup in the first and in the second product, and
+ * the waves that share them in the second.  HOST pointers. */
+fp8bs_status fp8bs_moe_experts_tile(int64_t T, int64_t H, int64_t I, int32_t E, int32_t topk, int32_t* rows,
+                                    int32_t* up_columns, int32_t* down_columns, int32_t* down_waves);
 
 /* Workspace bytes of fp8bs_moe_experts (bytes: HOST pointer). */
 fp8bs_status fp8bs_moe_experts_workspace(int64_t T, int64_t H, int64_t I, int32_t E, int32_t topk, int64_t* bytes);

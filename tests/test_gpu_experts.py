@@ -83,18 +83,21 @@ def test_experts(T, H, I, E, topk, pad):
 def exact_case(T, H, I, E, topk, seed, ids=None):
     """Whole numbers: x in {0, 1}, at least 64 ones in each row; gate weights 1;
     up weights in {-1, 0, 1}, nine of ten 0, so that no sum passes 24 bits; w2 in
-    {-1, 0, 1}; scales and weights powers of two."""
+    {-1, 0, 1}, more 0 where many terms are added; scales and weights powers of
+    two.  At most 16 experts differ (in their codes; all do in their scales)."""
     rng = np.random.default_rng(seed)
     w = {}
-    x = (rng.random((T, H)) < 0.55).astype(np.float32)
+    x = (rng.random((T, H)) < (0.55 if H <= 640 else 80 / H)).astype(np.float32)
     x[:, :64] = 1
     w["x"] = e4m3.encode(x)
     w["sx"] = np.ones((H // 128, T), np.float32)
-    w13 = np.ones((E, 2 * I, H), np.float32)
-    w13[:, I:] = rng.choice([-1, 0, 1], (E, I, H), p=[0.05, 0.9, 0.05])
-    w["w13"] = e4m3.encode(w13)
+    few = min(E, 16)
+    w13 = np.ones((few, 2 * I, H), np.float32)
+    w13[:, I:] = rng.choice([-1, 0, 1], (few, I, H), p=[0.05, 0.9, 0.05])
+    w["w13"] = e4m3.encode(w13)[np.arange(E) % few]
     w["s13"] = np.exp2(rng.integers(0, 2, (E, 2 * I // 128, H // 128))).astype(np.float32)
-    w["w2"] = e4m3.encode(rng.integers(-1, 2, (E, H, I)).astype(np.float32))
+    p = min(1 / 3, 500 / (I * topk) * (134 / float(x.sum(1).mean())) ** 1.5)
+    w["w2"] = e4m3.encode(rng.choice([-1, 0, 1], (few, H, I), p=[p, 1 - 2 * p, p]).astype(np.float32))[np.arange(E) % few]
     w["s2"] = np.exp2(rng.integers(-1, 2, (E, H // 128, I // 128))).astype(np.float32)
     if ids is None:
         ids = np.stack([rng.permutation(E)[:topk] for _ in range(T)])
@@ -116,9 +119,36 @@ def check_exact(w, **kw):
                                           (15, 128, 128, 1, 1), (16, 128, 128, 2, 2), (17, 128, 128, 1, 1),
                                           (31, 256, 128, 2, 1), (33, 128, 128, 2, 2), (49, 128, 256, 3, 2),
                                           (64, 128, 128, 1, 1), (65, 128, 128, 1, 1), (100, 256, 128, 2, 1),
-                                          (128, 128, 128, 2, 2), (128, 128, 128, 20, 16), (7, 640, 128, 64, 4), (128, 128, 128, 1024, 16)])
+                                          (128, 128, 128, 2, 2), (128, 128, 128, 20, 16), (7, 640, 128, 64, 4),
+                                          (128, 128, 128, 1024, 16), (128, 128, 128, 512, 16)])
 def test_experts_exactly(T, H, I, E, topk):
     check_exact(exact_case(T, H, I, E, topk, seed=T * 3 + H))
+
+
+# Every kernel, pinned: rows per pass, columns of the two products, waves that share the second's.
+@pytest.mark.parametrize("tile,T,H,I,E,topk", [
+    ((16, 8, 16, 4), 1, 128, 1152, 9, 2), ((16, 8, 32, 1), 3, 2048, 256, 9, 1), ((16, 8, 32, 4), 2, 1152, 384, 9, 3),
+    ((16, 16, 32, 4), 40, 256, 1152, 40, 2), ((16, 16, 64, 4), 3, 2048, 384, 40, 4), ((16, 16, 64, 4), 50, 1024, 640, 60, 6),
+    ((16, 16, 64, 1), 4, 2176, 640, 30, 6), ((16, 16, 64, 1), 60, 4096, 128, 100, 2),
+    # many rows: halves of units alone; whole units of the first product, of the second (its last one half empty); up to
+    # 16, 32 and 64 rows each, and more
+    ((64, 128, 256, 4), 64, 256, 384, 24, 8), ((64, 128, 256, 4), 64, 128, 1024, 64, 8),
+    ((64, 128, 256, 4), 64, 1920, 128, 64, 8), ((64, 128, 256, 4), 128, 128, 1024, 64, 16),
+    ((64, 128, 256, 4), 128, 1920, 128, 64, 16), ((64, 128, 256, 4), 128, 384, 640, 16, 8),
+    ((64, 128, 256, 4), 128, 640, 1024, 16, 16)])
+def test_experts_exactly_on_every_kernel(tile, T, H, I, E, topk):
+    assert fb.moe_experts_tile(T, H, I, E, topk) == tile
+    check_exact(exact_case(T, H, I, E, topk, seed=T + H + I))
+
+
+@pytest.mark.parametrize("T,H,I,E,topk", [(64, 256, 512, 20, 8), (128, 128, 1024, 24, 3), (100, 256, 640, 16, 10)])
+def test_experts_with_many_rows(T, H, I, E, topk):
+    assert fb.moe_experts_tile(T, H, I, E, topk)[0] == 64
+    w = expert_case(T, H, I, E, topk, seed=T, pad=3)
+    ref, tol = bound(w, U)
+    got = fb.moe_experts(*expert_dev(w), out_dtype=torch.float32)
+    assert np.all(np.abs(got.cpu().numpy() - ref) <= tol)
+    assert float(np.sqrt(((got.cpu().numpy() - ref) ** 2).sum() / (ref ** 2).sum())) < 2.0 ** -10
 
 
 @pytest.mark.parametrize("places", [2, 40])

@@ -38,7 +38,7 @@ def caller(lib, name, args, good):
 
 def test_every_declared_symbol_is_exported(lib):
     names = sorted(set(re.findall(r"^fp8bs_status (fp8bs_\w+)\s*\(", open(HEADER).read(), re.M)))
-    assert len(names) == 7, names
+    assert len(names) == 8, names
     for n in names:
         assert hasattr(lib, n), n
 
@@ -132,6 +132,28 @@ def test_experts(lib):
         assert call(**{bad: ODD}) == ALIGN, bad
     if NO_DEVICE:
         assert call() == DEVICE and call(dt=1, sx=0x10004, k=16, n=1 << 30) == DEVICE    # (topk may pass E)
+
+
+def test_experts_tile(lib):
+    f = lib.fp8bs_moe_experts_tile
+    f.argtypes, f.restype = [I64, I64, I64, I32, I32, P, P, P, P], ctypes.c_int
+    v = (I32 * 4)()
+    p = ctypes.addressof(v)
+
+    def tile(*sizes):
+        assert f(*sizes, p, p + 4, p + 8, p + 12) == OK
+        return tuple(v)
+    assert f(129, 256, 128, 4, 2, p, p, p, p) == SHAPE and f(3, 256, 100, 4, 2, p, p, p, p) == SHAPE
+    assert f(3, 256, 128, 4, 2, p, None, p, p) == NULL
+    # many rows per expert that fill the chip; too few columns or rows for that
+    assert tile(64, 7168, 2048, 32, 8) == tile(32, 7168, 2048, 32, 8) == tile(64, 256, 384, 24, 8) == (64, 128, 256, 4)
+    assert tile(31, 7168, 2048, 32, 8)[0] == tile(36, 2816, 256, 4, 3)[0] == tile(128, 128, 128, 63, 16)[0] == 16
+    # one wave per item, or four; narrower items where they are few
+    assert tile(1, 7168, 2048, 32, 8) == (16, 16, 64, 1) and tile(35, 4992, 256, 32, 5) == (16, 16, 64, 1)
+    assert tile(16, 7168, 2048, 32, 8) == (16, 16, 64, 4) and tile(1, 7168, 4096, 4, 2) == (16, 16, 32, 4)
+    assert tile(1, 1024, 512, 8, 2) == (16, 8, 16, 4) and tile(1, 1024, 256, 8, 2) == (16, 8, 32, 1)
+    from fp8_block_scaled_04_amd import fp8bs as fb
+    assert fb.moe_experts_tile(1, 7168, 2048, 32, 8) == (16, 16, 64, 1)
 
 
 def test_binding_refuses_cpu_tensors_and_large_counts(lib_path):
