@@ -30,7 +30,7 @@ constexpr int kThreads = 64 * kWaves;
 // A buffer of `bytes` (below 2^31) from `base`: reads past them give 0 without
 // touching memory.  Offsets of chunks and rows that do not exist; either of them,
 // and their sum with any offset that exists, is past every buffer of weights,
-// and the sum of both past every buffer of rows (at most 2^24 bytes).
+// and the sum of both past every buffer of rows (at most 2^27 bytes).
 constexpr uint32_t kNoChunk = 0x80000000u, kNoRow = 0x90000000u;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
@@ -82,10 +82,8 @@ int plan_bytes(const ExpertArgs& a) { return (a.T * a.topk * 4 + a.E * (mask_wor
 int image_words(const ExpertArgs& a) { return 1 + 2 * a.T * a.topk; }
 
 // `block`: rows that one pass over an expert's weights serves.
-template <int WAVES>
 __device__ __forceinline__ Plan make_plan(const ExpertArgs& a, uint32_t* lds, int block) {
-  constexpr int kThreads = 64 * WAVES;
-  __shared__ int waves[WAVES];
+  __shared__ int waves[kWaves];
   const int tid = threadIdx.x, places = a.T * a.topk, words = mask_words(a.T);
   Plan p;
   p.job = lds;
@@ -126,7 +124,7 @@ __device__ __forceinline__ Plan make_plan(const ExpertArgs& a, uint32_t* lds, in
   __syncthreads();
   before -= mine;
   int all = 0;
-  for (int w = 0; w < WAVES; ++w) {
+  for (int w = 0; w < kWaves; ++w) {
     if (w < tid / 64) before += waves[w];
     all += waves[w];
   }
@@ -160,14 +158,14 @@ __device__ __forceinline__ Plan make_plan(const ExpertArgs& a, uint32_t* lds, in
 // (Places without a row hold what LDS held: never used.)
 __device__ __forceinline__ void save_plan(const ExpertArgs& a, const Plan& p) {
   if (blockIdx.x != 0) return;
-  for (int i = threadIdx.x; i < 2 * a.T * a.topk; i += blockDim.x) a.image[1 + i] = p.job[i];
+  for (int i = threadIdx.x; i < 2 * a.T * a.topk; i += kThreads) a.image[1 + i] = p.job[i];
   if (threadIdx.x == 0) a.image[0] = (uint32_t)p.jobs;
 }
 
 __device__ __forceinline__ Plan load_plan(const ExpertArgs& a, uint32_t* lds) {
   const int places = a.T * a.topk;
   Plan p{lds, lds + places, nullptr, __builtin_amdgcn_readfirstlane((int)a.image[0])};
-  for (int i = threadIdx.x; i < 2 * places; i += blockDim.x) lds[i] = a.image[1 + i];
+  for (int i = threadIdx.x; i < 2 * places; i += kThreads) lds[i] = a.image[1 + i];
   __syncthreads();
   return p;
 }
@@ -181,7 +179,7 @@ __device__ __forceinline__ int place_of(int c) {
   return (c & ~63) + ((c >> 3) & 1) * 32 + ((c >> 4) & 3) * 8 + (c & 7);
 }
 
-// The waves' accumulators of NC fragments, in LDS (WAVES * NC * 256 floats) for
+// The waves' accumulators of NC fragments, in LDS (kWaves * NC * 256 floats) for
 // the sums over them.
 template <int NC>
 __device__ __forceinline__ void leave(const v4f (&acc)[NC], float* red) {
@@ -191,25 +189,24 @@ __device__ __forceinline__ void leave(const v4f (&acc)[NC], float* red) {
   __syncthreads();
 }
 // Row m of tokens, row c of the weights of fragment n: lane (c / 4) 16 + m has c % 4.
-template <int WAVES, int NC>
+template <int NC>
 __device__ __forceinline__ float total(const float* red, int n, int m, int c) {
   float t = 0.0f;
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) t += red[(w * NC + n) * 256 + ((c / 4) * 16 + m) * 4 + c % 4];
+  for (int w = 0; w < kWaves; ++w) t += red[(w * NC + n) * 256 + ((c / 4) * 16 + m) * 4 + c % 4];
   return t;
 }
 
-// The scales of one weight row block, chunk wave + WAVES l in lane l.
-template <int WAVES>
+// The scales of one weight row block, chunk wave + kWaves l in lane l.
 __device__ __forceinline__ float lane_scale(const float* block, int chunks) {
-  const int kb = wave_id() + (threadIdx.x % 64) * WAVES;
+  const int kb = wave_id() + (threadIdx.x % 64) * kWaves;
   return kb < chunks ? block[kb] : 0.0f;
 }
-// Chunks of one wave, at least the U that it fetches ahead (those past the end are
-// zeros): what is fetched is never more than one item ahead.
-template <int WAVES>
-__device__ __forceinline__ int steps_of(int chunks, int U) {
-  return max((chunks + WAVES - 1) / WAVES, U);
+// Chunks of one of the `waves` that share an item, at least the U that it fetches
+// ahead (those past the end are zeros): what is fetched is never more than one item
+// ahead.
+__device__ __forceinline__ int steps_of(int chunks, int waves, int U) {
+  return max((chunks + waves - 1) / waves, U);
 }
 
 // ---- gate and up ----
@@ -219,15 +216,15 @@ __device__ __forceinline__ int steps_of(int chunks, int U) {
 // fragment of eight rows of each.  A workgroup walks its items; its waves take the
 // 128-wide chunks of H in turn and keep U of them in flight, the first ones of the
 // next item too.
-template <int COLS, int WAVES, int OCC>
-__global__ __launch_bounds__(64 * WAVES, OCC) void k_moe_up(ExpertArgs a) {
+template <int COLS>
+__global__ __launch_bounds__(kThreads, 4) void k_moe_up(ExpertArgs a) {
   constexpr int NC = COLS / 8, U = 2, kHalf = COLS < 16 ? 8 : 16;
   extern __shared__ __align__(16) uint32_t lds[];
-  __shared__ __align__(16) float red[WAVES * NC * 256];
-  const Plan plan = make_plan<WAVES>(a, lds, 16);
+  __shared__ __align__(16) float red[kWaves * NC * 256];
+  const Plan plan = make_plan(a, lds, 16);
   save_plan(a, plan);
   const int lane = threadIdx.x % 64, wave = wave_id(), fr = lane % 16, fg = lane / 16;
-  const int chunks = a.H / 128, steps = steps_of<WAVES>(chunks, U);
+  const int chunks = a.H / 128, steps = steps_of(chunks, kWaves, U);
   const int tiles = a.I / COLS, items = plan.jobs * tiles;
   const int64_t panel = 2 * (int64_t)a.I * a.H;
   const auto xb = buffer(a.x, (int64_t)a.T * a.H);
@@ -254,15 +251,15 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_moe_up(ExpertArgs a) {
     xrow = there ? t * (uint32_t)a.H + fg * 16 : kNoRow;
     srow = there ? t * 4 : kNoRow;
     const float* sc = a.s13 + (int64_t)job.expert * (2 * a.I / 128) * chunks;
-    next_g = lane_scale<WAVES>(sc + (int64_t)(col0 / 128) * chunks, chunks);
-    next_u = lane_scale<WAVES>(sc + (int64_t)((a.I + col0) / 128) * chunks, chunks);
+    next_g = lane_scale(sc + (int64_t)(col0 / 128) * chunks, chunks);
+    next_u = lane_scale(sc + (int64_t)((a.I + col0) / 128) * chunks, chunks);
   };
   struct Chunk {
     u32x4 w0[NC], w1[NC], x0, x1;
     float sx;
   } c[U];
   auto fetch = [&](Chunk& k) {
-    const int kb = wave + step * WAVES;
+    const int kb = wave + step * kWaves;
     const uint32_t at = kb < chunks ? (uint32_t)kb * 128 : kNoChunk;
     const uint32_t sat = kb < chunks ? (uint32_t)(kb * a.T * 4) : kNoChunk;
 #pragma unroll
@@ -289,11 +286,11 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_moe_up(ExpertArgs a) {
     const Job job = plan.at(item / tiles);
     const int col0 = item % tiles * COLS;
     leave(acc, red);
-    for (int i = threadIdx.x; i < 16 * COLS; i += 64 * WAVES) {
+    for (int i = threadIdx.x; i < 16 * COLS; i += kThreads) {
       const int m = i / COLS, c = i % COLS;
       if (m >= job.n) break;
-      const float g = total<WAVES, NC>(red, c / 16, m, c % 16);
-      const float u = COLS < 16 ? total<WAVES, NC>(red, 0, m, 8 + c) : total<WAVES, NC>(red, NC / 2 + c / 16, m, c % 16);
+      const float g = total<NC>(red, c / 16, m, c % 16);
+      const float u = COLS < 16 ? total<NC>(red, 0, m, 8 + c) : total<NC>(red, NC / 2 + c / 16, m, c % 16);
       const float v = plan.weight[job.start + m] * (g / (1.0f + expf(-g))) * u;
       const __bf16 hi = (__bf16)v, lo = (__bf16)(v - (float)hi);
       const int64_t at = (int64_t)(job.start + m) * a.I + place_of(col0 + c);
@@ -356,12 +353,13 @@ __global__ __launch_bounds__(kThreads, 3) void k_moe_down(ExpertArgs a) {
   __shared__ __align__(16) float red[KS > 1 ? KS * NC * 256 : 1];
   const Plan plan = load_plan(a, lds);
   const int lane = threadIdx.x % 64, fr = lane % 16, fg = lane / 16;
-  const int chunks = a.I / 128, steps = steps_of<KS>(chunks, U), part = wave_id() % KS;
+  const int chunks = a.I / 128, steps = steps_of(chunks, KS, U), part = wave_id() % KS;
   const int tiles = a.H / COLS, items = plan.jobs * tiles, stride = gridDim.x * (kWaves / KS);
   const int64_t panel = (int64_t)a.H * a.I, acts = (int64_t)a.T * a.topk * a.I * 2;
   const auto hb = buffer(a.hi, acts), lb = buffer(a.lo, acts);
 
-  int item = blockIdx.x * (kWaves / KS) + wave_id() / KS, ahead = item, step = 0;
+  // (the first item of every workgroup before the second of any)
+  int item = wave_id() / KS * gridDim.x + blockIdx.x, ahead = item, step = 0;
   if (item >= items) return;
   auto wb = buffer(a.w2, 0);
   uint32_t wrow[NC], arow;
@@ -427,7 +425,7 @@ __global__ __launch_bounds__(kThreads, 3) void k_moe_down(ExpertArgs a) {
         const int m = i / COLS, c = i % COLS;
         if (m >= job.n) break;
         const int64_t place = plan.row[job.start + m] & 0xFFFF;
-        out[place * a.H + c] = total<KS, NC>(red, c / 16, m, c % 16);
+        out[place * a.H + c] = total<NC>(red, c / 16, m, c % 16);
       }
       __syncthreads();
     }
@@ -632,7 +630,7 @@ constexpr int kUpStage = 2 * kPiece * (64 * 128 + 66 * 4);   // bytes, for 64 ro
 // other, for their accumulators.
 __global__ __launch_bounds__(kThreads, 2) void k_moe_up_wide(ExpertArgs a) {
   extern __shared__ __align__(16) uint32_t lds[];
-  const Plan plan = make_plan<kWaves>(a, lds + kUpStage / 4, 64);
+  const Plan plan = make_plan(a, lds + kUpStage / 4, 64);
   save_plan(a, plan);
   const int tiles = a.I / 128, units = plan.jobs * tiles;
   const Share share = share_of(blockIdx.x, units);
@@ -856,7 +854,7 @@ unsigned grid_of(const ExpertArgs& a, int tiles, int per_cu) {
 
 template <int COLS>
 void launch_up(const ExpertArgs& a, hipStream_t stream) {
-  k_moe_up<COLS, kWaves, 4><<<grid_of(a, a.I / COLS, 4), kThreads, plan_bytes(a), stream>>>(a);
+  k_moe_up<COLS><<<grid_of(a, a.I / COLS, 4), kThreads, plan_bytes(a), stream>>>(a);
 }
 
 template <int COLS, int KS>
@@ -869,17 +867,17 @@ void launch_down(const ExpertArgs& a, hipStream_t stream) {
 // Kernel times in us of both sides, by (tokens, experts, topk, H, I):
 //   up, 8 columns against 16: (1, 2, 2, 6400, 256) 9.6 / 12.4, (1, 48, 5, 1792, 384)
 //     7.6 / 8.4, (4, 64, 1, 2048, 768) 8.4 / 8.4, (3, 128, 5, 4224, 768) 25.3 / 24.0
-//   down, one wave per item against four: (1, 32, 8, 7168, 2048) 24.5 / 26.5,
-//     (35, 32, 5, 4992, 256) 14.8 / 23.6, (16, 32, 8, 7168, 2048) 98.9 / 92.3; of few
-//     items (39, 32, 5, 1408, 2048) 29.6 / 25.0, (1, 4, 2, 7168, 4096) 39.0 / 15.6
+//   down, 64 columns, one wave per item against four: (1, 32, 8, 7168, 2048) 25.0 /
+//     26.6, (35, 32, 5, 4992, 256) 13.3 / 23.6, (39, 32, 5, 1408, 2048) 24.5 / 24.7; of
+//     few items (2, 16, 4, 4096, 1024) 13.1 / 10.3, (1, 4, 2, 7168, 4096) 39.2 / 15.7
 //   down, four waves, 64 columns against 32: (58, 32, 4, 1024, 1024) 12.1 / 14.4,
-//     (4, 64, 1, 2048, 768) 6.2 / 5.2; 32 against 16: the same 5.2 / 6.0, (1, 8, 2,
+//     (4, 64, 1, 2048, 768) 6.6 / 5.8; 32 against 16: the same 5.2 / 6.0, (1, 8, 2,
 //     1024, 512) 4.4 / 4.1
 ExpertTile narrow_tile(const ExpertArgs& a) {
   const int experts = std::min(a.E, a.T * a.topk);   // that may have rows
   const int up = experts * (a.I / 16) < 200 ? 8 : 16;
   const int items = experts * (a.H / 64);
-  if (items >= 800 && (a.I <= 512 || a.T * a.topk < 4 * experts)) return {16, up, 64, 1};
+  if (items >= 700) return {16, up, 64, 1};
   if (a.I <= 256) return {16, up, 32, 1};
   return {16, up, items >= 250 ? 64 : items > 64 ? 32 : 16, 4};
 }

@@ -128,7 +128,7 @@ def test_experts_exactly(T, H, I, E, topk):
 # Every kernel, pinned: rows per pass, columns of the two products, waves that share the second's.
 @pytest.mark.parametrize("tile,T,H,I,E,topk", [
     ((16, 8, 16, 4), 1, 128, 1152, 9, 2), ((16, 8, 32, 1), 3, 2048, 256, 9, 1), ((16, 8, 32, 4), 2, 1152, 384, 9, 3),
-    ((16, 16, 32, 4), 40, 256, 1152, 40, 2), ((16, 16, 64, 4), 3, 2048, 384, 40, 4), ((16, 16, 64, 4), 50, 1024, 640, 60, 6),
+    ((16, 16, 32, 4), 40, 256, 1152, 40, 2), ((16, 16, 64, 4), 3, 2048, 384, 40, 4), ((16, 16, 64, 4), 50, 1024, 640, 40, 6),
     ((16, 16, 64, 1), 4, 2176, 640, 30, 6), ((16, 16, 64, 1), 60, 4096, 128, 100, 2),
     # many rows: halves of units alone; whole units of the first product, of the second (its last one half empty); up to
     # 16, 32 and 64 rows each, and more

@@ -150,7 +150,7 @@ def test_experts_tile(lib):
     assert tile(31, 7168, 2048, 32, 8)[0] == tile(36, 2816, 256, 4, 3)[0] == tile(128, 128, 128, 63, 16)[0] == 16
     # one wave per item, or four; narrower items where they are few
     assert tile(1, 7168, 2048, 32, 8) == (16, 16, 64, 1) and tile(35, 4992, 256, 32, 5) == (16, 16, 64, 1)
-    assert tile(16, 7168, 2048, 32, 8) == (16, 16, 64, 4) and tile(1, 7168, 4096, 4, 2) == (16, 16, 32, 4)
+    assert tile(2, 4096, 1024, 16, 4) == (16, 16, 64, 4) and tile(1, 7168, 4096, 4, 2) == (16, 16, 32, 4)
     assert tile(1, 1024, 512, 8, 2) == (16, 8, 16, 4) and tile(1, 1024, 256, 8, 2) == (16, 8, 32, 1)
     from fp8_block_scaled_04_amd import fp8bs as fb
     assert fb.moe_experts_tile(1, 7168, 2048, 32, 8) == (16, 16, 64, 1)
