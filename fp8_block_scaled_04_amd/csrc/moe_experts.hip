@@ -790,28 +790,26 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_down_wide(ExpertArgs a) {
 
 // ---- the sum over a token's experts ----
 
-// Bit c: place c of token t has a row (its id is inside, and stands no further
-// left).  The same for the whole wave.
-__device__ __forceinline__ uint32_t places_with_rows(const ExpertArgs& a, int t) {
-  const int lane = threadIdx.x % 64;
-  const int id = lane < a.topk ? a.ids[t * a.topk + lane] : -1;
-  bool counts = (uint32_t)id < (uint32_t)a.E;
-  for (int c = 0; c < a.topk; ++c) counts = counts && !(c < lane && __builtin_amdgcn_readlane(id, c) == id);
-  return (uint32_t)__builtin_amdgcn_ballot_w64(counts);
-}
-
-// out[t] = the rows of token t's places added up in turn.  (Places without a row
-// are read, inside the workspace, and left out.)
+// out[t] = the rows of token t's places added up in turn.  A place has a row where
+// its id is inside and stands no further left; the others are read too (inside the
+// workspace; that way no read waits for the ids) and left out.
 __global__ __launch_bounds__(kThreads) void k_moe_join(ExpertArgs a) {
-  const int t = blockIdx.y, h0 = (blockIdx.x * kThreads + threadIdx.x) * 4, h = min(h0, a.H - 4);
-  v4f v{0.0f, 0.0f, 0.0f, 0.0f};
+  const int t = blockIdx.y, h0 = (blockIdx.x * kThreads + threadIdx.x) * 4, h = min(h0, a.H - 4), lane = threadIdx.x % 64;
+  const int id = lane < a.topk ? a.ids[t * a.topk + lane] : -1;
   const v4f* from = reinterpret_cast<const v4f*>(a.part + (int64_t)t * a.topk * a.H + h);
   const int step = a.H / 4;
-  const uint32_t there = places_with_rows(a, t);
-  for (int c0 = 0; c0 < a.topk; c0 += 8) {           // eight rows in flight (16 at most)
-    v4f r[8];
+  v4f r[8];
+  auto fetch = [&](int c0) {                         // eight in flight, of at most 16
 #pragma unroll
     for (int c = 0; c < 8; ++c) r[c] = from[min(c0 + c, a.topk - 1) * step];
+  };
+  fetch(0);
+  bool counts = (uint32_t)id < (uint32_t)a.E;
+  for (int c = 0; c < a.topk; ++c) counts = counts && !(c < lane && __builtin_amdgcn_readlane(id, c) == id);
+  const uint32_t there = (uint32_t)__builtin_amdgcn_ballot_w64(counts);
+  v4f v{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int c0 = 0; c0 < a.topk; c0 += 8) {
+    if (c0) fetch(c0);
 #pragma unroll
     for (int c = 0; c < 8; ++c)
       if (there >> (c0 + c) & 1) v += r[c];
