@@ -752,12 +752,16 @@ def rms_norm_quantize(x, weight, eps: float = 1e-6, residual=None, pow2: bool = 
     return (q, s, h, rstd, y) if return_y else (q, s, h, rstd)
 
 
-@functools.lru_cache(maxsize=4096)
-def rms_norm_backward_workspace_bytes(M: int, K: int) -> int:
-    """Workspace bytes of rms_norm_backward for [M][K]."""
+@functools.lru_cache(maxsize=4096)                      # (a pure function of sizes; the call costs 1 us)
+def _norm_back_bytes(M, K):
     out = ctypes.c_int64(0)
     _check(_norm_back_ws(M, K, ctypes.byref(out)), "rms_norm_backward_workspace")
     return int(out.value)
+
+
+def rms_norm_backward_workspace_bytes(M: int, K: int) -> int:
+    """Workspace bytes of rms_norm_backward for [M][K]."""
+    return _norm_back_bytes(M, K)
 
 
 def rms_norm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, accumulate: bool = False, workspace=None):
@@ -786,7 +790,7 @@ def rms_norm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, accum
         dweight = rstd.new_empty((K,))
     else:
         _shaped(dweight, "dweight", torch.float32, (K,), dev)
-    workspace, ws, ws_bytes = _workspace(workspace, rms_norm_backward_workspace_bytes(M, K), dev)
+    workspace, ws, ws_bytes = _workspace(workspace, _norm_back_bytes(M, K), dev)
     _launch(dev, _norm_back, "rms_norm_backward", dy.data_ptr(), h.data_ptr(), rstd.data_ptr(), weight.data_ptr(), code,
             dh.data_ptr() if dh is not None else None, M, K, dx.data_ptr(), dweight.data_ptr(), 1 if accumulate else 0,
             ws, ws_bytes)
@@ -832,13 +836,17 @@ def moe_route_backward(logits, ids, dweights, renormalize: bool = True):
 
 
 @functools.lru_cache(maxsize=4096)
-def moe_experts_workspace_bytes(T: int, H: int, I: int, E: int, topk: int) -> int:
-    """Workspace bytes of moe_experts for T tokens of width H, E experts of
-    inner width I."""
+def _experts_bytes(T, H, I, E, topk):
     _fits(E, topk)
     out = ctypes.c_int64(0)
     _check(_experts_ws(T, H, I, E, topk, ctypes.byref(out)), "moe_experts_workspace")
     return int(out.value)
+
+
+def moe_experts_workspace_bytes(T: int, H: int, I: int, E: int, topk: int) -> int:
+    """Workspace bytes of moe_experts for T tokens of width H, E experts of
+    inner width I."""
+    return _experts_bytes(T, H, I, E, topk)
 
 
 def moe_experts_tile(T: int, H: int, I: int, E: int, topk: int):
@@ -882,7 +890,7 @@ def moe_experts(x, sx, ids, weights, w13, s13, w2, s2, out_dtype=torch.bfloat16,
         out = sx.new_empty((T, H), dtype=out_dtype)
     else:
         _shaped(out, "out", out_dtype, (T, H), dev)
-    workspace, ws, ws_bytes = _workspace(workspace, moe_experts_workspace_bytes(T, H, I, E, topk), dev)
+    workspace, ws, ws_bytes = _workspace(workspace, _experts_bytes(T, H, I, E, topk), dev)
     _launch(dev, _experts, "moe_experts", x.data_ptr(), sx.data_ptr(), ids.data_ptr(), weights.data_ptr(),
             w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), out.data_ptr(), T, H, I, E, topk, code, ws,
             ws_bytes)

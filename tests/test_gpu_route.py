@@ -37,7 +37,8 @@ def distance(x):
     """top - x of the logits that count, 0 elsewhere."""
     live = np.where(np.isfinite(x), x, -np.inf)
     top = live.max(1, keepdims=True)
-    return np.where(np.isfinite(x) & np.isfinite(top), top - x, 0.0)
+    known = np.isfinite(x) & np.isfinite(top)
+    return np.where(known, np.where(known, top, 0.0) - np.where(known, x, 0.0), 0.0)
 
 
 def check(x, dev, topk, renorm, seed=0):
