@@ -6,6 +6,10 @@
 // (up to 256 experts and 16 places): lane l has experts 16 n + l, four tokens share
 // each instruction, and a maximum over 16 lanes is four DPP steps.  Otherwise a
 // wave holds one token, expert 64 n + lane at v[n] of a lane.
+//
+// 16384 tokens, 256 experts, 8 places: 10.4 us (BF16 logits, 9 MB), with one token
+// per wave 14.7; the gradient 8.1 us (FP32, 18 MB), with one token per wave 12.6.
+// 64 tokens: 5.1 us, all of it latency.
 #include <algorithm>
 #include <type_traits>
 
