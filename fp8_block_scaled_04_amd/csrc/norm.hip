@@ -118,7 +118,7 @@ __global__ __launch_bounds__(1024) void k_rms_norm(NormArgs a) {
       float amax = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        h[v][e] = h[v][e] * rstd * w[v][e];
+        h[v][e] = h[v][e] * w[v][e] * rstd;             // (h w is exact for BF16 weights)
         amax = fmaxf(amax, __builtin_fabsf(h[v][e]));
       }
       if (a.y) put_piece<true>(static_cast<uint16_t*>(a.y) + at, p, pack8(h[v]));

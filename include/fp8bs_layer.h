@@ -29,7 +29,7 @@ enum { FP8BS_ROUTE_RENORM = 4u };
  * Residual addition, RMS norm and 1x128 quantization:
  *   h    = RN_bf16(x + residual)            (h = x where residual is NULL)
  *   rstd = 1 / sqrt(mean over k of h[m][k]^2 + eps)
- *   y    = h rstd weight[k]                 in FP32
+ *   y    = h weight[k] rstd                 in FP32
  *   q, s = the 1x128 quantization of y (the rule of fp8bs.h), as the A operand
  *          of the GEMMs takes it
  *   x, residual : BF16 [M][K]
