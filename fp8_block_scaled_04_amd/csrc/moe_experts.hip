@@ -893,10 +893,15 @@ ExpertTile narrow_tile(const ExpertArgs& a) {
 // Whether an expert has many rows, were they spread evenly, and the chip is full
 // with fewer and larger shares.  Both products, wide against narrow: (32, 32, 8,
 // 7168, 2048) 256 / 267 us, (24, 32, 8, 7168, 2048) 255 / 257, (64, 8, 4, 4096,
-// 1536) 61 / 77, (32, 8, 8, 2048, 512) 26 / 24, (36, 4, 3, 2816, 256) 26 / 15.
+// 1536) 61 / 77, (32, 8, 8, 2048, 512) 26 / 24, (36, 4, 3, 2816, 256) 26 / 15.  With
+// 64 rows and more the narrow kernels read an expert four times and more: (128, 2, 2,
+// 7168, 2048) 82 / 169, (128, 1, 1, 7168, 2048) 76 / 98, (128, 2, 2, 4096, 512) 41 / 43,
+// but (100, 1, 1, 512, 2048) 39 / 21.
 bool wide(const ExpertArgs& a) {
   const int experts = std::min(a.E, a.T * a.topk);
-  return a.T * a.topk >= 8 * experts && experts * (a.I / 128) >= 64;
+  const int places = a.T * a.topk;
+  return (places >= 8 * experts && experts * (a.I / 128) >= 64) ||
+         (places >= 64 * experts && (int64_t)experts * a.H * a.I >= 1 << 22);
 }
 
 }  // namespace

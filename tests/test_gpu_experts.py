@@ -135,7 +135,7 @@ def test_experts_exactly(T, H, I, E, topk):
     ((64, 128, 256, 4), 64, 256, 384, 24, 8), ((64, 128, 256, 4), 64, 128, 1024, 64, 8),
     ((64, 128, 256, 4), 64, 1920, 128, 64, 8), ((64, 128, 256, 4), 128, 128, 1024, 64, 16),
     ((64, 128, 256, 4), 128, 1920, 128, 64, 16), ((64, 128, 256, 4), 128, 384, 640, 16, 8),
-    ((64, 128, 256, 4), 128, 640, 1024, 16, 16)])
+    ((64, 128, 256, 4), 128, 640, 1024, 16, 16), ((64, 128, 256, 4), 128, 4096, 512, 2, 2)])
 def test_experts_exactly_on_every_kernel(tile, T, H, I, E, topk):
     assert fb.moe_experts_tile(T, H, I, E, topk) == tile
     check_exact(exact_case(T, H, I, E, topk, seed=T + H + I))

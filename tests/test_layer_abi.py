@@ -147,7 +147,8 @@ def test_experts_tile(lib):
     assert f(3, 256, 128, 4, 2, p, None, p, p) == NULL
     # many rows per expert that fill the chip; too few columns or rows for that
     assert tile(64, 7168, 2048, 32, 8) == tile(32, 7168, 2048, 32, 8) == tile(64, 256, 384, 24, 8) == (64, 128, 256, 4)
-    assert tile(31, 7168, 2048, 32, 8)[0] == tile(36, 2816, 256, 4, 3)[0] == tile(128, 128, 128, 63, 16)[0] == 16
+    assert tile(128, 7168, 2048, 1, 1) == tile(128, 4096, 512, 2, 2) == (64, 128, 256, 4)
+    assert tile(100, 512, 2048, 1, 1)[0] == tile(31, 7168, 2048, 32, 8)[0] == tile(36, 2816, 256, 4, 3)[0] == tile(128, 128, 128, 63, 16)[0] == 16
     # one wave per item, or four; narrower items where they are few
     assert tile(1, 7168, 2048, 32, 8) == (16, 16, 64, 1) and tile(35, 4992, 256, 32, 5) == (16, 16, 64, 1)
     assert tile(2, 4096, 1024, 16, 4) == (16, 16, 64, 4) and tile(1, 7168, 4096, 4, 2) == (16, 16, 32, 4)
