@@ -163,6 +163,11 @@ def test_experts_that_stand_twice_or_outside(places):
     assert (got[1] == 0).all()
 
 
+def test_experts_more_places_than_experts():
+    ids = np.random.default_rng(3).integers(0, 2, (20, 16))
+    check_exact(exact_case(20, 128, 128, 2, 16, seed=2, ids=ids))
+
+
 def test_experts_all_tokens_one_expert():
     ids = np.full((128, 1), 6)
     check_exact(exact_case(128, 128, 128, 7, 1, seed=6, ids=ids))

@@ -164,6 +164,43 @@ def test_large_rows_pass_32_bits():
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("pow2", [False, True])
+def test_norm_feeds_the_gemms(pow2):
+    # codes and scales go into the dense GEMM as they are: its product of their values, within the GEMMs' tolerance
+    from oracle import gemm
+    from tests.gpu_util import ABS_RMS, REL, codes_host
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    x = torch.randn(37, 1024, generator=gen, device=DEV).bfloat16()
+    w = (0.02 * torch.randn(256, 1024, generator=gen, device=DEV)).bfloat16()
+    q, s, _, _ = fb.rms_norm_quantize(x, torch.rand(1024, generator=gen, device=DEV), pow2=pow2)
+    wq, ws = fb.quantize_128x128(w, pow2=pow2)
+    got = fb.gemm(q, s, wq, ws, out_dtype=torch.float32, pow2_scales=pow2).cpu().numpy().astype(np.float64)
+    ref = gemm.gemm_f64(codes_host(q), s.cpu().numpy(), codes_host(wq), ws.cpu().numpy())
+    assert np.all(np.abs(got - ref) <= REL * np.abs(ref) + ABS_RMS * np.sqrt(np.mean(ref ** 2)))
+
+
+def test_norm_without_its_optional_outputs():
+    # through the C ABI: rstd and y NULL leave the others as they are
+    from fp8_block_scaled_04_amd import fp8bs
+    x, w = torch.randn(9, 384, device=DEV).bfloat16(), torch.rand(384, device=DEV)
+    want = fb.rms_norm_quantize(x, w)
+    q, s = torch.empty_like(want[0]), torch.empty_like(want[1])
+    status = fp8bs._norm(x.data_ptr(), None, w.data_ptr(), 1, 1e-6, 9, 384, None, None, q.data_ptr(), s.data_ptr(), None,
+                         0, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert status == 0 and same([q, s], want[:2])
+
+
+def test_gradients_accumulate_over_parts():
+    # two halves of a batch into one dweight: the sum of theirs
+    x = torch.randn(60, 256, device=DEV).bfloat16()
+    w, rstd = torch.rand(256, device=DEV), torch.rand(60, device=DEV)
+    parts = [fb.rms_norm_backward(x[i:i + 30], x[i:i + 30], rstd[i:i + 30], w) for i in (0, 30)]
+    acc = torch.zeros(256, device=DEV)
+    dx = [fb.rms_norm_backward(x[i:i + 30], x[i:i + 30], rstd[i:i + 30], w, dweight=acc, accumulate=True)[0] for i in (0, 30)]
+    assert same(dx, [p[0] for p in parts]) and torch.equal(acc, parts[0][1] + parts[1][1])
+
+
 def test_arguments_keep_their_values():
     w = expert_dev(expert_case(5, 256, 128, 4, 2, seed=3))
     before = [t.clone() for t in w]
