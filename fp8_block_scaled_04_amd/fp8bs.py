@@ -708,8 +708,8 @@ def _device_of(t, name):
 
 def _shaped(t, name, dtype, shape, dev):
     """A dense tensor of this type and shape on GPU `dev`."""
-    _on(t, name, dtype, len(shape), dev)
-    if t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _on(t, name, dtype, len(shape), dev)
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -798,10 +798,10 @@ def rms_norm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, accum
 
 
 def moe_route(logits, topk: int, renormalize: bool = True):
-    """The topk experts of each token by logits [T][E] (BF16 or FP32), largest
-    first (ties: the lowest index), and their softmax weights: over the chosen
-    ones (renormalize) or over all.  An expert of logit -inf or NaN is never
-    chosen; places without one get id -1 and weight 0.
+    """The topk (at most 64) experts of each token by logits [T][E] (BF16 or FP32,
+    E at most 1024), largest first (ties: the lowest index), and their softmax
+    weights: over the chosen ones (renormalize) or over all.  An expert of logit
+    -inf or NaN is never chosen; places without one get id -1 and weight 0.
     -> (ids int32 [T][topk], weights FP32 [T][topk])"""
     dev = _device_of(logits, "logits")
     code = _type_code(logits, "logits")
