@@ -50,13 +50,15 @@ __device__ __forceinline__ void weight8(float (&f)[8], const void* weight, bool 
   }
 }
 
-// Sum over the workgroup, the same order on every lane and call.  `red` has 16
-// floats of its own for each of two calls in a row: a wave may still read the
-// last call's while another writes this one's.
+// Sum over a row's lanes (threadIdx.x; a workgroup has blockDim.y rows), the same
+// order on every lane and call.  `red` has 16 floats of its own for each of two
+// calls in a row: a wave may still read the last call's while another writes this
+// one's.
 __device__ __forceinline__ float group_sum(float v, float* red) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
   const int waves = blockDim.x / 64;
+  red += threadIdx.y * waves;
   if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = v;
   __syncthreads();
   float t = 0.0f;
@@ -134,14 +136,21 @@ __global__ __launch_bounds__(1024) void k_rms_norm(NormArgs a) {
   }
 }
 
-// Row group g takes rows g, g + groups, ...; its sums for dweight stay in
+// Row group g takes rows g, g + groups, ..., or with MANY blockDim.y rows of each
+// such run at once (narrow rows: kBackLanes below); its sums for dweight stay in
 // registers and leave as one partial row.  Two workgroups of seven waves per CU
 // (7168 columns) cover each other's waits; the next row fetched ahead by one
 // workgroup per CU (its registers leave no room for two) took 99 us against 84.
-template <int V>
-__global__ __launch_bounds__(1024) void k_rms_norm_back(NormBackArgs a) {
+// Narrow rows, one at a time, leave a CU two to eight waves: 8192 rows of 512,
+// 1024, 1536 and 2048 took 24.4, 28.7, 31.5 and 33.5 us, up to 512 lanes at work
+// 12.7, 17.8, 25.5 and 28.5 (up to 1024: 14.6, 21.3, 24.1, 33.7; up to 256: 13.7,
+// 21.1, 31.2, 33.2).
+constexpr int kBackLanes = 512;
+template <int V, bool MANY>
+__global__ __launch_bounds__(MANY ? kBackLanes : 1024) void k_rms_norm_back(NormBackArgs a) {
   __shared__ float red[2][16];
   const int pieces = a.K / 8, threads = blockDim.x, tid = threadIdx.x;
+  const int rows = MANY ? blockDim.y : 1, row = MANY ? threadIdx.y : 0;
   float w[V][8], dw[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -151,20 +160,21 @@ __global__ __launch_bounds__(1024) void k_rms_norm_back(NormBackArgs a) {
     if (p < pieces) weight8(w[v], a.weight, a.weight_f32, p);
   }
   int turn = 0;
-  for (int64_t m = blockIdx.x; m < a.M; m += a.groups, turn ^= 1) {
-    const int64_t at = m * a.K;
+  for (int64_t m0 = (int64_t)blockIdx.x * rows; m0 < a.M; m0 += (int64_t)a.groups * rows, turn ^= 1) {
+    const int64_t m = m0 + row, at = m * a.K;
+    const bool in = !MANY || m < a.M;                // (every wave takes part in the row sum's barrier)
     u32x4 dyp[V], hp[V], dhp[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = v * threads + tid;
       dyp[v] = hp[v] = dhp[v] = u32x4{0u, 0u, 0u, 0u};
-      if (p < pieces) {
+      if (p < pieces && in) {
         dyp[v] = piece(static_cast<const uint16_t*>(a.dy) + at, p);
         hp[v] = piece(static_cast<const uint16_t*>(a.h) + at, p);
         if (a.dh) dhp[v] = piece(static_cast<const uint16_t*>(a.dh) + at, p);
       }
     }
-    const float rstd = a.rstd[m];
+    const float rstd = in ? a.rstd[m] : 0.0f;
     float g[V][8], n[V][8], dot = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -182,12 +192,24 @@ __global__ __launch_bounds__(1024) void k_rms_norm_back(NormBackArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = v * threads + tid;
-      if (p >= pieces) break;
+      if (p >= pieces || !in) break;
       float d[8];
       unpack8(d, dhp[v]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) d[e] = __builtin_fmaf(rstd, __builtin_fmaf(-n[v][e], mean, g[v][e]), d[e]);
       put_piece<false>(static_cast<uint16_t*>(a.dx) + at, p, pack8(d));
+    }
+  }
+  if (MANY) {                                        // the rows' sums, joined in their order
+    __shared__ float join[8][kBackLanes];
+    const int at = row * threads + tid;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) join[e][at] = dw[0][e];
+    __syncthreads();
+    if (row) return;
+    for (int o = 1; o < rows; ++o) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dw[0][e] += join[e][o * threads + tid];
     }
   }
   float* part = a.part + (int64_t)blockIdx.x * a.K;
@@ -256,8 +278,11 @@ hipError_t launch_rms_norm(const NormArgs& a, bool pow2, hipStream_t stream) {
 hipError_t launch_rms_norm_back(const NormBackArgs& a, hipStream_t stream) {
   if (a.groups) {
     const Shape s = shape_of(a.K);
-    const auto k = s.v == 1 ? k_rms_norm_back<1> : k_rms_norm_back<2>;
-    k<<<a.groups, s.threads, 0, stream>>>(a);
+    // rows at once: as many as the lanes allow and every group still has
+    int rows = 1;
+    while (s.v == 1 && 2 * rows * s.threads <= kBackLanes && 2 * rows * a.groups <= a.M) rows *= 2;
+    const auto k = rows > 1 ? k_rms_norm_back<1, true> : s.v == 1 ? k_rms_norm_back<1, false> : k_rms_norm_back<2, false>;
+    k<<<a.groups, dim3(s.threads, rows), 0, stream>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
   }
   k_rms_norm_dweight<<<a.K / 32, 8 * kRuns, 0, stream>>>(a.part, a.groups, a.K, a.dweight, a.accumulate);

@@ -164,6 +164,29 @@ def test_norm_backward(m, k, with_dh, kind):
         assert torch.equal(fb.rms_norm_backward(bf16_dev(dy), args[1], args[2], wdev, dh=dhd, dx=dhd)[0], dx)
 
 
+@pytest.mark.parametrize("m,k", [(1023, 2048), (1025, 2048), (2053, 1024), (4095, 512), (4097, 512), (4103, 640), (9001, 128)])
+def test_norm_backward_of_many_narrow_rows(m, k):
+    # several rows of a workgroup at once, the last run of rows cut short.  A row's gradient depends on nothing else:
+    # bit for bit that of the same row in a call of a few.  dweight within the roundings of test_norm_backward (a lane's
+    # rows, then the lanes' sums, are no longer chain than the group's rows)
+    rng = np.random.default_rng(m * 3 + k)
+    w, raw = weight_of(rng, k, "bf16")
+    h, dy, dh = rows_bits(rng, m, k), rows_bits(rng, m, k, 1e-3), rows_bits(rng, m, k, 1e-3)
+    rstd = layer.norm(h, None, w, 1e-6)[1].astype(np.float32)
+    out = torch.full((m + 2, k), -7.0, dtype=torch.bfloat16, device=DEV)
+    dx, dw = fb.rms_norm_backward(bf16_dev(dy), bf16_dev(h), f32_dev(rstd), bf16_dev(raw), dh=bf16_dev(dh), dx=out[:m])
+    assert (out[m:] == -7).all()
+    dx_ref, dw_ref = layer.norm_backward(dy, h, rstd, w, dh)
+    bx, bw = back_bound(dy, h, rstd.astype(np.float64), w, dh)
+    assert np.all(np.abs(dx.float().cpu().numpy() - dx_ref) <= 2.0 ** -8 * np.abs(dx_ref) + bx * 1.01 + 2.0 ** -134)
+    groups = fb.rms_norm_backward_workspace_bytes(m, k) // (4 * k)
+    chain = -(-m // groups) + -(-groups // 16) + 16 + 3
+    assert np.all(np.abs(dw.cpu().numpy() - dw_ref) <= chain * bw * 1.01)
+    few = slice(m - 37, m)
+    assert torch.equal(fb.rms_norm_backward(bf16_dev(dy[few]), bf16_dev(h[few]), f32_dev(rstd[few]), bf16_dev(raw),
+                                            dh=bf16_dev(dh[few]))[0], dx[m - 37:])
+
+
 def test_norm_backward_of_no_rows():
     e = torch.empty(0, 256, dtype=torch.bfloat16, device=DEV)
     w = torch.ones(256, device=DEV)
