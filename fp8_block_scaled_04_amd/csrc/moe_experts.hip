@@ -3,7 +3,8 @@
 //   k_moe_up    per expert, g and u = w13 x, then the weighted activations
 //               weight g / (1 + exp(-g)) u, as two BF16 parts
 //   k_moe_down  w2 times them
-//   k_moe_join  the sums of each token's rows
+//   k_moe_join  the sums of each token's rows (few weights: k_moe_down_whole takes
+//               its place and that of k_moe_down)
 //
 // Bound by HBM: every expert that has a token is read once, 3 H I codes for at
 // most a few dozen rows of products.  So weights go from memory straight to the
@@ -52,6 +53,15 @@ __device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t r, uint32_t at) {
 }
 __device__ __forceinline__ v8i join(u32x4 a, u32x4 b) {
   return v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+// The bits of 16 lanes joined.
+__device__ __forceinline__ uint32_t row16_or(uint32_t v) {
+  v |= (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);    // quad_perm [1, 0, 3, 2]
+  v |= (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true);    // quad_perm [2, 3, 0, 1]
+  v |= (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true);   // row_half_mirror
+  v |= (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true);   // row_mirror
+  return v;
 }
 
 // This wave's number, on the scalar unit.
@@ -175,7 +185,7 @@ __device__ __forceinline__ void save_plan(const ExpertArgs& a, const Plan& p) {
 __device__ __forceinline__ Plan load_plan(const ExpertArgs& a, uint32_t* lds) {
   const int places = a.T * a.topk;
   Plan p{lds, lds + places, nullptr, __builtin_amdgcn_readfirstlane((int)a.image[0])};
-  for (int i = threadIdx.x; i < 2 * places; i += kThreads) lds[i] = a.image[1 + i];
+  for (int i = threadIdx.x; i < 2 * places; i += blockDim.x) lds[i] = a.image[1 + i];
   __syncthreads();
   return p;
 }
@@ -187,6 +197,13 @@ __device__ __forceinline__ Plan load_plan(const ExpertArgs& a, uint32_t* lds) {
 // of 16 columns lie 32 apart, and the rows' 64-byte pieces of a product are whole.
 __device__ __forceinline__ int place_of(int c) {
   return (c & ~63) + ((c >> 3) & 1) * 32 + ((c >> 4) & 3) * 8 + (c & 7);
+}
+
+// Columns h .. h + 3 of the call's result for token t.
+__device__ __forceinline__ void put_out(const ExpertArgs& a, int t, int h, v4f v) {
+  const int64_t at = (int64_t)t * a.H + h;
+  if (a.out_f32) *reinterpret_cast<v4f*>(static_cast<float*>(a.out) + at) = v;
+  else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
 }
 
 // The waves' accumulators of NC fragments, in LDS (kWaves * NC * 256 floats) for
@@ -479,6 +496,87 @@ __global__ __launch_bounds__(kThreads, 3) void k_moe_down(ExpertArgs a) {
       }
     }
   }
+}
+
+// Few tokens (at most 16): all experts of 16 columns of H in one workgroup, a row of
+// the matrix core's result per token, so that the sums over experts stay in its
+// accumulators and nothing is left to k_moe_join.  The waves take the chunks of all
+// jobs in turn.
+constexpr int kWholeWaves = 8;
+__global__ __launch_bounds__(64 * kWholeWaves) void k_moe_down_whole(ExpertArgs a) {
+  constexpr int U = 2;
+  extern __shared__ __align__(16) uint32_t lds[];
+  __shared__ __align__(16) v4f red[kWholeWaves * 64];
+  const Plan plan = load_plan(a, lds);
+  const int lane = threadIdx.x % 64, wave = wave_id(), fr = lane % 16, fg = lane / 16, col0 = blockIdx.x * 16;
+  const int chunks = a.I / 128, units = plan.jobs * chunks;
+  const int64_t panel = (int64_t)a.H * a.I, acts = (int64_t)a.T * a.topk * a.I * 2;
+  const auto hb = buffer(a.hi, acts), lb = buffer(a.lo, acts);
+  const uint32_t wrow = (uint32_t)((col0 + fr) * (int64_t)a.I + fg * 16);
+  struct Chunk {
+    u32x4 w0, w1;
+  } c[U];
+  auto fetch = [&](Chunk& k, int unit) {
+    const int u = min(unit, units - 1), kb = u % chunks;
+    const auto wb = buffer(a.w2 + plan.at(u / chunks).expert * panel, unit < units ? panel : 0);
+    k.w0 = load16(wb, wrow + kb * 128);
+    k.w1 = load16(wb, wrow + kb * 128 + 64);
+  };
+  u32x4 hi[4], lo[4];
+  bool there;                                        // whether token fr has a row of the unit's job
+  float scale;
+  auto fetch_acts = [&](int unit) {
+    const int u = min(unit, units - 1), kb = u % chunks;
+    const Job job = plan.at(u / chunks);
+    uint32_t tokens = fr < job.n ? 1u << (plan.row[job.start + fr] >> 16) : 0u;
+    tokens = row16_or(tokens);
+    there = unit < units && (tokens >> fr & 1);
+    const int r = job.start + __builtin_popcount(tokens & ((1u << fr) - 1));
+    const uint32_t at = there ? (uint32_t)(r * (int64_t)a.I + kb * 128 + fg * 8) * 2 : kNoRow;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      hi[j] = load16(hb, at + j * 64);
+      lo[j] = load16(lb, at + j * 64);
+    }
+    scale = a.s2[((int64_t)job.expert * (a.H / 128) + col0 / 128) * chunks + kb];
+  };
+  const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
+  v4f acc = zero;
+  if (wave < units) {
+    fetch(c[0], wave);
+    fetch_acts(wave);
+#pragma unroll
+    for (int i = 1; i < U; ++i) fetch(c[i], wave + i * kWholeWaves);
+    for (int unit = wave; unit < units; unit += U * kWholeWaves) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int u = unit + i * kWholeWaves;
+        const v8bf b[4] = {to_bf16(c[i].w0.x, c[i].w0.y), to_bf16(c[i].w0.z, c[i].w0.w), to_bf16(c[i].w1.x, c[i].w1.y),
+                           to_bf16(c[i].w1.z, c[i].w1.w)};
+        v4f p = zero;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, hi[j]), p, 0, 0, 0);
+          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, lo[j]), p, 0, 0, 0);
+        }
+        // (a token without a row has zeros times whatever the codes and scales are)
+        const float s = scale;
+        const bool counts = there;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = counts ? __builtin_fmaf(p[e], s, acc[e]) : acc[e];
+        fetch_acts(u + kWholeWaves);
+        fetch(c[i], u + U * kWholeWaves);
+      }
+    }
+  }
+  red[wave * 64 + lane] = acc;
+  __syncthreads();
+  const int m = threadIdx.x / 4, g = threadIdx.x % 4;   // four columns of a token
+  if (m >= a.T) return;
+  v4f v = red[g * 16 + m];
+#pragma unroll
+  for (int w = 1; w < kWholeWaves; ++w) v += red[w * 64 + g * 16 + m];
+  put_out(a, m, col0 + g * 4, v);
 }
 
 // ---- many rows per expert ----
@@ -824,10 +922,7 @@ __global__ __launch_bounds__(kThreads) void k_moe_join(ExpertArgs a) {
     for (int c = 0; c < 8; ++c)
       if (there >> (c0 + c) & 1) v += r[c];
   }
-  if (h0 >= a.H) return;
-  const int64_t at = (int64_t)t * a.H + h;
-  if (a.out_f32) *reinterpret_cast<v4f*>(static_cast<float*>(a.out) + at) = v;
-  else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
+  if (h0 < a.H) put_out(a, t, h, v);
 }
 
 int64_t aligned(int64_t bytes) { return (bytes + 255) / 256 * 256; }
@@ -871,6 +966,19 @@ void launch_down(const ExpertArgs& a, hipStream_t stream) {
   k_moe_down<COLS, KS><<<grid_of(a, groups, 3), kThreads, a.T * a.topk * 8, stream>>>(a);
 }
 
+// Whether so little of w2 is read that the last sum, a kernel of its own with 2 us of
+// its launch, costs more than 16 columns of H per workgroup do.  Calls in a row, in us,
+// k_moe_down_whole against k_moe_down and k_moe_join, by (tokens, experts, topk, H, I):
+// (1, 8, 2, 1024, 512) 16.7 / 18.7, (16, 4, 4, 512, 512) 16.7 / 19.8, (11, 4, 3, 3456, 128)
+// 16.6 / 18.7, (16, 8, 4, 4096, 512) 24.0 / 26.6, (16, 16, 4, 2048, 256) 16.8 / 19.1; but
+// (16, 4, 4, 1024, 1024) 20.2 / 19.2, (16, 16, 4, 1024, 512) 20.9 / 19.4, (1, 8, 8, 2048,
+// 1024) 22.5 / 21.7, (16, 4, 4, 7168, 1024) 39.3 / 32.9, (1, 32, 8, 7168, 2048) 84.7 / 73.6.
+// (Four or 16 waves, or four chunks in flight: none better over these.)
+bool whole(const ExpertArgs& a, int experts) {
+  const int chunks = experts * (a.I / 128) * ((a.H + 4095) / 4096);   // of a CU, with a workgroup on every one
+  return a.T <= 16 && chunks <= (a.H < 2048 ? 16 : 32);
+}
+
 // Narrow items where there are few, so that more workgroups share the reading.
 // Kernel times in us of both sides, by (tokens, experts, topk, H, I):
 //   up, 8 columns against 16: (1, 2, 2, 6400, 256) 9.6 / 12.4, (1, 48, 5, 1792, 384)
@@ -884,6 +992,7 @@ void launch_down(const ExpertArgs& a, hipStream_t stream) {
 ExpertTile narrow_tile(const ExpertArgs& a) {
   const int experts = std::min(a.E, a.T * a.topk);   // that may have rows
   const int up = experts * (a.I / 16) < 200 ? 8 : 16;
+  if (whole(a, experts)) return {16, up, 16, kWholeWaves};
   const int items = experts * (a.H / 64);
   if (items >= 700) return {16, up, 64, 1};
   if (a.I <= 256) return {16, up, 32, 1};
@@ -919,6 +1028,10 @@ hipError_t launch_moe_experts(const ExpertArgs& a, hipStream_t stream) {
   } else {
     if (t.up == 8) launch_up<8>(a, stream);
     else launch_up<16>(a, stream);
+    if (t.waves == kWholeWaves) {
+      k_moe_down_whole<<<a.H / 16, 64 * kWholeWaves, a.T * a.topk * 8, stream>>>(a);
+      return hipGetLastError();
+    }
     if (t.waves == 1 && t.down == 64) launch_down<64, 1>(a, stream);
     else if (t.waves == 1) launch_down<32, 1>(a, stream);
     else if (t.down == 64) launch_down<64, 4>(a, stream);

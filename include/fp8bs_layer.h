@@ -129,7 +129,8 @@ fp8bs_status fp8bs_moe_experts(const uint8_t* x, const float* sx, const int32_t*
 /* Kernels that a fp8bs_moe_experts call of these sizes would run on (host-side
  * query for tests and tuning): rows that one pass over an expert's weights serves
  * (16 or 64), columns of a workgroup in the first and in the second product, and
- * the waves that share them in the second.  HOST pointers. */
+ * the waves that share them in the second (8: those of all experts at once, so
+ * that no sum over experts is left).  HOST pointers. */
 fp8bs_status fp8bs_moe_experts_tile(int64_t T, int64_t H, int64_t I, int32_t E, int32_t topk, int32_t* rows,
                                     int32_t* up_columns, int32_t* down_columns, int32_t* down_waves);
 

@@ -127,9 +127,13 @@ def test_experts_exactly(T, H, I, E, topk):
 
 # Every kernel, pinned: rows per pass, columns of the two products, waves that share the second's.
 @pytest.mark.parametrize("tile,T,H,I,E,topk", [
-    ((16, 8, 16, 4), 1, 128, 1152, 9, 2), ((16, 8, 32, 1), 3, 2048, 256, 9, 1), ((16, 8, 32, 4), 2, 1152, 384, 9, 3),
+    ((16, 8, 16, 4), 1, 128, 1152, 9, 2), ((16, 8, 32, 1), 17, 2048, 256, 9, 1), ((16, 8, 32, 4), 2, 1152, 384, 9, 3),
     ((16, 16, 32, 4), 40, 256, 1152, 40, 2), ((16, 16, 64, 4), 3, 2048, 384, 40, 4), ((16, 16, 64, 4), 50, 1024, 640, 40, 6),
     ((16, 16, 64, 1), 4, 2176, 640, 30, 6), ((16, 16, 64, 1), 60, 4096, 128, 100, 2),
+    # all experts at once: fewer chunks than waves, as many, more; one token, 16; a row for every expert, one expert for all
+    ((16, 8, 16, 8), 1, 128, 128, 1, 1), ((16, 8, 16, 8), 3, 2048, 256, 9, 1), ((16, 8, 16, 8), 16, 128, 128, 16, 16),
+    ((16, 8, 16, 8), 16, 256, 2048, 1, 1), ((16, 16, 16, 8), 2, 2048, 128, 64, 14), ((16, 16, 16, 8), 16, 2304, 1024, 4, 2),
+    ((16, 8, 16, 8), 13, 4224, 640, 3, 2), ((16, 8, 16, 8), 15, 3968, 256, 12, 5),
     # many rows: halves of units alone; whole units of the first product, of the second (its last one half empty); up to
     # 16, 32 and 64 rows each, and more
     ((64, 128, 256, 4), 64, 256, 384, 24, 8), ((64, 128, 256, 4), 64, 128, 1024, 64, 8),
@@ -139,6 +143,20 @@ def test_experts_exactly(T, H, I, E, topk):
 def test_experts_exactly_on_every_kernel(tile, T, H, I, E, topk):
     assert fb.moe_experts_tile(T, H, I, E, topk) == tile
     check_exact(exact_case(T, H, I, E, topk, seed=T + H + I))
+
+
+@pytest.mark.parametrize("T,H,I,E,topk", [(5, 256, 384, 4, 1), (16, 256, 384, 16, 1), (40, 256, 384, 4, 1), (64, 256, 640, 16, 2)])
+@pytest.mark.parametrize("where", ["w2", "s2", "w13"])
+def test_experts_of_others_do_not_matter(T, H, I, E, topk, where):
+    # NaN codes or scales of an expert reach its own tokens and no others
+    w = exact_case(T, H, I, E, topk, seed=T + E)
+    clean = fb.moe_experts(*expert_dev(w), out_dtype=torch.float32)
+    bad = int(w["ids"][T // 2][0])
+    mine = torch.from_numpy((w["ids"] == bad).any(1)).to(DEV)
+    w[where] = w[where].copy()
+    w[where][bad] = np.float32(np.nan) if where == "s2" else 0x7F
+    got = fb.moe_experts(*expert_dev(w), out_dtype=torch.float32)
+    assert got[mine].isnan().all() and torch.equal(got[~mine], clean[~mine])
 
 
 @pytest.mark.parametrize("T,H,I,E,topk", [(64, 256, 512, 20, 8), (128, 128, 1024, 24, 3), (100, 256, 640, 16, 10)])

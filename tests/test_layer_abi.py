@@ -152,7 +152,10 @@ def test_experts_tile(lib):
     # one wave per item, or four; narrower items where they are few
     assert tile(1, 7168, 2048, 32, 8) == (16, 16, 64, 1) and tile(35, 4992, 256, 32, 5) == (16, 16, 64, 1)
     assert tile(2, 4096, 1024, 16, 4) == (16, 16, 64, 4) and tile(1, 7168, 4096, 4, 2) == (16, 16, 32, 4)
-    assert tile(1, 1024, 512, 8, 2) == (16, 8, 16, 4) and tile(1, 1024, 256, 8, 2) == (16, 8, 32, 1)
+    assert tile(1, 128, 1152, 9, 2) == (16, 8, 16, 4) and tile(17, 1024, 256, 8, 2) == (16, 8, 32, 1)
+    # all experts at once where they are small and the tokens few
+    assert tile(1, 1024, 512, 8, 2) == tile(1, 1024, 256, 8, 2) == tile(16, 4096, 256, 8, 4) == (16, 8, 16, 8)
+    assert tile(16, 1024, 512, 8, 4)[3] == tile(1, 7168, 1024, 4, 4)[3] == 4
     from fp8_block_scaled_04_amd import fp8bs as fb
     assert fb.moe_experts_tile(1, 7168, 2048, 32, 8) == (16, 16, 64, 1)
 
