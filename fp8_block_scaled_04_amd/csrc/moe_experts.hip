@@ -987,8 +987,8 @@ bool whole(const ExpertArgs& a, int experts) {
 //     26.6, (35, 32, 5, 4992, 256) 13.3 / 23.6, (39, 32, 5, 1408, 2048) 24.5 / 24.7; of
 //     few items (2, 16, 4, 4096, 1024) 13.1 / 10.3, (1, 4, 2, 7168, 4096) 39.2 / 15.7
 //   down, four waves, 64 columns against 32: (58, 32, 4, 1024, 1024) 12.1 / 14.4,
-//     (4, 64, 1, 2048, 768) 6.6 / 5.8; 32 against 16: the same 5.2 / 6.0, (1, 8, 2,
-//     1024, 512) 4.4 / 4.1
+//     (4, 64, 1, 2048, 768) 6.6 / 5.8; 32 against 16: the same 5.2 / 6.0, (1, 4, 4,
+//     1024, 1408) 5.6 / 5.2, (17, 1, 1, 512, 1024) 6.6 / 5.8, (20, 4, 1, 512, 2048) 8.0 / 6.9
 ExpertTile narrow_tile(const ExpertArgs& a) {
   const int experts = std::min(a.E, a.T * a.topk);   // that may have rows
   const int up = experts * (a.I / 16) < 200 ? 8 : 16;
