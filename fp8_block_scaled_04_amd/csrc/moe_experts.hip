@@ -3,8 +3,8 @@
 //   k_moe_up    per expert, g and u = w13 x, then the weighted activations
 //               weight g / (1 + exp(-g)) u, as two BF16 parts
 //   k_moe_down  w2 times them
-//   k_moe_join  the sums of each token's rows (few weights: k_moe_down_whole takes
-//               its place and that of k_moe_down)
+//   k_moe_join  the sums of each token's rows (not with one place per token; few
+//               weights: k_moe_down_whole takes its place and that of k_moe_down)
 //
 // Bound by HBM: every expert that has a token is read once, 3 H I codes for at
 // most a few dozen rows of products.  So weights go from memory straight to the
@@ -206,6 +206,21 @@ __device__ __forceinline__ void put_out(const ExpertArgs& a, int t, int h, v4f v
   else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
 }
 
+// A row of the second product, columns h .. h + 3: the result itself where a token
+// has one place, else a part of it for k_moe_join.
+__device__ __forceinline__ void put_row(const ExpertArgs& a, int place, int h, v4f v) {
+  if (a.topk == 1) put_out(a, place, h, v);
+  else *reinterpret_cast<v4f*>(a.part + (int64_t)place * a.H + h) = v;
+}
+// With one place per token: zeros for the tokens without an expert.
+__device__ __forceinline__ void put_zeros(const ExpertArgs& a) {
+  if (a.topk != 1) return;
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    if ((uint32_t)a.ids[t] < (uint32_t)a.E) continue;
+    for (int h = threadIdx.x * 4; h < a.H; h += kThreads * 4) put_out(a, t, h, v4f{0.0f, 0.0f, 0.0f, 0.0f});
+  }
+}
+
 // The waves' accumulators of NC fragments, in LDS (kWaves * NC * 256 floats) for
 // the sums over them.
 template <int NC>
@@ -384,6 +399,7 @@ __global__ __launch_bounds__(kThreads, 3) void k_moe_down(ExpertArgs a) {
   const int tiles = a.H / COLS, items = plan.jobs * tiles, stride = gridDim.x * (kWaves / KS);
   const int64_t panel = (int64_t)a.H * a.I, acts = (int64_t)a.T * a.topk * a.I * 2;
   const auto hb = buffer(a.hi, acts), lb = buffer(a.lo, acts);
+  put_zeros(a);
 
   // (the first item of every workgroup before the second of any)
   int item = wave_id() / KS * gridDim.x + blockIdx.x, ahead = item, step = 0;
@@ -440,19 +456,21 @@ __global__ __launch_bounds__(kThreads, 3) void k_moe_down(ExpertArgs a) {
   for (int n = 0; n < NC; ++n) acc[n] = zero;
   auto finish = [&]() {
     const Job job = plan.at(item / tiles);
-    float* out = a.part + item % tiles * COLS;
+    const int col0 = item % tiles * COLS;
     if (KS == 1) {
       if (fr >= job.n) return;                       // a lane has four columns of a row
-      const int64_t place = plan.row[job.start + fr] & 0xFFFF;
+      const int place = plan.row[job.start + fr] & 0xFFFF;
 #pragma unroll
-      for (int n = 0; n < NC; ++n) *reinterpret_cast<v4f*>(out + place * a.H + n * 16 + fg * 4) = acc[n];
+      for (int n = 0; n < NC; ++n) put_row(a, place, col0 + n * 16 + fg * 4, acc[n]);
     } else {
       leave(acc, red);
-      for (int i = threadIdx.x; i < 16 * COLS; i += kThreads) {
-        const int m = i / COLS, c = i % COLS;
-        if (m >= job.n) break;
-        const int64_t place = plan.row[job.start + m] & 0xFFFF;
-        out[place * a.H + c] = total<NC>(red, c / 16, m, c % 16);
+      const int m = threadIdx.x % 16, g = threadIdx.x / 16;
+      if (m < job.n && g < COLS / 4) {
+        const v4f* from = reinterpret_cast<const v4f*>(red) + threadIdx.x;   // fragment g / 4, its columns g % 4 * 4 ...
+        v4f v = from[0];
+#pragma unroll
+        for (int w = 1; w < KS; ++w) v += from[w * NC * 64];
+        put_row(a, plan.row[job.start + m] & 0xFFFF, col0 + g * 4, v);
       }
       __syncthreads();
     }
@@ -862,9 +880,9 @@ __device__ __forceinline__ void down_wide(const ExpertArgs& a, const Plan& plan,
   for (int f = 0; f < MF; ++f) {
     const int r = f * 16 + fr;
     if (r >= job.n || col >= a.H) continue;
-    float* to = a.part + (int64_t)(plan.row[job.start + r] & 0xFFFF) * a.H + col + fg * 4;
+    const int place = plan.row[job.start + r] & 0xFFFF;
 #pragma unroll
-    for (int n = 0; n < NC; ++n) *reinterpret_cast<v4f*>(to + n * 16) = acc[f][n];
+    for (int n = 0; n < NC; ++n) put_row(a, place, col + n * 16 + fg * 4, acc[f][n]);
   }
 }
 
@@ -874,6 +892,7 @@ constexpr int kDownStage = 2 * 2 * 64 * 256;   // bytes, for 64 rows
 __global__ __launch_bounds__(kThreads, 2) void k_moe_down_wide(ExpertArgs a) {
   extern __shared__ __align__(16) uint32_t lds[];
   const Plan plan = load_plan(a, lds + kDownStage / 4);
+  put_zeros(a);
   const int tiles = (a.H + 255) / 256, units = plan.jobs * tiles;
   const Share share = share_of(blockIdx.x, units);
   if (share.unit >= units) return;
@@ -940,7 +959,7 @@ int64_t experts_workspace(ExpertArgs& a, void* base) {
   };
   a.hi = reinterpret_cast<uint16_t*>(take(places * a.I * 2));
   a.lo = reinterpret_cast<uint16_t*>(take(places * a.I * 2));
-  a.part = reinterpret_cast<float*>(take(places * a.H * 4));
+  a.part = reinterpret_cast<float*>(take(a.topk == 1 ? 0 : places * a.H * 4));
   a.image = reinterpret_cast<uint32_t*>(take(image_words(a) * 4));
   return at;
 }
@@ -1038,6 +1057,9 @@ hipError_t launch_moe_experts(const ExpertArgs& a, hipStream_t stream) {
     else if (t.down == 32) launch_down<32, 4>(a, stream);
     else launch_down<16, 4>(a, stream);
   }
+  // one place per token: nothing to add up, 3 us of a call (64 tokens, 16 experts of
+  // 7168 x 2048: 139 -> 135 us; 32 tokens, 8 of 1024 x 512: 19 -> 16.5)
+  if (a.topk == 1) return hipGetLastError();
   k_moe_join<<<dim3((unsigned)((a.H / 4 + kThreads - 1) / kThreads), (unsigned)a.T), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }

@@ -145,6 +145,27 @@ def test_experts_exactly_on_every_kernel(tile, T, H, I, E, topk):
     check_exact(exact_case(T, H, I, E, topk, seed=T + H + I))
 
 
+# One place per token, a fifth of them outside: no sum over places is left.  On every kernel of the second product.
+@pytest.mark.parametrize("tile,T,H,I,E", [
+    ((16, 8, 16, 8), 16, 128, 128, 3), ((16, 16, 16, 4), 16, 128, 2304, 3), ((16, 8, 32, 1), 17, 2048, 256, 9),
+    ((16, 16, 32, 4), 40, 256, 1152, 40), ((16, 16, 64, 4), 50, 1024, 640, 40), ((16, 16, 64, 1), 60, 4096, 128, 100),
+    ((64, 128, 256, 4), 128, 384, 1024, 8), ((64, 128, 256, 4), 128, 4096, 512, 2)])
+def test_experts_of_one_place(tile, T, H, I, E):
+    assert fb.moe_experts_tile(T, H, I, E, 1) == tile
+    rng = np.random.default_rng(T + E)
+    ids = np.where(rng.random((T, 1)) < 0.2, rng.choice([-1, E, -(1 << 31), 1 << 30], (T, 1)), rng.integers(0, E, (T, 1)))
+    ids[-1] = -1
+    w = exact_case(T, H, I, E, 1, seed=T + H + I, ids=ids)
+    more = torch.full((T + 1, H), float("nan"), device=DEV)
+    check_exact(w, out=more[:T])
+    assert more[T].isnan().all()
+    half = torch.full((T + 1, H), float("nan"), dtype=torch.bfloat16, device=DEV)
+    fb.moe_experts(*expert_dev(w), out=half[:T])
+    assert torch.equal(half[:T], more[:T].to(torch.bfloat16)) and half[T].isnan().all()
+    w["ids"][:] = E
+    assert (fb.moe_experts(*expert_dev(w), out=half[:T]) == 0).all()
+
+
 @pytest.mark.parametrize("T,H,I,E,topk", [(5, 256, 384, 4, 1), (16, 256, 384, 16, 1), (40, 256, 384, 4, 1), (64, 256, 640, 16, 2)])
 @pytest.mark.parametrize("where", ["w2", "s2", "w13"])
 def test_experts_of_others_do_not_matter(T, H, I, E, topk, where):
