@@ -3,13 +3,13 @@
 //
 // Bound by instructions: each choice is a maximum over a token's logits, and one
 // wave instruction takes four cycles.  So 16 lanes hold a token where they can
-// (up to 256 experts and 16 places): lane l has experts 16 n + l, four tokens share
-// each instruction, and a maximum over 16 lanes is four DPP steps.  Otherwise a
+// (up to 256 experts and 16 places): each lane has a 16th of the experts, four tokens
+// share each instruction, and a maximum over 16 lanes is four DPP steps.  Otherwise a
 // wave holds one token, expert 64 n + lane at v[n] of a lane.
 //
-// 16384 tokens, 256 experts, 8 places: 10.4 us (BF16 logits, 9 MB), with one token
-// per wave 14.7; the gradient 8.1 us (FP32, 18 MB), with one token per wave 12.6.
-// 64 tokens: 5.1 us, all of it latency.
+// 16384 tokens, 256 experts, 8 places: 7.5 us (BF16 logits, 9 MB), the gradient 7.3
+// (FP32, 18 MB); 64 tokens 3.8 us, all of it latency.  (One token per wave against 16
+// lanes, logits read one by one: 14.7 and 10.4 us, the gradient 12.6 and 8.1.)
 #include <algorithm>
 #include <type_traits>
 
@@ -253,26 +253,84 @@ __device__ __forceinline__ void sort_falling(double (&k)[N]) {
       }
 }
 
+// Rows are read and written in pieces of P values, up to 16 bytes (piece_of below): a
+// lane has every 16th piece, so that a wave's access is whole lines.  16384 tokens,
+// 256 experts, in us, single values -> pieces: BF16 9.9 -> 7.5, its gradient (softmax
+// over all) 13.0 -> 10.1; FP32 8.8 -> 8.2, its gradient (over the chosen) 7.5 -> 7.3, but
+// 10.6 with a lane's values one after the other.
+template <int P>
+__device__ __forceinline__ int expert_at(int n, int l) {
+  return n / P * (16 * P) + l * P + n % P;
+}
+
+// Lane l's logits of token t; -inf where there is none.
+template <int N, int P>
+__device__ __forceinline__ void read_row(float (&x)[N], const RouteArgs& a, int64_t t, int l) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) x[n] = -__builtin_inff();
+  if (t >= a.T) return;
+#pragma unroll
+  for (int n = 0; n < N; n += P) {
+    const int e = expert_at<P>(n, l);
+    if (e >= a.E) break;
+    const int64_t at = t * a.E + e;
+    if constexpr (P == 1) {
+      x[n] = logit(a, at);
+    } else {
+      typedef uint32_t Piece __attribute__((ext_vector_type(P / 2)));
+      if (P == 4 && a.logits_f32) {
+        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + at);
+        x[n] = v.x, x[n + 1] = v.y, x[n + 2] = v.z, x[n + 3] = v.w;
+      } else {
+        const Piece v = *reinterpret_cast<const Piece*>(static_cast<const uint16_t*>(a.logits) + at);
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i) x[n + 2 * i] = bf16_lo(v[i]), x[n + 2 * i + 1] = bf16_hi(v[i]);
+      }
+    }
+  }
+}
+
+// And its gradients.
+template <int N, int P>
+__device__ __forceinline__ void write_row(const float (&x)[N], const RouteArgs& a, int64_t t, int l) {
+  if (t >= a.T) return;
+#pragma unroll
+  for (int n = 0; n < N; n += P) {
+    const int e = expert_at<P>(n, l);
+    if (e >= a.E) break;
+    const int64_t at = t * a.E + e;
+    if constexpr (P == 1) {
+      put(a, at, x[n]);
+    } else {
+      typedef uint32_t Piece __attribute__((ext_vector_type(P / 2)));
+      if (P == 4 && a.logits_f32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(a.dlogits) + at) = make_float4(x[n], x[n + 1], x[n + 2], x[n + 3]);
+      } else {
+        Piece v;
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i) v[i] = pack2_bf16(x[n + 2 * i], x[n + 2 * i + 1]);
+        *reinterpret_cast<Piece*>(static_cast<uint16_t*>(a.dlogits) + at) = v;
+      }
+    }
+  }
+}
+
 // Each lane sorts its own N logits and keeps them in LDS; a choice is then the
 // largest of the 16 lists' heads, and one list moves on.
-template <int N>
+template <int N, int P>
 __global__ __launch_bounds__(64 * kWaves) void k_route_rows(RouteArgs a) {
   __shared__ double lists[N + 1][64 * kWaves];
   const int l = threadIdx.x % 16, tid = threadIdx.x;
   const int64_t step = (int64_t)gridDim.x * kTokens;
   float x[N];
-  auto fetch = [&](int64_t t) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) x[n] = t < a.T && 16 * n + l < a.E ? logit(a, t * a.E + 16 * n + l) : -__builtin_inff();
-  };
   lists[N][tid] = 0.0;                               // (each lane reads and writes its own column only)
   // (the four rows of a wave go on together, so that their DPP steps see live lanes)
   int64_t t = (int64_t)blockIdx.x * kTokens + tid / 16;
-  fetch(t);
+  read_row<N, P>(x, a, t, l);
   for (int64_t first = (int64_t)blockIdx.x * kTokens; first < a.T; first += step, t += step) {
     double k[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) k[n] = key_of(rank_of(x[n]), 16 * n + l);
+    for (int n = 0; n < N; ++n) k[n] = key_of(rank_of(x[n]), expert_at<P>(n, l));
     float sum = 0.0f, top = 0.0f;
     if (!a.renorm) {
       double best = k[0];
@@ -283,7 +341,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_rows(RouteArgs a) {
 #pragma unroll
       for (int n = 0; n < N; ++n) sum += weight_of(x[n], top);
     }
-    fetch(t + step);
+    read_row<N, P>(x, a, t + step, l);
     sort_falling(k);
 #pragma unroll
     for (int n = 0; n < N; ++n) lists[n][tid] = k[n];
@@ -306,7 +364,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_rows(RouteArgs a) {
   }
 }
 
-template <int N>
+template <int N, int P>
 __global__ __launch_bounds__(64 * kWaves) void k_route_back_rows(RouteArgs a) {
   const int l = threadIdx.x % 16;
   const int64_t step = (int64_t)gridDim.x * kTokens;
@@ -327,9 +385,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_back_rows(RouteArgs a) {
       for (int n = 0; n < N; ++n) p[n] = 0.0f;
     } else {
       float top = -__builtin_inff(), sum = 0.0f;
+      read_row<N, P>(p, a, t, l);
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        p[n] = live && 16 * n + l < a.E ? logit(a, t * a.E + 16 * n + l) : -__builtin_inff();
         if (!(p[n] > -__builtin_inff())) p[n] = -__builtin_inff();
         top = fmaxf(top, p[n]);
       }
@@ -355,8 +413,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_back_rows(RouteArgs a) {
     }
     if (!a.renorm) total -= place * mean;
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      if (live && 16 * n + l < a.E) put(a, t * a.E + 16 * n + l, -(p[n] * mean));
+    for (int n = 0; n < N; ++n) p[n] = -(p[n] * mean);
+    write_row<N, P>(p, a, t, l);
     // the places' own experts, over what other lanes of this wave have just
     // written there (a wave's stores to one address stay in order)
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -369,13 +427,34 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_back_rows(RouteArgs a) {
 unsigned grid_of(int64_t T, int tokens) { return (unsigned)std::min<int64_t>((T + tokens - 1) / tokens, 2048); }
 
 bool by_rows(const RouteArgs& a) { return a.E <= 256 && a.topk <= 16; }
+// Values of a piece: as many as 16 bytes and a lane hold, of rows that are whole pieces
+// (arrays start at multiples of 16 bytes).
+int piece_of(const RouteArgs& a) {
+  if (!a.logits_f32 && a.E > 64 && a.E % 8 == 0) return 8;
+  return a.E % 4 == 0 ? 4 : 1;
+}
+// f(N, P), both known when compiled.
+template <class F>
+void with_shape(const RouteArgs& a, F f) {
+  const auto with_piece = [&](auto n) {
+    const int p = piece_of(a);
+    if constexpr (decltype(n)::value > 4)
+      if (p == 8) return f(n, std::integral_constant<int, 8>());
+    if (p == 4) return f(n, std::integral_constant<int, 4>());
+    return f(n, std::integral_constant<int, 1>());
+  };
+  if (a.E <= 64) return with_piece(std::integral_constant<int, 4>());
+  if (a.E <= 128) return with_piece(std::integral_constant<int, 8>());
+  return with_piece(std::integral_constant<int, 16>());
+}
 
 }  // namespace
 
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream) {
   if (by_rows(a)) {
-    const auto k = a.E <= 64 ? k_route_rows<4> : a.E <= 128 ? k_route_rows<8> : k_route_rows<16>;
-    k<<<grid_of(a.T, kTokens), 64 * kWaves, 0, stream>>>(a);
+    with_shape(a, [&](auto n, auto p) {
+      k_route_rows<decltype(n)::value, decltype(p)::value><<<grid_of(a.T, kTokens), 64 * kWaves, 0, stream>>>(a);
+    });
   } else {
     const auto k = a.E <= 256 ? k_route<4> : k_route<16>;
     k<<<grid_of(a.T, kWaves), 64 * kWaves, 0, stream>>>(a);
@@ -385,8 +464,9 @@ hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream) {
 
 hipError_t launch_moe_route_back(const RouteArgs& a, hipStream_t stream) {
   if (by_rows(a)) {
-    const auto k = a.E <= 64 ? k_route_back_rows<4> : a.E <= 128 ? k_route_back_rows<8> : k_route_back_rows<16>;
-    k<<<grid_of(a.T, kTokens), 64 * kWaves, 0, stream>>>(a);
+    with_shape(a, [&](auto n, auto p) {
+      k_route_back_rows<decltype(n)::value, decltype(p)::value><<<grid_of(a.T, kTokens), 64 * kWaves, 0, stream>>>(a);
+    });
   } else {
     const auto k = a.E <= 256 ? k_route_back<4> : k_route_back<16>;
     k<<<grid_of(a.T, kWaves), 64 * kWaves, 0, stream>>>(a);

@@ -80,6 +80,17 @@ def test_route(t, e, topk, kind, renorm):
     check(x, dev, topk, renorm)
 
 
+# Rows that are whole pieces of 4 and 8 logits and rows that are not, for each number of experts per lane; a last piece
+# in the middle of the lanes.
+@pytest.mark.parametrize("t,e,topk", [(5, 4, 4), (17, 12, 3), (2, 62, 7), (19, 72, 5), (4, 76, 16), (6, 127, 8), (21, 131, 8),
+                                      (7, 132, 2), (16, 136, 16), (3, 252, 10), (15, 248, 8), (9, 254, 1), (40000, 8, 2)])
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_of_whole_and_broken_pieces(t, e, topk, kind, renorm):
+    x, dev = make(np.random.default_rng(t * 1000 + e), t, e, kind)
+    check(x, dev, topk, renorm)
+
+
 @pytest.mark.parametrize("renorm", [False, True])
 def test_route_ties_and_signed_zeros(renorm):
     rng = np.random.default_rng(1)
