@@ -111,14 +111,16 @@ __device__ __forceinline__ float quot(float x, const TileScale& t) {
 // E4M3 encode (hardware OCP-FP8 conversion, round to nearest even), four
 // values into one dword, byte i = value i.
 //
-// pack4_e4m3 is for the quantizers, whose values satisfy |y| <= 448 * (1 +
-// 2^-22) < 464 (x / s with s = RN(amax / 448) exceeds 448 only when the
-// scale rounded down): round to nearest even maps everything in [448, 464)
-// to 448, so no clamp is needed (every BF16 amax, about half of them with a
-// scale that rounded down, is checked bit-exact in
-// tests/test_gpu_exhaustive.py).  pack4_e4m3_sat clamps to +-448 first
-// (satfinite) for arbitrary inputs; the cast is compared with the oracle on
-// all 2^32 FP32 bit patterns there.
+// pack4_e4m3 is for values x / s with |x| up to the largest BF16 amax of their
+// tile.  s = RN(amax / 448) is off by at most half a step, 2^-24 of a normal s; a
+// subnormal s has n >= 146 steps of 2^-149 (amax >= 2^-133) and is off by at most
+// 1 / (2 n).  So |x / s| < 450, round to nearest even maps everything in
+// [448, 464) to 448, and no clamp is needed (every BF16 amax, about half of them
+// with a scale that rounded down, is checked bit-exact in
+// tests/test_gpu_exhaustive.py).  Below 2^-136, where FP32 values can lie and BF16
+// ones cannot, n <= 14 leaves quotients past 464, for which the conversion gives
+// NaN: pack4_e4m3_sat clamps to +-448 first (satfinite) for arbitrary inputs; the
+// cast is compared with the oracle on all 2^32 FP32 bit patterns there.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float clamp448(float y) {
   return __builtin_fminf(__builtin_fmaxf(y, -kE4M3Max), kE4M3Max);
