@@ -40,7 +40,8 @@ enum { FP8BS_ROUTE_RENORM = 4u };
  *   q, s        : E4M3 [M][K], FP32 [K/128][M]
  *   rstd        : FP32 [M], or NULL
  *   flags       : 0 or FP8BS_SCALE_POW2
- * The sum of squares is FP32: it has to stay below 2^128.  Inputs must be finite.
+ * The sum of squares and y are FP32: they have to stay below 2^128 in size, and
+ * h weight below 2^144.  Inputs must be finite.
  * Requires 0 <= M < 2^31, 0 < K <= 16384, K % 128 == 0, eps >= 2^-126 and
  * finite; residual and h both given or both NULL (else FP8BS_ERR_NULL).
  */

@@ -8,6 +8,8 @@ import torch
 import fp8_block_scaled_04_amd as fb
 from oracle import bf16, quantize
 from tests.gpu_util import bf16_dev, codes_host, f32_bits_host, f32_dev, require_gpu
+from tests.layer_util import rows_bits, weight_of
+from tests.test_gpu_norm import check
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +52,29 @@ def test_norm_of_a_small_tile_among_ones(pow2):
     y = (x * w * rstd.cpu().numpy().astype(np.float64)[:, None]).astype(np.float32)
     q_ref, s_ref = quantize.quantize_rows_f32(y, pow2)
     assert np.array_equal(f32_bits_host(s), s_ref.view(np.uint32)) and np.array_equal(codes_host(q), q_ref)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("h,weight", [(-80, -80), (-70, -64), (34, 100), (55, 73), (-100, 40), (-100, -24), (0, 0)])
+def test_norm_of_products_past_the_normal_range(h, weight, kind):
+    # h weight below 2^-126 or past 2^128 (below 2^144) where y is neither: the bounds of test_gpu_norm.py hold as
+    # anywhere
+    rng = np.random.default_rng(200 + h)
+    w, raw = weight_of(rng, 768, kind)
+    w = w * 2.0 ** weight
+    dev = f32_dev(w) if kind == "fp32" else bf16_dev(bf16.from_f64_rne(w))
+    check(rows_bits(rng, 7, 768, 2.0 ** h), None, w, dev, 2.0 ** -126)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_norm_of_rows_with_both_ends(kind):
+    # one row: large h with ordinary weights, tiny h with very large ones, zeros of either
+    rng = np.random.default_rng(77)
+    w, raw = weight_of(rng, 1024, kind)
+    size = np.exp2(np.repeat([0, 100, 110, -100, -10, 0, 80, 0], 128).astype(np.float64))
+    x = rng.standard_normal((5, 1024)) * np.exp2(np.repeat([55, -100, -118, 50, -40, 0, 55, 55], 128).astype(np.float64))
+    x[:, 640:704] = 0
+    w = w * size
+    w[700:768] = 0
+    dev = f32_dev(w) if kind == "fp32" else bf16_dev(bf16.from_f64_rne(w))
+    check(bf16.from_f64_rne(x), None, w, dev, 1e-6)
