@@ -198,7 +198,9 @@ __global__ __launch_bounds__(256) void k_quantize_1x128(const uint16_t* __restri
 // Sixteen values of one tile -> sixteen codes (byte i = value i).  SCALED:
 // the tile is one of those with amax < 2^-60, evaluated on x * 2^64.  The
 // callers branch on a wave-uniform flag, so the common case carries no
-// per-element multiply or select.
+// per-element multiply or select.  Values that were dequantized can lie below
+// BF16's range, where a scale of a few steps of 2^-149 leaves quotients past
+// 464: such tiles are SCALED ones, and saturate.
 template <bool POW2, bool SCALED>
 __device__ __forceinline__ uint4 quantize16(const float (&x)[16], const TileScale& t) {
   uint32_t packed[4];
@@ -207,7 +209,7 @@ __device__ __forceinline__ uint4 quantize16(const float (&x)[16], const TileScal
     float y[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = quot<POW2>(SCALED ? x[4 * k + e] * t.sx : x[4 * k + e], t);
-    packed[k] = pack4_e4m3(y[0], y[1], y[2], y[3]);
+    packed[k] = SCALED ? pack4_e4m3_sat(y[0], y[1], y[2], y[3]) : pack4_e4m3(y[0], y[1], y[2], y[3]);
   }
   return make_uint4(packed[0], packed[1], packed[2], packed[3]);
 }
