@@ -26,11 +26,15 @@ _PUBLIC = (
 )
 
 __all__ = list(_PUBLIC)
+_NAMES = frozenset(_PUBLIC)
 
 
 def __getattr__(name):
-    if name in _PUBLIC:
-        from . import fp8bs
-        value = globals()[name] = getattr(fp8bs, name)   # (later lookups find it at once)
-        return value
+    if name in _NAMES:
+        # looked up each time: what stands in the binding now.  (The import statement costs
+        # over 1 us, once it has set this global.)
+        binding = globals().get("fp8bs")
+        if binding is None:
+            from . import fp8bs as binding
+        return getattr(binding, name)
     raise AttributeError(name)
