@@ -117,8 +117,9 @@ fp8bs_status fp8bs_moe_route_backward(const void* logits, int32_t logits_type, c
  *               that share it must not overlap in time
  * The first product promotes FP8 chunk products as the GEMMs do.  The weighted
  * activations are held as two BF16 parts (2^-17 of a value is lost) and meet the
- * codes of w2, which BF16 holds exactly (parts below 2^-126 may count as 0; the
- * weighted activations have to stay below 2^127); sums are FP32, in a fixed order.
+ * codes of w2, which BF16 holds exactly (parts below 2^-126 may count as 0); sums
+ * are FP32, in a fixed order.  A chunk's products are added before their scale: the
+ * weighted activations have to stay below 2^112 (2^112 * 448 * 128 < 2^128).
  * Requires 0 <= T <= 128 (more tokens: the grouped GEMMs), 0 < topk <= 16,
  * 0 < E <= 1024, H and I multiples of 128 from 128 to 32768 with 2 H I < 2^31.
  */
