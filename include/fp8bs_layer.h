@@ -61,7 +61,8 @@ fp8bs_status fp8bs_rms_norm_quantize(const void* x, const void* residual, const 
  *            (with 0 where M is 0)
  *   workspace : fp8bs_rms_norm_backward_workspace bytes (NULL if 0), contents
  *               overwritten; calls that share it must not overlap in time
- * Sums are FP32 and in a fixed order: the same inputs give the same bits.
+ * n, g and the sums are FP32: they have to stay below 2^128 in size, and keep fewer
+ * bits below 2^-126.  The order is fixed: the same inputs give the same bits.
  * Requires M and K as above, accumulate in {0, 1} (else FP8BS_ERR_FLAGS).
  */
 fp8bs_status fp8bs_rms_norm_backward(const void* dy, const void* h, const float* rstd, const void* weight,
