@@ -613,7 +613,10 @@ __device__ __forceinline__ int swizzle16(int row, int s) { return s ^ (row & 15)
 // Work of one workgroup: a job and a unit of columns, or half of one.  Whole units
 // read a job's rows half as often, halves leave less undone at the end: so as many
 // whole units as fill the chip in rounds of two workgroups per CU come first, and
-// the rest in halves (64 tokens of 32 experts of 7168 x 2048: 287 -> 279 us).
+// the rest in halves (64 tokens of 32 experts of 7168 x 2048: 287 -> 279 us).  Two fit
+// up to about 850 places; with more of them the plan's LDS leaves one per CU: 128 tokens
+// of 8 of 32 experts of 7168 x 2048 take 424 us, 64 tokens of 16 of 32 take 460, where
+// the weights alone are 248 at the read's rate.
 struct Share {
   int unit, half;   // half: 0, 1, or -1 for both
 };
@@ -1024,7 +1027,10 @@ ExpertTile narrow_tile(const ExpertArgs& a) {
 // 1536) 61 / 77, (32, 8, 8, 2048, 512) 26 / 24, (36, 4, 3, 2816, 256) 26 / 15.  With
 // 64 rows and more the narrow kernels read an expert four times and more: (128, 2, 2,
 // 7168, 2048) 82 / 169, (128, 1, 1, 7168, 2048) 76 / 98, (128, 2, 2, 4096, 512) 41 / 43,
-// but (100, 1, 1, 512, 2048) 39 / 21.
+// but (100, 1, 1, 512, 2048) 39 / 21.  One rule for both products, which sees neither the
+// second one's units nor whether ids are outside [0, E) (places without rows count):
+// few units leave most of the chip idle, (20, 4, 2, 512, 2048) 27 us, of 2.2 at the
+// read's rate.
 bool wide(const ExpertArgs& a) {
   const int experts = std::min(a.E, a.T * a.topk);
   const int places = a.T * a.topk;

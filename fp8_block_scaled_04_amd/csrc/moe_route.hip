@@ -10,6 +10,9 @@
 // 16384 tokens, 256 experts, 8 places: 7.5 us (BF16 logits, 9 MB), the gradient 7.3
 // (FP32, 18 MB); 64 tokens 3.8 us, all of it latency.  (One token per wave against 16
 // lanes, logits read one by one: 14.7 and 10.4 us, the gradient 12.6 and 8.1.)
+// 16384 tokens of 384, 512 and 1024 experts, BF16, one token per wave: 39, 40 and 50 us,
+// the gradient (over the chosen) 22, 23 and 24; by bytes 2, 3 and 6 each.  All three have
+// 16 logits per lane, however many of them there are.
 #include <algorithm>
 #include <type_traits>
 
@@ -235,8 +238,8 @@ __device__ __forceinline__ double row_max(double v) {
   return step(v, std::integral_constant<int, 0x140>());
 }
 
-// Falling order, by odd-even merging (N a power of two; all indexes are known when
-// compiled).
+// Falling order, by Batcher's odd-even merge sort (N a power of two; all indexes are
+// known when compiled).
 template <int N>
 __device__ __forceinline__ void sort_falling(double (&k)[N]) {
 #pragma unroll

@@ -7,8 +7,12 @@
 // codes (rounded to BF16 first, a code would be off by up to 2^-8 of the value more).
 //
 // HBM-bound.  8192 x 7168 with a residual: forward 70 us, 413 MB at 5.9 TB/s;
-// backward 80 + 5 us (the sums over rows), 470 MB at 5.5 TB/s; a plain copy moves
-// 4.9 TB/s.  The forward pass keeps the vector unit busy 61 % of the time.
+// backward 80 + 5 us (the sums over rows), 470 MB at 5.5 TB/s.  A plain copy of 2 GiB
+// moves 4.9 TB/s; of these sizes a part is still in the last-level cache when the next
+// call reads it, and nontemporal streams of 0.1 to 0.2 GB reach 6.1.  The forward pass
+// keeps the vector unit busy 63 % of the time.  Narrow rows, forward, calls in a replayed
+// graph: 8192 rows of 512, 1024 and 2048 take 8.5, 14.2 and 23.7 us (6.0, 12.0 and 23.9
+// at the copy's rate), one or two waves per workgroup.
 #include <algorithm>
 
 #include "layer.h"
