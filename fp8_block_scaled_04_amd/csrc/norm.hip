@@ -12,7 +12,7 @@
 // call reads it, and nontemporal streams of 0.1 to 0.2 GB reach 6.1.  The forward pass
 // keeps the vector unit busy 63 % of the time.  Narrow rows, forward, calls in a replayed
 // graph: 8192 rows of 512, 1024 and 2048 take 8.5, 14.2 and 23.7 us (6.0, 12.0 and 23.9
-// at the copy's rate), one or two waves per workgroup.
+// at the copy's rate), one, two and four waves per workgroup.
 #include <algorithm>
 
 #include "layer.h"
