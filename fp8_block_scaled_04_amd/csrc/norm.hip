@@ -125,7 +125,8 @@ __global__ __launch_bounds__(1024) void k_rms_norm(NormArgs a) {
     // weight may leave FP32's normal range on its way to a y inside it.  (Choosing by the
     // weights' size where rstd < 2^-16, too: 8192 x 7168 73 us against 69.)
     const uint32_t power = max(bits & 0x7F800000u, 0x37800000u);
-    const float up = __builtin_bit_cast(float, power), rest = __builtin_bit_cast(float, bits - power + 0x3F800000u);
+    const float up = __builtin_bit_cast(float, power);
+    const float rest = rstd * __builtin_bit_cast(float, 0x7F000000u - power);   // (1 / up: 0 and NaN stay what they are)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = v * threads + tid;

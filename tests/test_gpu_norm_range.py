@@ -78,3 +78,24 @@ def test_norm_of_rows_with_both_ends(kind):
     w[700:768] = 0
     dev = f32_dev(w) if kind == "fp32" else bf16_dev(bf16.from_f64_rne(w))
     check(bf16.from_f64_rne(x), None, w, dev, 1e-6)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_norm_of_rows_out_of_range_leaves_the_others(kind):
+    # NaN, infinities and sums of squares past 2^128 in rows of their own; the sum of squares gives rstd 0 and codes of 0
+    rng = np.random.default_rng(21)
+    w, raw = weight_of(rng, 1152, kind)
+    dev = f32_dev(raw) if kind == "fp32" else bf16_dev(raw)
+    x = rng.standard_normal((40, 1152))
+    clean = fb.rms_norm_quantize(bf16_dev(bf16.from_f64_rne(x)), dev, return_y=True)
+    bad = x.copy()
+    bad[3, 700] = np.nan
+    bad[17, 0], bad[18, 1151] = np.inf, -np.inf
+    bad[30] = 2.0 ** 70
+    got = fb.rms_norm_quantize(bf16_dev(bf16.from_f64_rne(bad)), dev, return_y=True)
+    rest = [m for m in range(40) if m not in (3, 17, 18, 30)]
+    for a, b in zip(clean, got):
+        pick = (lambda t: t[:, rest]) if a.shape == (9, 40) else (lambda t: t[rest])
+        assert torch.equal(pick(a.view(torch.uint8) if a.element_size() == 1 else a), pick(b.view(torch.uint8) if b.element_size() == 1 else b))
+    assert got[3][30] == 0 and (codes_host(got[0])[30] & 0x7F == 0).all() and (got[4][30] == 0).all()
+    assert got[3][3].isnan() and got[4][3].isnan().all()
